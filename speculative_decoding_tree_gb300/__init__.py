@@ -2,8 +2,10 @@
 
 A thin ctypes binding over libtreeverify.so, whose C ABI is declared in
 include/tree_verify.h (the verify step), include/tree_expand.h (dynamic
-draft-tree expansion), include/tree_lm_head.h (fused lm_head + argmax) and
-include/tree_rope.h (tree-position RoPE and the K/V scatter).  Every function here only marshals arguments (torch
+draft-tree expansion), include/tree_lm_head.h (fused lm_head + argmax),
+include/tree_rope.h (tree-position RoPE and the K/V scatter),
+include/tree_window.h (attention over a sliding window with sinks) and
+include/tree_kv4.h (a KV cache held in 4 bits).  Every function here only marshals arguments (torch
 tensors or raw device addresses, a stream) and raises on a non-zero status;
 all work happens in the library's CUDA kernels.  There is no CPU fallback:
 calling into a library that was not built raises ``LibraryNotBuilt``.
@@ -20,6 +22,9 @@ __all__ = [
     "tree_accept_commit_sampled", "TvExpandDesc", "make_expand_desc", "tv_expand_workspace_size",
     "tv_expand_steps", "tv_tree_expand_step", "TvLmHeadDesc", "make_lmhead_desc", "tv_lm_head_workspace_size",
     "tv_lm_head_argmax", "tv_tree_rope_scatter", "tree_accept_commit_argmax", "tv_check_bounded_wait",
+    "TvWindow", "make_window", "tv_window_workspace_size", "tv_window_attn_plan", "tree_verify_attn_window",
+    "tv_kv4_cache_bytes", "tv_kv4_append", "tv_kv4_read", "tree_accept_commit_argmax_kv4", "tv_kv4_workspace_size",
+    "tv_kv4_attn_plan", "tree_verify_attn_kv4",
 ]
 
 F32, BF16 = 0, 1
@@ -62,6 +67,10 @@ class TvLmHeadDesc(ctypes.Structure):
     _fields_ = [(n, ctypes.c_int32) for n in ("rows", "hidden", "vocab")]
 
 
+class TvWindow(ctypes.Structure):
+    _fields_ = [("window", ctypes.c_int64), ("sinks", ctypes.c_int64)]
+
+
 _LIB = None
 _P = ctypes.c_void_p
 _I = ctypes.c_int32
@@ -84,6 +93,18 @@ _SIG = {
     "tv_tree_rope_scatter": [ctypes.POINTER(TvDesc), ctypes.c_double] + [_P] * 11,
     "tree_accept_commit_argmax": [ctypes.POINTER(TvDesc)] + [_P] * 15,
     "tv_check_bounded_wait": [ctypes.c_int64, _P, _P],
+    "tv_window_workspace_size": [ctypes.POINTER(TvDesc), ctypes.POINTER(TvWindow), ctypes.POINTER(ctypes.c_size_t)],
+    "tv_window_attn_plan": [ctypes.POINTER(TvDesc), ctypes.POINTER(TvWindow), ctypes.POINTER(TvPlan)],
+    "tree_verify_attn_window": [ctypes.POINTER(TvDesc), ctypes.POINTER(TvWindow)] + [_P] * 12
+                               + [ctypes.c_size_t, _P, _P],
+    "tv_kv4_cache_bytes": [ctypes.POINTER(TvDesc), ctypes.POINTER(ctypes.c_int64), ctypes.POINTER(ctypes.c_int64)],
+    "tv_kv4_append": [ctypes.POINTER(TvDesc), ctypes.c_int64, ctypes.c_int64] + [_P] * 9,
+    "tv_kv4_read": [ctypes.POINTER(TvDesc), ctypes.c_int64, ctypes.c_int64] + [_P] * 9,
+    "tree_accept_commit_argmax_kv4": [ctypes.POINTER(TvDesc)] + [_P] * 15,
+    "tv_kv4_workspace_size": [ctypes.POINTER(TvDesc), ctypes.POINTER(TvWindow), ctypes.POINTER(ctypes.c_size_t)],
+    "tv_kv4_attn_plan": [ctypes.POINTER(TvDesc), ctypes.POINTER(TvWindow), ctypes.POINTER(TvPlan)],
+    "tree_verify_attn_kv4": [ctypes.POINTER(TvDesc), ctypes.POINTER(TvWindow)] + [_P] * 12
+                            + [ctypes.c_size_t, _P, _P],
 }
 
 
@@ -265,3 +286,86 @@ def tree_accept_commit_argmax(desc, argmax, draft_tokens, parents, node_offsets,
 
 def tv_check_bounded_wait(limit_ns, status, stream=None):
     _check(lib().tv_check_bounded_wait(int(limit_ns), _ptr(status), _stream(stream)), "tv_check_bounded_wait")
+
+
+def make_window(window: int, sinks: int = 0) -> TvWindow:
+    return TvWindow(int(window), int(sinks))
+
+
+def _win(win):
+    return None if win is None else ctypes.byref(win)
+
+
+def _plan_dict(p: TvPlan) -> dict:
+    return {name: getattr(p, name) for name, _ in TvPlan._fields_}
+
+
+def tv_window_workspace_size(desc: TvDesc, win: TvWindow) -> int:
+    n = ctypes.c_size_t(0)
+    _check(lib().tv_window_workspace_size(ctypes.byref(desc), _win(win), ctypes.byref(n)),
+           "tv_window_workspace_size")
+    return n.value
+
+
+def tv_window_attn_plan(desc: TvDesc, win: TvWindow) -> dict:
+    p = TvPlan()
+    _check(lib().tv_window_attn_plan(ctypes.byref(desc), _win(win), ctypes.byref(p)), "tv_window_attn_plan")
+    return _plan_dict(p)
+
+
+def tree_verify_attn_window(desc, win, q, k_cache, v_cache, page_table, prefix_len, node_offsets, k_tree, v_tree, anc,
+                            depth, out, workspace, workspace_bytes, status, stream=None):
+    _check(lib().tree_verify_attn_window(ctypes.byref(desc), _win(win), _ptr(q), _ptr(k_cache), _ptr(v_cache),
+                                         _ptr(page_table), _ptr(prefix_len), _ptr(node_offsets), _ptr(k_tree),
+                                         _ptr(v_tree), _ptr(anc), _ptr(depth), _ptr(out), _ptr(workspace),
+                                         int(workspace_bytes), _ptr(status), _stream(stream)),
+           "tree_verify_attn_window")
+
+
+def tv_kv4_cache_bytes(desc: TvDesc) -> tuple:
+    """(bytes of the 4-bit K cache, bytes of the 4-bit V cache)."""
+    k, v = ctypes.c_int64(0), ctypes.c_int64(0)
+    _check(lib().tv_kv4_cache_bytes(ctypes.byref(desc), ctypes.byref(k), ctypes.byref(v)), "tv_kv4_cache_bytes")
+    return k.value, v.value
+
+
+def tv_kv4_append(desc, rows, max_rows, k, v, row_offsets, start, k4, v4, page_table, status, stream=None):
+    _check(lib().tv_kv4_append(ctypes.byref(desc), int(rows), int(max_rows), _ptr(k), _ptr(v), _ptr(row_offsets),
+                               _ptr(start), _ptr(k4), _ptr(v4), _ptr(page_table), _ptr(status), _stream(stream)),
+           "tv_kv4_append")
+
+
+def tv_kv4_read(desc, rows, max_rows, k4, v4, page_table, row_offsets, start, k, v, status, stream=None):
+    _check(lib().tv_kv4_read(ctypes.byref(desc), int(rows), int(max_rows), _ptr(k4), _ptr(v4), _ptr(page_table),
+                             _ptr(row_offsets), _ptr(start), _ptr(k), _ptr(v), _ptr(status), _stream(stream)),
+           "tv_kv4_read")
+
+
+def tree_accept_commit_argmax_kv4(desc, argmax, draft_tokens, parents, node_offsets, k_tree, v_tree, k4, v4,
+                                  page_table, prefix_len, accept_len, path, tokens, status, stream=None):
+    _check(lib().tree_accept_commit_argmax_kv4(ctypes.byref(desc), _ptr(argmax), _ptr(draft_tokens), _ptr(parents),
+                                               _ptr(node_offsets), _ptr(k_tree), _ptr(v_tree), _ptr(k4), _ptr(v4),
+                                               _ptr(page_table), _ptr(prefix_len), _ptr(accept_len), _ptr(path),
+                                               _ptr(tokens), _ptr(status), _stream(stream)),
+           "tree_accept_commit_argmax_kv4")
+
+
+def tv_kv4_workspace_size(desc: TvDesc, win: TvWindow = None) -> int:
+    n = ctypes.c_size_t(0)
+    _check(lib().tv_kv4_workspace_size(ctypes.byref(desc), _win(win), ctypes.byref(n)), "tv_kv4_workspace_size")
+    return n.value
+
+
+def tv_kv4_attn_plan(desc: TvDesc, win: TvWindow = None) -> dict:
+    p = TvPlan()
+    _check(lib().tv_kv4_attn_plan(ctypes.byref(desc), _win(win), ctypes.byref(p)), "tv_kv4_attn_plan")
+    return _plan_dict(p)
+
+
+def tree_verify_attn_kv4(desc, win, q, k4, v4, page_table, prefix_len, node_offsets, k_tree, v_tree, anc, depth, out,
+                         workspace, workspace_bytes, status, stream=None):
+    _check(lib().tree_verify_attn_kv4(ctypes.byref(desc), _win(win), _ptr(q), _ptr(k4), _ptr(v4), _ptr(page_table),
+                                      _ptr(prefix_len), _ptr(node_offsets), _ptr(k_tree), _ptr(v_tree), _ptr(anc),
+                                      _ptr(depth), _ptr(out), _ptr(workspace), int(workspace_bytes), _ptr(status),
+                                      _stream(stream)),
+           "tree_verify_attn_kv4")

@@ -8,18 +8,9 @@
 #include "tree_expand.h"
 #include "tv_internal.cuh"
 #include "tv_accept.cuh"
+#include "tv_host.cuh"
 
 namespace tv {
-namespace {
-
-bool mul_ok(int64_t a, int64_t b, int64_t* out) { return !__builtin_mul_overflow(a, b, out); }
-bool add_ok(int64_t a, int64_t b, int64_t* out) { return !__builtin_add_overflow(a, b, out); }
-
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
-int64_t align_up(int64_t x, int64_t a) { return (x + a - 1) / a * a; }
-
-}  // namespace
 
 int num_sms() {
   // per device (plans are made for the current device), safe across host threads
@@ -38,8 +29,6 @@ int num_sms() {
   if (tracked) cached[dev].store(n, std::memory_order_relaxed);
   return n;
 }
-
-namespace {
 
 // Checks shared by every entry point.  Order follows the pages' validation
 // list: dtype, head_dim, zero heads before the GQA modulo, shapes, overflow
@@ -72,15 +61,7 @@ int validate(const tv_desc* d) {
   return TV_OK;
 }
 
-struct Plan {
-  tv_plan pub;
-  int G;
-  int tree_tile;             // num_chunks rule: 0, or the key tile (one-wave plans)
-  int tile_stride;
-  int64_t o_part_bytes, ml_part_bytes;
-  int64_t counter_bytes;     // the persistent kernel's work counter (0 for the other kernels)
-  int64_t part_bytes() const { return o_part_bytes + ml_part_bytes + counter_bytes; }
-};
+namespace {
 
 int make_plan(const tv_desc* d, Plan* p) {
   int G = d->num_q_heads / d->num_kv_heads;
@@ -197,6 +178,8 @@ int64_t accept_bytes(const tv_desc* d, int V) {
   return 2 * align_up((int64_t)d->total_rows * vc * 4, 256);
 }
 
+}  // namespace
+
 cudaStream_t as_stream(void* s) { return reinterpret_cast<cudaStream_t>(s); }
 
 int check_attn_ptrs(const tv_desc* d, const void* q, const void* kc, const void* vc, const int32_t* pt,
@@ -246,8 +229,12 @@ AttnParams attn_params(const tv_desc* d, const Plan& pl, const void* q, const vo
   a.rows_per_tile = pl.pub.rows_per_tile; a.row_tiles = pl.pub.row_tiles;
   a.tile_stride = pl.tile_stride;
   a.part_bf16 = part_bf16(d, pl);
+  a.depth = nullptr;
+  a.window = pl.window; a.sinks = pl.sinks; a.map_tile = pl.map_tile;
   return a;
 }
+
+namespace {
 
 int launch_partials(const tv_desc* d, const Plan& pl, const AttnParams& a, cudaStream_t s) {
   cudaError_t e = pl.pub.kernel == 3   ? launch_attn_tcp(a, s)
@@ -256,6 +243,8 @@ int launch_partials(const tv_desc* d, const Plan& pl, const AttnParams& a, cudaS
                                        : launch_attn_simt(a, d->dtype, s);
   return e == cudaSuccess ? TV_OK : TV_ERR_CUDA;
 }
+
+}  // namespace
 
 int launch_merge_from(const tv_desc* d, const Plan& pl, const int32_t* plen, const int32_t* no, void* out,
                       const void* ws, int32_t* st, cudaStream_t s, int skip_single) {
@@ -273,10 +262,13 @@ int launch_merge_from(const tv_desc* d, const Plan& pl, const int32_t* plen, con
   m.chunk = pl.pub.chunk; m.tree_tile = pl.tree_tile; m.splits = pl.pub.num_splits;
   m.Hkv = d->num_kv_heads; m.G = pl.G; m.rows_per_tile = pl.pub.rows_per_tile;
   m.row_tiles = pl.pub.row_tiles; m.tile_stride = pl.tile_stride;
+  m.window = pl.window; m.sinks = pl.sinks; m.map_tile = pl.map_tile;
   merge_shape(d->batch * d->num_kv_heads * pl.pub.row_tiles, pl.tile_stride, d->head_dim, m.part_bf16 ? 2 : 4,
               pl.pub.num_splits, num_sms(), &m.slab_rows, &m.batch_splits);
   return launch_merge(m, s) == cudaSuccess ? TV_OK : TV_ERR_CUDA;
 }
+
+namespace {
 
 // tree_accept_commit and its sampled form: validation, workspace, launch.
 int accept_commit_impl(const tv_desc* desc, int32_t vocab, int32_t logits_dtype, const void* d_logits, int sampled,

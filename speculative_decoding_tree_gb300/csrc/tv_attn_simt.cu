@@ -16,6 +16,7 @@
 #include <cfloat>
 
 #include "tv_internal.cuh"
+#include "tv_kv4.cuh"
 
 namespace tv {
 namespace {
@@ -45,7 +46,11 @@ __device__ __forceinline__ void load8<__nv_bfloat16>(const __nv_bfloat16* src, f
   }
 }
 
-template <typename T, int D>
+// KV4: the prefix is a 4-bit cache (tree_kv4.h), expanded to fp32 as a tile is
+// staged: K by 8 channels of a key, V by 8 keys of a channel, one 32-bit word
+// each.  WIN: a sliding window with sinks (KeyMap): the chunk walks virtual
+// keys, and a row's view is applied as a mask on the scores.
+template <typename T, int D, bool KV4 = false, bool WIN = false>
 __global__ __launch_bounds__(128) void attn_simt_kernel(AttnParams p) {
   constexpr int RPW = 1024 / D;          // rows per warp
   constexpr int ROWS = 4 * RPW;          // rows per CTA
@@ -57,6 +62,7 @@ __global__ __launch_bounds__(128) void attn_simt_kernel(AttnParams p) {
   float* vs = ks + kKeyTile * KS;                         // [32][D]
   float* ps = vs + kKeyTile * D;                          // [4 warps][RPW][32]
   __shared__ uint64_t s_anc[ROWS];
+  __shared__ int s_dep[WIN ? ROWS : 1], s_kdep[WIN ? kMaxNodes : 1];   // depths of the CTA's rows and of the tree
   dep_wait();
   dep_launch();
 
@@ -72,10 +78,12 @@ __global__ __launch_bounds__(128) void attn_simt_kernel(AttnParams p) {
   const int64_t Praw = p.prefix_len[b];
   const int64_t P = clamp_prefix(Praw, p.max_prefix, p.capacity);
   if (P != Praw && threadIdx.x == 0 && rt == 0 && s == 0 && g == 0) set_status(p.status, TV_DEV_BAD_PREFIX);
-  const int nch = num_chunks(P, p.chunk, p.tree_tile);
+  const KeyMap km = key_map(P, WIN ? p.window : 0, p.sinks, p.map_tile);
+  const int64_t L = WIN ? km.len : P;
+  const int nch = num_chunks(L, p.chunk, p.tree_tile);
   if (s >= nch) return;
   const int64_t k_begin = (int64_t)s * p.chunk;
-  const int64_t k_end = min(P, k_begin + p.chunk);
+  const int64_t k_end = min(L, k_begin + p.chunk);
   const bool has_tree = (s == nch - 1);
 
   const T* q = reinterpret_cast<const T*>(p.q);
@@ -100,7 +108,10 @@ __global__ __launch_bounds__(128) void attn_simt_kernel(AttnParams p) {
   for (int r = tid; r < ROWS; r += blockDim.x) {
     const int m = m0 + r;
     s_anc[r] = m < nrows ? p.anc[o0 + m / p.G] : 0ull;
+    if (WIN) s_dep[r] = m < nrows ? p.depth[o0 + m / p.G] : 0;
   }
+  if (WIN)
+    for (int j = tid; j < n; j += blockDim.x) s_kdep[j] = p.depth[o0 + j];
 
   float m_run[RPW], l_run[RPW];
   float4 acc[RPW][CPL];
@@ -123,15 +134,64 @@ __global__ __launch_bounds__(128) void attn_simt_kernel(AttnParams p) {
     const bool tree_tile = tile >= n_prefix_tiles;
     const int64_t t0 = tree_tile ? (tile - n_prefix_tiles) * kKeyTile : k_begin + tile * kKeyTile;
     const int64_t t1 = tree_tile ? (int64_t)n : k_end;
+    const int64_t c0 = (!WIN || tree_tile) ? t0 : km.pos(t0);   // cache position of the tile's first key
     __syncthreads();   // previous tile fully consumed (and query rows staged)
+    if (KV4 && !tree_tile) {
+      const uint8_t* k4 = reinterpret_cast<const uint8_t*>(p.k_cache);
+      const uint8_t* v4 = reinterpret_cast<const uint8_t*>(p.v_cache);
+      for (int e = tid; e < kKeyTile * (D / 8); e += blockDim.x) {
+        const int j = e % kKeyTile, c8 = e / kKeyTile;          // K: key j, channels 8 c8 ..
+        const int64_t pos = c0 + j;
+        float4 lo = make_float4(0.f, 0.f, 0.f, 0.f), hi = lo;
+        if (t0 + j < t1 && !(WIN && pos >= p.sinks && pos <= P - p.window)) {
+          const uint8_t* blk = kv4::block_at(k4, kv4::k_block_bytes(D), b, g, pos / kPageSize, p.Hkv, p.max_pages,
+                                             p.page_table, p.num_pages);
+          if (blk) {
+            const int i = (int)(pos % kPageSize), c = c8 / 4;
+            const uint32_t w = *reinterpret_cast<const uint32_t*>(blk + kv4::k_code(c, i) + (c8 % 4) * 4);
+            const float sc = kv4::scale_of(blk[kv4::k_scale(D, c, i)]);
+            lo = make_float4((kv4::nibble(w, 0) - 8) * sc, (kv4::nibble(w, 1) - 8) * sc,
+                             (kv4::nibble(w, 2) - 8) * sc, (kv4::nibble(w, 3) - 8) * sc);
+            hi = make_float4((kv4::nibble(w, 4) - 8) * sc, (kv4::nibble(w, 5) - 8) * sc,
+                             (kv4::nibble(w, 6) - 8) * sc, (kv4::nibble(w, 7) - 8) * sc);
+          } else if (c8 == 0) {
+            set_status(p.status, TV_DEV_BAD_PAGE);
+          }
+        }
+        float4* kd = reinterpret_cast<float4*>(ks + j * KS + c8 * 8);
+        kd[0] = lo;
+        kd[1] = hi;
+      }
+      for (int e = tid; e < (kKeyTile / 8) * D; e += blockDim.x) {
+        const int ch = e % D, j0 = e / D * 8;                   // V: channel ch, keys j0 .. j0 + 7 (one block)
+        const int64_t pos = c0 + j0;
+        uint32_t w = 0x88888888u;
+        const uint8_t* blk = nullptr;
+        if (t0 + j0 < t1 && !(WIN && pos >= p.sinks && pos + 7 <= P - p.window))
+          blk = kv4::block_at(v4, kv4::v_block_bytes(D), b, g, pos / kPageSize, p.Hkv, p.max_pages, p.page_table,
+                              p.num_pages);
+        const int i = (int)(pos % kPageSize);
+        uint2 sc8 = make_uint2(0u, 0u);
+        if (blk) {
+          w = *reinterpret_cast<const uint32_t*>(blk + kv4::v_code(ch) + i / 8 * 4);
+          sc8 = *reinterpret_cast<const uint2*>(blk + kv4::v_scale(D, i));
+        }
+#pragma unroll
+        for (int t = 0; t < 8; ++t) {
+          const uint32_t code = ((t < 4 ? sc8.x : sc8.y) >> (8 * (t & 3))) & 255u;
+          vs[(j0 + t) * D + ch] = (kv4::nibble(w, t) - 8) * kv4::scale_of(code);
+        }
+      }
+    } else
     // cooperative load of 32 keys x D of K and V, converted to fp32
     for (int e = tid; e < kKeyTile * (D / 8); e += blockDim.x) {
       const int j = e / (D / 8), c8 = e % (D / 8);
-      const int64_t pos = t0 + j;
+      const int64_t pos = c0 + j;
       float tk[8], tv[8];
       const T* ksrc = nullptr;
       const T* vsrc = nullptr;
-      if (pos < t1) {
+      // (WIN: rows that no row sees hold undefined values, and stay zeros)
+      if (t0 + j < t1 && !(WIN && !tree_tile && pos >= p.sinks && pos <= P - p.window)) {
         if (tree_tile) {
           const int64_t row = (int64_t)g * p.R + o0 + pos;
           ksrc = kt + row * D;
@@ -184,13 +244,17 @@ __global__ __launch_bounds__(128) void attn_simt_kernel(AttnParams p) {
         sc[r] = fmaf(qv.w, kv.w, sc[r]);
       }
     }
-    const int64_t pos = t0 + lane;
-    const bool in_range = pos < t1;
+    const int64_t pos = c0 + lane;
+    const bool in_range = t0 + lane < t1;
     float* pw = ps + warp * RPW * kKeyTile;
 #pragma unroll
     for (int r = 0; r < RPW; ++r) {
       bool vis = in_range;
       if (tree_tile) vis = vis && ((s_anc[warp * RPW + r] >> pos) & 1ull);
+      if (WIN && vis) {
+        const int64_t kd = tree_tile ? s_kdep[pos] : pos - P;   // key's and row's positions, relative to P
+        vis = P + kd < p.sinks || s_dep[warp * RPW + r] - kd < p.window;
+      }
       float x = vis ? sc[r] * p.scale_log2 : -INFINITY;
       float mx = x;
 #pragma unroll
@@ -273,29 +337,41 @@ __global__ __launch_bounds__(128) void attn_simt_kernel(AttnParams p) {
   }
 }
 
-template <typename T, int D>
+template <typename T, int D, bool KV4 = false, bool WIN = false>
 cudaError_t launch_simt_t(const AttnParams& p, cudaStream_t s) {
   constexpr int RPW = 1024 / D;
   constexpr int ROWS = 4 * RPW;
   const size_t smem = sizeof(float) * (ROWS * D + kKeyTile * (D + 4) + kKeyTile * D + 4 * RPW * kKeyTile);
-  cudaError_t e = ensure_max_dynamic_smem<attn_simt_kernel<T, D>>((int)smem);
+  cudaError_t e = ensure_max_dynamic_smem<attn_simt_kernel<T, D, KV4, WIN>>((int)smem);
   if (e != cudaSuccess) return e;
   dim3 grid(p.row_tiles * p.Hkv, p.splits, p.B);
-  return launch_dep(attn_simt_kernel<T, D>, grid, dim3(128), smem, s, p);
+  return launch_dep(attn_simt_kernel<T, D, KV4, WIN>, grid, dim3(128), smem, s, p);
+}
+
+template <bool KV4, bool WIN>
+cudaError_t launch_simt_any(const AttnParams& p, int dtype, cudaStream_t s) {
+  if (dtype == TV_F32) {
+    if (p.d == 128) return launch_simt_t<float, 128, KV4, WIN>(p, s);
+    if (p.d == 256) return launch_simt_t<float, 256, KV4, WIN>(p, s);
+    return launch_simt_t<float, 512, KV4, WIN>(p, s);
+  }
+  if (p.d == 128) return launch_simt_t<__nv_bfloat16, 128, KV4, WIN>(p, s);
+  if (p.d == 256) return launch_simt_t<__nv_bfloat16, 256, KV4, WIN>(p, s);
+  return launch_simt_t<__nv_bfloat16, 512, KV4, WIN>(p, s);
 }
 
 }  // namespace
 
 cudaError_t launch_attn_simt(const AttnParams& p, int dtype, cudaStream_t s) {
-  if (dtype == TV_F32) {
-    if (p.d == 128) return launch_simt_t<float, 128>(p, s);
-    if (p.d == 256) return launch_simt_t<float, 256>(p, s);
-    return launch_simt_t<float, 512>(p, s);
-  }
-  if (p.d == 128) return launch_simt_t<__nv_bfloat16, 128>(p, s);
-  if (p.d == 256) return launch_simt_t<__nv_bfloat16, 256>(p, s);
-  return launch_simt_t<__nv_bfloat16, 512>(p, s);
+  return launch_simt_any<false, false>(p, dtype, s);
 }
 
+cudaError_t launch_attn_simt_window(const AttnParams& p, int dtype, cudaStream_t s) {
+  return launch_simt_any<false, true>(p, dtype, s);
+}
+
+cudaError_t launch_attn_simt_kv4(const AttnParams& p, int dtype, cudaStream_t s) {
+  return p.window > 0 ? launch_simt_any<true, true>(p, dtype, s) : launch_simt_any<true, false>(p, dtype, s);
+}
 
 }  // namespace tv

@@ -87,7 +87,11 @@ __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
   return *reinterpret_cast<uint32_t*>(&h);
 }
 
-template <int D>
+// WIN: a sliding window with sinks (KeyMap).  The chunk walks virtual keys; a
+// row's view is applied as a mask on the scores of the tiles that reach below
+// the last row's window, and V rows that no row sees are zeroed like the ones
+// past the prefix end (their contents are not defined: 0 x NaN).
+template <int D, bool WIN = false>
 __global__ void __launch_bounds__(kThreads, 1)
 tv_attn_tc_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUtensorMap tm_q,
                   const __grid_constant__ CUtensorMap tm_kc, const __grid_constant__ CUtensorMap tm_vc,
@@ -103,6 +107,8 @@ tv_attn_tc_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ 
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem_raw + C::NBARS * 8);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   float* xch = reinterpret_cast<float*>(smem_raw + 256);        // [2 parity][2 half][128 rows]
+  int* s_kdep = reinterpret_cast<int*>(smem_raw + 2304);        // [64] depths of the tree's nodes (WIN)
+  static_assert(2304 + 64 * 4 <= kHeader, "depths overflow the header");
   uint8_t* sQ = smem_raw + kHeader;
   uint8_t* ring = sQ + C::Q_BYTES;
   auto bar = [&](int i) { return smem_u32(&bars[i]); };
@@ -169,7 +175,7 @@ tv_attn_tc_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ 
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  if (warp == 3) {
+  if (!WIN && warp == 3) {
     // an idle warp warms L2 (and the TLB) for what the first steps read,
     // while the previous kernel may still run: the sequence's lengths, the
     // first kPrefetchTiles K and V tiles the chunk can hold (bounded by the
@@ -230,10 +236,18 @@ tv_attn_tc_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ 
   active = active && m0 < nrows;
   const int64_t P = clamp_prefix(Praw, p.max_prefix, p.capacity);
   if (active && P != Praw && tid == 0 && rt == 0 && s == 0 && g == 0) set_status(p.status, TV_DEV_BAD_PREFIX);
-  const int nch = num_chunks(P, p.chunk, p.tree_tile);
+  const KeyMap km = key_map(P, WIN ? p.window : 0, p.sinks, p.map_tile);
+  const int64_t L = WIN ? km.len : P;
+  const int nch = num_chunks(L, p.chunk, p.tree_tile);
   active = active && s < nch;                      // uniform over the CTA
   const int64_t k_begin = (int64_t)s * p.chunk;
-  const int64_t k_end = min(P, k_begin + p.chunk);
+  const int64_t k_end = min(L, k_begin + p.chunk);
+  // positions [sinks, first) are seen by no row
+  const int64_t first_pos = WIN ? P - p.window + 1 : 0;
+  auto tile_pos = [&](int tile) -> int64_t {       // cache position of a prefix tile's first key
+    const int64_t v = k_begin + (int64_t)tile * BN;
+    return WIN ? km.pos(v) : v;
+  };
   const bool has_tree = (s == nch - 1);
   const int npt = (int)((k_end - k_begin + BN - 1) / BN);      // prefix tiles
   const int T = npt + (has_tree ? 1 : 0);
@@ -255,8 +269,9 @@ tv_attn_tc_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ 
     const int oob_row = p.paged ? (int)(p.num_pages * p.Hkv * kPageSize) : 0;
     auto page_id = [&](int tile) -> int {           // raw page id of this lane's page, or INT_MIN (none)
       if (!p.paged || tile >= npt || lane >= BN / kPageSize) return INT_MIN;
-      const int64_t pos = k_begin + (int64_t)tile * BN + lane * kPageSize;
-      if (pos >= k_end) return INT_MIN;
+      if (k_begin + (int64_t)tile * BN + lane * kPageSize >= k_end) return INT_MIN;
+      const int64_t pos = tile_pos(tile) + lane * kPageSize;
+      if (WIN && pos >= p.sinks && pos + kPageSize <= first_pos) return INT_MIN;   // no row sees the page
       return p.page_table[(int64_t)b * p.max_pages + pos / kPageSize];
     };
     auto page_row = [&](int pid) -> int {           // TMA row of a page id, checked where it is used
@@ -280,7 +295,17 @@ tv_attn_tc_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ 
         const int tile = kind == 0 ? t : t - 1;
         if ((kind == 0 && t >= T) || (kind == 1 && t < 1)) continue;
         const bool tree = (tile == npt);
-        const bool tail_fix = (kind == 1) && !tree && tile == npt - 1 && tail_valid < BN;
+        // V rows to zero: [z0, z1) (no row sees them) and [ze, BN) (past the end)
+        int z0 = 0, z1 = 0, ze = BN;
+        if (kind == 1 && !tree) {
+          if (tile == npt - 1) ze = tail_valid;
+          if (WIN) {
+            const int64_t p0 = tile_pos(tile);
+            z0 = (int)min((int64_t)ze, max((int64_t)0, p.sinks - p0));
+            z1 = (int)min((int64_t)ze, max((int64_t)z0, first_pos - p0));
+          }
+        }
+        const bool tail_fix = ze < BN || z1 > z0;
         for (int c = 0; c < CPT && ok; ++c, ++j) {
           const int slot = j % NS, use = j / NS;
           if (use > 0 && !__all_sync(kAll, mbar_wait(EMPTY(slot), (use - 1) & 1, abort_flag, kWaitNs))) {
@@ -294,7 +319,7 @@ tv_attn_tc_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ 
               mbar_expect_tx(fb, CHUNK_BYTES);
               const CUtensorMap* m = tree ? (kind == 0 ? &tm_kt : &tm_vt) : (kind == 0 ? &tm_kc : &tm_vc);
               const int64_t row = tree ? (int64_t)g * p.R + o0
-                                       : ((int64_t)b * p.Hkv + g) * p.capacity + k_begin + (int64_t)tile * BN;
+                                       : ((int64_t)b * p.Hkv + g) * p.capacity + tile_pos(tile);
               for (int bx = 0; bx < 2; ++bx)
                 tma_load_2d(smem_u32(dst + bx * BOX_BYTES), m, fb, c * CH + bx * 64, (int)row);
             }
@@ -312,15 +337,16 @@ tv_attn_tc_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ 
           }
           __syncwarp();
           if (tail_fix) {
-            // the chunk's rows past the prefix end become zeros before the MMA reads them
+            // rows past the prefix end (and unseen rows) become zeros before the MMA reads them
             if (!__all_sync(kAll, mbar_wait(TAIL, tail_uses & 1, abort_flag, kWaitNs))) {
               ok = false;
               break;
             }
             ++tail_uses;
-            const int nz = BN - tail_valid;
+            const int nu = z1 - z0, nz = nu + BN - ze;
             for (int e = lane; e < 2 * nz * 8; e += 32) {
-              const int bx = e / (nz * 8), r = tail_valid + (e / 8) % nz, q16 = e % 8;
+              const int j = (e / 8) % nz;
+              const int bx = e / (nz * 8), r = j < nu ? z0 + j : ze + j - nu, q16 = e % 8;
               *reinterpret_cast<uint4*>(dst + bx * BOX_BYTES + r * 128 + q16 * 16) = make_uint4(0, 0, 0, 0);
             }
             fence_proxy_async_smem();
@@ -431,6 +457,12 @@ tv_attn_tc_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ 
     const int kofs = half * (BN / 2);                       // first key of this half
     float m_ref = -INFINITY, l = 0.f;
     bool ok = true;
+    int dep = 0;
+    if (WIN) {
+      if (row_ok) dep = p.depth[o0 + node];
+      if (tid - 128 < n) s_kdep[tid - 128] = p.depth[o0 + tid - 128];
+      asm volatile("bar.sync 1, 256;" ::: "memory");        // the softmax warps
+    }
     for (int t = 0; t < T && ok; ++t) {
       if (!__all_sync(kAll, mbar_wait(S_FULL(t & 1), (t >> 1) & 1, abort_flag, kWaitNs))) { ok = false; break; }
       tc_fence_after();
@@ -443,15 +475,24 @@ tv_attn_tc_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ 
         for (int e = 0; e < 64; ++e) sv[e] = __uint_as_float(rr[e]);
       }
       const bool tree = (t == npt);
-      const bool partial = tree || (t == npt - 1 && tail_valid < BN);
+      bool partial = tree || (t == npt - 1 && tail_valid < BN);
+      int rel_s = 0, rel_lo = 0;                            // WIN: visible keys are < rel_s or >= rel_lo
+      if (WIN && !tree) {
+        const int64_t p0 = tile_pos(t);
+        partial = partial || p0 < P + kMaxNodes - p.window;
+        rel_s = (int)min((int64_t)BN, max((int64_t)0, p.sinks - p0));
+        rel_lo = (int)min((int64_t)BN, max((int64_t)0, first_pos + dep - p0));
+      }
       if (partial) {
         // tree tile: ancestor bits; last prefix tile: key range
-        const int lim = tree ? min(n, 64) : tail_valid;
+        const int lim = tree ? min(n, 64) : (t == npt - 1 ? tail_valid : BN);
 #pragma unroll
         for (int e = 0; e < 64; ++e) {
           const int key = kofs + e;
           bool vis = key < lim;
           if (tree) vis = vis && ((anc >> (key & 63)) & 1ull);
+          if (WIN && tree) vis = vis && (P + s_kdep[key & 63] < p.sinks || dep - (int64_t)s_kdep[key & 63] < p.window);
+          if (WIN && !tree) vis = vis && (key < rel_s || key >= rel_lo);
           sv[e] = vis ? sv[e] : -INFINITY;
         }
       }
@@ -641,7 +682,7 @@ bool encode(CUtensorMap* m, const void* ptr, int rank, const cuuint64_t* dims, c
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int D>
+template <int D, bool WIN = false>
 cudaError_t launch_tc_t(const AttnParams& p, cudaStream_t st) {
   CUtensorMap mq, mkc, mvc, mkt, mvt;
   const cuuint64_t row_bytes = (cuuint64_t)D * 2;
@@ -680,10 +721,10 @@ cudaError_t launch_tc_t(const AttnParams& p, cudaStream_t st) {
                 p.part_bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32))
       return cudaErrorInvalidValue;
   }
-  cudaError_t e = ensure_max_dynamic_smem<tv_attn_tc_kernel<D>>((int)Cfg<D>::SMEM);
+  cudaError_t e = ensure_max_dynamic_smem<tv_attn_tc_kernel<D, WIN>>((int)Cfg<D>::SMEM);
   if (e != cudaSuccess) return e;
   dim3 grid(p.row_tiles, p.Hkv * p.splits, p.B);
-  return launch_dep(tv_attn_tc_kernel<D>, grid, dim3(kThreads), Cfg<D>::SMEM, st, p, mq, mkc, mvc, mkt, mvt, mop);
+  return launch_dep(tv_attn_tc_kernel<D, WIN>, grid, dim3(kThreads), Cfg<D>::SMEM, st, p, mq, mkc, mvc, mkt, mvt, mop);
 }
 
 }  // namespace
@@ -704,6 +745,11 @@ int tc_key_tile(int) { return BN; }
 cudaError_t launch_attn_tc(const AttnParams& p, cudaStream_t s) {
   if (p.d == 128) return launch_tc_t<128>(p, s);
   return launch_tc_t<256>(p, s);
+}
+
+cudaError_t launch_attn_tc_window(const AttnParams& p, cudaStream_t s) {
+  if (p.d == 128) return launch_tc_t<128, true>(p, s);
+  return launch_tc_t<256, true>(p, s);
 }
 
 }  // namespace tv

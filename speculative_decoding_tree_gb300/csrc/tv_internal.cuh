@@ -48,7 +48,42 @@ struct AttnParams {
   int rows_per_tile;         // query rows per row tile (node x group head)
   int row_tiles;
   int tile_stride;           // partial rows reserved per tile (>= rows_per_tile)
+  // a sliding window with sinks (window 0: the whole prefix; KeyMap below)
+  const int32_t* depth;      // [R], read when window > 0
+  int64_t window, sinks;
+  int map_tile;              // keys the sink region is rounded up to
 };
+
+// The prefix positions a windowed call walks, as one range of virtual keys:
+// [0, s0) are positions 0 .. s0 - 1 (the sinks, rounded up to whole key
+// tiles), [s0, len) are positions w0 .. P - 1 (w0: the first position any row
+// sees, rounded down to a 16-position block).  Without a gap between the two
+// (and without a window) the range is the prefix itself.  A tile of map_tile
+// keys never holds keys of both regions.
+struct KeyMap {
+  int64_t s0, w0, len;
+  __host__ __device__ int64_t pos(int64_t v) const { return v < s0 ? v : v - s0 + w0; }
+};
+
+__host__ __device__ inline KeyMap key_map(int64_t P, int64_t window, int64_t sinks, int tile) {
+  KeyMap m{0, 0, P};
+  if (window <= 0) return m;
+  const int64_t first = P - window + 1;            // the root's first window position
+  const int64_t w0 = first > 0 ? first / kPageSize * kPageSize : 0;
+  const int64_t s = sinks < P ? sinks : P;
+  const int64_t s0 = (s + tile - 1) / tile * tile;
+  if (w0 > s0) m = KeyMap{s0, w0, s0 + P - w0};
+  return m;
+}
+
+// Upper bound of key_map(P).len over every P <= max_prefix: the prefix, or
+// the sinks' tiles, the window and what rounding w0 down adds.
+__host__ __device__ inline int64_t key_map_bound(int64_t max_prefix, int64_t window, int64_t sinks, int tile) {
+  if (window <= 0 || window > max_prefix) return max_prefix;
+  const int64_t s = sinks < max_prefix ? sinks : max_prefix;
+  const int64_t n = (s + tile - 1) / tile * tile + window + kPageSize - 2;
+  return n < max_prefix ? n : max_prefix;
+}
 
 // Slot of the partial of query row m_in of row tile rt of (sequence b, KV
 // head g) from split s.  The splits of one row are adjacent, and the rows of
@@ -75,6 +110,8 @@ struct MergeParams {
   int early_reads;           // launched right after the split pass of the same call
   int slab_rows;             // rows per merge CTA (2..32, a power of two, <= tile_stride)
   int batch_splits;          // splits gathered into shared memory at once
+  int64_t window, sinks;     // as in AttnParams (0: the whole prefix)
+  int map_tile;
 };
 
 // Merge CTA shape for `tiles` (sequence, KV head, row tile) triples.
@@ -213,7 +250,10 @@ cudaError_t ensure_max_dynamic_smem(int bytes) {
 
 // Launchers (return cudaError_t of the launch).
 cudaError_t launch_attn_simt(const AttnParams& p, int dtype, cudaStream_t s);
+cudaError_t launch_attn_simt_window(const AttnParams& p, int dtype, cudaStream_t s);
+cudaError_t launch_attn_simt_kv4(const AttnParams& p, int dtype, cudaStream_t s);
 cudaError_t launch_attn_tc(const AttnParams& p, cudaStream_t s);
+cudaError_t launch_attn_tc_window(const AttnParams& p, cudaStream_t s);
 cudaError_t launch_attn_tc2(const AttnParams& p, cudaStream_t s);
 cudaError_t launch_attn_tcp(const AttnParams& p, cudaStream_t s);
 int64_t tcp_units(const AttnParams& p);

@@ -72,7 +72,7 @@ __global__ __launch_bounds__(kMergeThreads) void merge_slab_kernel(MergeParams p
   const int nrows = n * p.G;
   const int m_first = rt * p.rows_per_tile + r0;
   const int64_t P = clamp_prefix(Praw, p.max_prefix, p.capacity);
-  const int nch = num_chunks(P, p.chunk, p.tree_tile);
+  const int nch = num_chunks(key_map(P, p.window, p.sinks, p.map_tile).len, p.chunk, p.tree_tile);
   // rows this CTA writes (none: empty slab, or the split pass wrote them)
   const bool live = valid && r0 < p.rows_per_tile && m_first < nrows && !(p.skip_single && nch == 1);
   const int rows = live ? min(RS, min(p.rows_per_tile - r0, nrows - m_first)) : 0;

@@ -13,7 +13,9 @@ import torch
 from . import (BF16, F32, make_desc, make_expand_desc, tree_accept_commit, tree_accept_commit_sampled,
                tree_verify_attn, tv_attn_merge, tv_attn_partials, tv_build_tree_mask, tv_expand_steps,
                tv_expand_workspace_size, tv_tree_expand_step, tv_workspace_size, make_lmhead_desc,
-               tv_lm_head_argmax, tv_lm_head_workspace_size, tree_accept_commit_argmax)
+               tv_lm_head_argmax, tv_lm_head_workspace_size, tree_accept_commit_argmax,
+               make_window, tree_verify_attn_window, tv_window_workspace_size, tree_verify_attn_kv4,
+               tree_accept_commit_argmax_kv4, tv_kv4_append, tv_kv4_cache_bytes, tv_kv4_read, tv_kv4_workspace_size)
 
 _DT = {torch.float32: F32, torch.bfloat16: BF16}
 
@@ -108,6 +110,79 @@ class DeviceStep:
         return 4 + (1 if tv_attn_plan(self.desc)["num_splits"] > 1 else 0)
 
 
+class DeviceWindowStep(DeviceStep):
+    """A verify step whose rows see a sliding window and the first positions
+    (sinks) of the prefix; acceptance and commit are DeviceStep's."""
+
+    def __init__(self, w, window, sinks=0, **kw):
+        super().__init__(w, **kw)
+        self.win = make_window(window, sinks)
+        self.attn_ws_bytes = tv_window_workspace_size(self.desc, self.win)
+        self.attn_workspace = torch.empty(max(self.attn_ws_bytes, 256), dtype=torch.uint8, device=self.device)
+
+    def attn(self, stream=None):
+        tree_verify_attn_window(self.desc, self.win, self.q, self.k_cache, self.v_cache, self.page_table,
+                                self.prefix_len, self.node_offsets, self.k_tree, self.v_tree, self.anc, self.depth,
+                                self.out, self.attn_workspace, self.attn_ws_bytes, self.status, stream)
+
+
+class DeviceKv4Step(DeviceStep):
+    """A verify step on a cache held in 4 bits (win: (window, sinks) or None).
+    The workload's prefix rows are written by tv_kv4_append; accept_commit
+    walks on a given argmax and quantises the accepted rows."""
+
+    def __init__(self, w, win=None, **kw):
+        super().__init__(w, **kw)
+        self.win = None if win is None else make_window(*win)
+        kb, vb = tv_kv4_cache_bytes(self.desc)
+        self.k4 = torch.zeros(kb, dtype=torch.uint8, device=self.device)
+        self.v4 = torch.zeros(vb, dtype=torch.uint8, device=self.device)
+        self.attn_ws_bytes = tv_kv4_workspace_size(self.desc, self.win)
+        self.attn_workspace = torch.empty(max(self.attn_ws_bytes, 256), dtype=torch.uint8, device=self.device)
+        k, v, lens = self._prefix_rows()
+        self.k_cache = self.v_cache = None
+        self.append(k, v, lens, torch.zeros_like(self.prefix_len))
+
+    def _prefix_rows(self):
+        """The prefix of every sequence as [Hkv, sum P, d] rows, and their counts."""
+        lens = self.w.prefix_len.tolist()
+        rows = []
+        for x in (self.k_cache, self.v_cache):
+            if self.page_table is None:
+                rows.append([x[b, :, :n] for b, n in enumerate(lens)])
+            else:
+                flat = [x[self.page_table[b].long()].transpose(0, 1).flatten(1, 2) for b in range(len(lens))]
+                rows.append([f[:, :n] for f, n in zip(flat, lens)])
+        return torch.cat(rows[0], 1).contiguous(), torch.cat(rows[1], 1).contiguous(), lens
+
+    def _offsets(self, counts):
+        return torch.tensor([0] + torch.tensor(counts).cumsum(0).tolist(), dtype=torch.int32, device=self.device)
+
+    def append(self, k, v, counts, start, stream=None):
+        """Write k, v [Hkv, sum counts, d] at positions start[b] + i."""
+        tv_kv4_append(self.desc, k.shape[1], max(counts), k, v, self._offsets(counts), start, self.k4, self.v4,
+                      self.page_table, self.status, stream)
+
+    def read(self, counts, start, stream=None):
+        """The values at positions start[b] + i, [Hkv, sum counts, d] each."""
+        k = torch.empty(self.desc.num_kv_heads, sum(counts), self.desc.head_dim, dtype=self.q.dtype,
+                        device=self.device)
+        v = torch.empty_like(k)
+        tv_kv4_read(self.desc, k.shape[1], max(counts), self.k4, self.v4, self.page_table, self._offsets(counts),
+                    start, k, v, self.status, stream)
+        return k, v
+
+    def attn(self, stream=None):
+        tree_verify_attn_kv4(self.desc, self.win, self.q, self.k4, self.v4, self.page_table, self.prefix_len,
+                             self.node_offsets, self.k_tree, self.v_tree, self.anc, self.depth, self.out,
+                             self.attn_workspace, self.attn_ws_bytes, self.status, stream)
+
+    def accept_commit_argmax(self, argmax, stream=None):
+        tree_accept_commit_argmax_kv4(self.desc, argmax, self.draft, self.parents, self.node_offsets, self.k_tree,
+                                      self.v_tree, self.k4, self.v4, self.page_table, self.prefix_len,
+                                      self.accept_len, self.path, self.tokens, self.status, stream)
+
+
 class DeviceExpand:
     """Device buffers of one expansion workload (workloads.ExpandSpec): the
     synthetic drafter's logits of every step (resident), the roots, the tree
@@ -189,6 +264,8 @@ def main(argv=None):
     ap.add_argument("--attn-only", action="store_true", help="mask and attention only")
     ap.add_argument("--sampled", type=float, default=0.0,
                     help="temperature > 0: sampled verification (tree_accept_commit_sampled)")
+    ap.add_argument("--window", default="", help="W,S: rows see the last W and the first S positions (attention only)")
+    ap.add_argument("--kv4", action="store_true", help="the prefix in a 4-bit cache (attention only; with --window too)")
     ap.add_argument("--expand", default="", help="run a dynamic-expansion workload instead (eagle2, batched)")
     ap.add_argument("--lm-head", default="", help="run a fused lm_head + argmax workload instead (qwen, batched)")
     ap.add_argument("--vocab", type=int, default=0, help="with --lm-head: a smaller vocabulary (e.g. for a profiler)")
@@ -214,7 +291,9 @@ def main(argv=None):
         return 0 if status == 0 else 1
     w = wl.make_workload(wl.CONFIGS[a.config], canary=0.0,
                          argmax_fn=lambda x: torch.argmax(x.float(), dim=1))   # plants the draft tokens
-    st = DeviceStep(w)
+    win = tuple(int(x) for x in a.window.split(",")) if a.window else None
+    st = DeviceKv4Step(w, win) if a.kv4 else (DeviceWindowStep(w, *win) if win else DeviceStep(w))
+    a.attn_only = a.attn_only or a.kv4 or win is not None
     p0 = st.prefix_len.clone()
     for _ in range(a.steps):
         st.prefix_len.copy_(p0)
