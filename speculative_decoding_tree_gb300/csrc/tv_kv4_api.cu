@@ -20,9 +20,9 @@ int check_window(const tv_window* w) {
 // at most (key_map_bound) instead of max_prefix.
 int make_window_plan(const tv_desc* d, const tv_window* w, bool kv4, Plan* p) {
   const int G = d->num_q_heads / d->num_kv_heads;
-  const bool tc = !kv4 && tc_supported(d, G);
-  const int key_tile = tc ? tc_key_tile(d->head_dim) : 32;
-  const int rows_per_tile = tc ? (128 / G) * G : 4 * (1024 / d->head_dim);
+  const bool tc = !kv4 && tc_supported(d, G), tc4 = kv4 && kv4_tc_supported(d, G);
+  const int key_tile = tc ? tc_key_tile(d->head_dim) : (tc4 ? kv4_tc_key_tile() : 32);
+  const int rows_per_tile = tc ? (128 / G) * G : (tc4 ? kv4_tc_rows(G) : 4 * (1024 / d->head_dim));
   const int row_tiles = (d->max_nodes * G + rows_per_tile - 1) / rows_per_tile;
   p->window = w ? (w->window < kNoWindow ? w->window : kNoWindow) : 0;
   p->sinks = w ? w->sinks : 0;
@@ -51,16 +51,16 @@ int make_window_plan(const tv_desc* d, const tv_window* w, bool kv4, Plan* p) {
   const int64_t grid = units * splits;
   if (grid > ((int64_t)1 << 31) - 1) return TV_ERR_OVERFLOW;
   const int64_t grid_y = tc ? (int64_t)d->num_kv_heads * splits : (int64_t)splits;
-  if (d->batch > kMaxGridYZ || (int64_t)d->num_kv_heads * row_tiles > kMaxGridYZ || grid_y > kMaxGridYZ)
+  if (d->batch > kMaxGridYZ || (int64_t)d->num_kv_heads * row_tiles > kMaxGridYZ || (!tc4 && grid_y > kMaxGridYZ))
     return TV_ERR_SHAPE;
   p->G = G;
   p->tree_tile = tree_tile;
-  p->pub.kernel = tc ? 1 : 0;
+  p->pub.kernel = tc ? 1 : (tc4 ? 4 : 0);
   p->pub.num_splits = splits;
   p->pub.chunk = (int)chunk;
   p->pub.row_tiles = row_tiles;
   p->pub.rows_per_tile = rows_per_tile;
-  p->pub.grid_ctas = (int)grid;
+  p->pub.grid_ctas = (int)(tc4 && grid > sms ? sms : grid);
   p->counter_bytes = 0;
   p->tile_stride = tc ? 128 : rows_per_tile;
   int64_t t, o_bytes, ml_bytes;
@@ -124,7 +124,8 @@ int attention(const tv_desc* d, const tv_window* w, bool kv4, const void* q, con
   a.depth = depth;
   a.out = out;                                       // one-chunk sequences are finished by the split pass
   const cudaStream_t s = as_stream(stream);
-  const cudaError_t e = kv4                 ? launch_attn_simt_kv4(a, d->dtype, s)
+  const cudaError_t e = p.pub.kernel == 4 ? launch_attn_kv4(a, s)
+                        : kv4               ? launch_attn_simt_kv4(a, d->dtype, s)
                         : p.pub.kernel == 1 ? launch_attn_tc_window(a, s)
                                             : launch_attn_simt_window(a, d->dtype, s);
   if (e != cudaSuccess) return TV_ERR_CUDA;
