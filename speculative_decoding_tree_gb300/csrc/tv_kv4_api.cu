@@ -22,14 +22,15 @@ int make_window_plan(const tv_desc* d, const tv_window* w, bool kv4, Plan* p) {
   const int G = d->num_q_heads / d->num_kv_heads;
   const bool tc = !kv4 && tc_supported(d, G), tc4 = kv4 && kv4_tc_supported(d, G);
   const int key_tile = tc ? tc_key_tile(d->head_dim) : (tc4 ? kv4_tc_key_tile() : 32);
-  const int rows_per_tile = tc ? (128 / G) * G : (tc4 ? kv4_tc_rows(G) : 4 * (1024 / d->head_dim));
+  const int rows_per_tile = tc ? (128 / G) * G : (tc4 ? kv4_tc_columns(d->max_nodes, G) / G * G : 4 * (1024 / d->head_dim));
   const int row_tiles = (d->max_nodes * G + rows_per_tile - 1) / rows_per_tile;
   p->window = w ? (w->window < kNoWindow ? w->window : kNoWindow) : 0;
   p->sinks = w ? w->sinks : 0;
   p->map_tile = key_tile;
   const int64_t L = key_map_bound(d->max_prefix, p->window, p->sinks, key_tile);
   const int64_t units = (int64_t)d->batch * d->num_kv_heads * row_tiles;
-  const int64_t sms = num_sms();
+  // CTAs that run at once
+  const int64_t sms = num_sms() * (int64_t)(tc4 ? kv4_tc_ctas_per_sm(d->head_dim, kv4_tc_columns(d->max_nodes, G)) : 1);
   int64_t chunk;
   int tree_tile = 0;
   if (d->batch == 1) {
@@ -50,8 +51,8 @@ int make_window_plan(const tv_desc* d, const tv_window* w, bool kv4, Plan* p) {
   const int splits = num_chunks(L, (int)chunk, tree_tile);
   const int64_t grid = units * splits;
   if (grid > ((int64_t)1 << 31) - 1) return TV_ERR_OVERFLOW;
-  const int64_t grid_y = tc ? (int64_t)d->num_kv_heads * splits : (int64_t)splits;
-  if (d->batch > kMaxGridYZ || (int64_t)d->num_kv_heads * row_tiles > kMaxGridYZ || (!tc4 && grid_y > kMaxGridYZ))
+  const int64_t grid_y = tc || tc4 ? (int64_t)d->num_kv_heads * splits : (int64_t)splits;
+  if (d->batch > kMaxGridYZ || (int64_t)d->num_kv_heads * row_tiles > kMaxGridYZ || grid_y > kMaxGridYZ)
     return TV_ERR_SHAPE;
   p->G = G;
   p->tree_tile = tree_tile;
@@ -60,7 +61,7 @@ int make_window_plan(const tv_desc* d, const tv_window* w, bool kv4, Plan* p) {
   p->pub.chunk = (int)chunk;
   p->pub.row_tiles = row_tiles;
   p->pub.rows_per_tile = rows_per_tile;
-  p->pub.grid_ctas = (int)(tc4 && grid > sms ? sms : grid);
+  p->pub.grid_ctas = (int)grid;
   p->counter_bytes = 0;
   p->tile_stride = tc ? 128 : rows_per_tile;
   int64_t t, o_bytes, ml_bytes;
@@ -124,7 +125,7 @@ int attention(const tv_desc* d, const tv_window* w, bool kv4, const void* q, con
   a.depth = depth;
   a.out = out;                                       // one-chunk sequences are finished by the split pass
   const cudaStream_t s = as_stream(stream);
-  const cudaError_t e = p.pub.kernel == 4 ? launch_attn_kv4(a, s)
+  const cudaError_t e = p.pub.kernel == 4 ? launch_attn_kv4(a, kv4_tc_columns(d->max_nodes, p.G), s)
                         : kv4               ? launch_attn_simt_kv4(a, d->dtype, s)
                         : p.pub.kernel == 1 ? launch_attn_tc_window(a, s)
                                             : launch_attn_simt_window(a, d->dtype, s);
