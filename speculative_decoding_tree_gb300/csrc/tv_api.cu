@@ -202,7 +202,7 @@ int check_attn_ptrs(const tv_desc* d, const void* q, const void* kc, const void*
 // of the output alone puts them (relative 2.8e-3 against 1.7e-3 on a 60-node
 // tree over 4096 keys), and their partials are few.
 int part_bf16(const tv_desc* d, const Plan& pl) {
-  return (pl.pub.kernel != 0 && pl.pub.kernel != 4 && pl.window == 0 && d->dtype == TV_BF16 && !d->out_f32) ? 1 : 0;
+  return (pl.pub.kernel != 0 && pl.pub.kernel < 4 && pl.window == 0 && d->dtype == TV_BF16 && !d->out_f32) ? 1 : 0;
 }
 
 AttnParams attn_params(const tv_desc* d, const Plan& pl, const void* q, const void* kc, const void* vc,

@@ -20,50 +20,69 @@ int check_window(const tv_window* w) {
 // at most (key_map_bound) instead of max_prefix.
 int make_window_plan(const tv_desc* d, const tv_window* w, bool kv4, Plan* p) {
   const int G = d->num_q_heads / d->num_kv_heads;
-  const bool tc = !kv4 && tc_supported(d, G), tc4 = kv4 && kv4_tc_supported(d, G);
-  const int key_tile = tc ? tc_key_tile(d->head_dim) : (tc4 ? kv4_tc_key_tile() : 32);
-  const int rows_per_tile = tc ? (128 / G) * G : (tc4 ? kv4_tc_columns(d->max_nodes, G) / G * G : 4 * (1024 / d->head_dim));
+  // kernel: CUDA cores (0), one tensor-core CTA per row tile (1), and for the
+  // 4-bit cache tcgen05 (4) or, for few rows, registers only (5)
+  const int r_tiles = kv4 ? kv4_rows_tiles(d, G) : 0;
+  int kernel = 0, key_tile = 32, rows_per_tile = 4 * (1024 / d->head_dim), ctas_per_sm = 1;
+  int step = 32;                                     // keys a chunk grows by
+  if (!kv4 && tc_supported(d, G)) {
+    kernel = 1;
+    step = key_tile = tc_key_tile(d->head_dim);
+    rows_per_tile = (128 / G) * G;
+  } else if (r_tiles > 0) {
+    kernel = 5;
+    key_tile = kv4_rows_key_tile();
+    step = 4 * key_tile;                             // a span for each warp
+    rows_per_tile = 8 * r_tiles / G * G;
+    ctas_per_sm = kv4_rows_ctas_per_sm(d->head_dim, r_tiles);
+  } else if (kv4 && kv4_tc_supported(d, G)) {
+    kernel = 4;
+    step = key_tile = kv4_tc_key_tile();
+    const int cols = kv4_tc_columns(d->max_nodes, G);
+    rows_per_tile = cols / G * G;
+    ctas_per_sm = kv4_tc_ctas_per_sm(d->head_dim, cols);
+  }
   const int row_tiles = (d->max_nodes * G + rows_per_tile - 1) / rows_per_tile;
   p->window = w ? (w->window < kNoWindow ? w->window : kNoWindow) : 0;
   p->sinks = w ? w->sinks : 0;
   p->map_tile = key_tile;
   const int64_t L = key_map_bound(d->max_prefix, p->window, p->sinks, key_tile);
   const int64_t units = (int64_t)d->batch * d->num_kv_heads * row_tiles;
-  // CTAs that run at once
-  const int64_t sms = num_sms() * (int64_t)(tc4 ? kv4_tc_ctas_per_sm(d->head_dim, kv4_tc_columns(d->max_nodes, G)) : 1);
+  const int64_t slots = (int64_t)num_sms() * ctas_per_sm;          // CTAs that run at once
   int64_t chunk;
   int tree_tile = 0;
   if (d->batch == 1) {
-    // one wave (make_plan's rule)
-    int64_t want = sms / units;
+    // one wave (make_plan's rule); kernel 5 keeps the tree with the last chunk
+    int64_t want = slots / units;
     if (want < 1) want = 1;
-    const int64_t tiles = (L + key_tile - 1) / key_tile;
-    if (tiles > ((int64_t)1 << 30) / key_tile) return TV_ERR_OVERFLOW;
-    tree_tile = key_tile;
+    const int64_t tiles = (L + step - 1) / step;
+    if (tiles > ((int64_t)1 << 30) / step) return TV_ERR_OVERFLOW;
+    if (kernel != 5) tree_tile = step;
     int64_t c = (tiles + want - 1) / want;
     if (c < 1) c = 1;
-    while (c <= tiles && num_chunks(L, (int)(c * key_tile), tree_tile) > want) ++c;
-    chunk = c * key_tile;
+    while (c <= tiles && num_chunks(L, (int)(c * step), tree_tile) > want) ++c;
+    chunk = c * step;
   } else {
-    chunk = align_up(1920, key_tile);
+    chunk = align_up(1920, step);
   }
   if (chunk > (int64_t)1 << 30) return TV_ERR_OVERFLOW;
   const int splits = num_chunks(L, (int)chunk, tree_tile);
   const int64_t grid = units * splits;
   if (grid > ((int64_t)1 << 31) - 1) return TV_ERR_OVERFLOW;
-  const int64_t grid_y = tc || tc4 ? (int64_t)d->num_kv_heads * splits : (int64_t)splits;
+  // grids: sequences on z, (KV head, split) or, kernel 0, splits on y, the merge's (KV head, row tile) on y
+  const int64_t grid_y = kernel ? (int64_t)d->num_kv_heads * splits : (int64_t)splits;
   if (d->batch > kMaxGridYZ || (int64_t)d->num_kv_heads * row_tiles > kMaxGridYZ || grid_y > kMaxGridYZ)
     return TV_ERR_SHAPE;
   p->G = G;
   p->tree_tile = tree_tile;
-  p->pub.kernel = tc ? 1 : (tc4 ? 4 : 0);
+  p->pub.kernel = kernel;
   p->pub.num_splits = splits;
   p->pub.chunk = (int)chunk;
   p->pub.row_tiles = row_tiles;
   p->pub.rows_per_tile = rows_per_tile;
   p->pub.grid_ctas = (int)grid;
   p->counter_bytes = 0;
-  p->tile_stride = tc ? 128 : rows_per_tile;
+  p->tile_stride = kernel == 1 ? 128 : rows_per_tile;
   int64_t t, o_bytes, ml_bytes;
   if (!mul_ok(splits, d->batch, &t) || !mul_ok(t, d->num_kv_heads, &t) || !mul_ok(t, row_tiles, &t) ||
       !mul_ok(t, p->tile_stride, &t))
@@ -125,7 +144,8 @@ int attention(const tv_desc* d, const tv_window* w, bool kv4, const void* q, con
   a.depth = depth;
   a.out = out;                                       // one-chunk sequences are finished by the split pass
   const cudaStream_t s = as_stream(stream);
-  const cudaError_t e = p.pub.kernel == 4 ? launch_attn_kv4(a, kv4_tc_columns(d->max_nodes, p.G), s)
+  const cudaError_t e = p.pub.kernel == 5   ? launch_attn_kv4_rows(a, kv4_rows_tiles(d, p.G), s)
+                        : p.pub.kernel == 4 ? launch_attn_kv4(a, kv4_tc_columns(d->max_nodes, p.G), s)
                         : kv4               ? launch_attn_simt_kv4(a, d->dtype, s)
                         : p.pub.kernel == 1 ? launch_attn_tc_window(a, s)
                                             : launch_attn_simt_window(a, d->dtype, s);

@@ -159,7 +159,7 @@ __device__ void store_block(const T* k_rows, const T* v_rows, int d, uint8_t* kb
     uint2* dst = reinterpret_cast<uint2*>(vb + v_code(ch));
     uint32_t w[2] = {0u, 0u};
     if (keep_lo | keep_hi) {
-      const uint2 old = *dst;
+      const uint2 old = __ldcg(dst);           // through L2: the line's other blocks change meanwhile
       w[0] = old.x & keep_lo;
       w[1] = old.y & keep_hi;
     }
