@@ -3,17 +3,22 @@
 //
 // Quantisation of a group with largest magnitude A (32 channels of K, all
 // channels of V at one position): the smallest scale s with 7 s >= A, then
-// q = round(x / s) to even, |q| <= 7, u = q + 8.  The quotient is taken with
-// a reciprocal and corrected by the exact residual x - q s (one fused
-// multiply-add: it has no more bits than x), so the result is that of exact
-// arithmetic, ties included.
+// q = round(x / s) to even, |q| <= 7, u = q + 8.  x / s is taken as x times
+// the reciprocal, rounded to a whole number by adding 1.5 x 2^23 in one fused
+// multiply-add (no conversion instruction: those run at a quarter of the
+// rate), and corrected by the exact residual x - q s (it has no more bits than
+// x): the result is that of exact arithmetic, ties included.  The sum's low
+// bits are q, so eight of them pack by multiply-adds.
 //
-// One CTA handles the 16-position block of one KV head, K and V.  K is
-// quantised where it is loaded: four lanes hold a position's 32-channel group
-// and share its maximum.  V's codes run along the positions, so its 16 rows
-// are staged in shared memory once and read back by channel; a block that is
-// written in part keeps the other positions' nibbles.  Both directions are
-// bound by the bytes they move; nothing is read twice.
+// One CTA handles the 16-position block of one KV head, K and V, and issues
+// all its loads before the first use.  K is quantised where it is loaded: four
+// lanes hold a position's 32-channel group and share its maximum.  V's codes
+// run along the positions, so its 16 rows are staged in shared memory once and
+// read back by channel; a block that is written in part keeps the other
+// positions' nibbles.  Reading expands pairs as the attention does (mask and
+// one bf16 fused multiply-add, exact) and turns V back through shared memory.
+// Both directions are meant to be bound by the bytes they move; nothing is
+// read twice.
 #include "tv_kv4.cuh"
 #include "tv_kv4_store.cuh"
 
@@ -24,45 +29,87 @@ using namespace kv4;
 
 constexpr int kThreads = 128;
 
-// 8 values of a row in global memory (through L2: rows are read once)
+// 8 values of a row in global memory, raw (through L2: rows are read once)
 template <typename T>
-__device__ __forceinline__ void load_row8(const T* src, float (&x)[8]);
+struct Row8;
 
 template <>
-__device__ __forceinline__ void load_row8<float>(const float* src, float (&x)[8]) {
-  const float4 a = __ldcg(reinterpret_cast<const float4*>(src)), b = __ldcg(reinterpret_cast<const float4*>(src) + 1);
-  x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
-  x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
+struct Row8<float> {
+  float4 a, b;
+  __device__ __forceinline__ void load(const float* src) {
+    a = __ldcg(reinterpret_cast<const float4*>(src));
+    b = __ldcg(reinterpret_cast<const float4*>(src) + 1);
+  }
+  __device__ __forceinline__ void zero() { a = b = make_float4(0.f, 0.f, 0.f, 0.f); }
+  __device__ __forceinline__ void get(float (&x)[8]) const {
+    x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
+    x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
+  }
+  // largest magnitude as bits: above 0x7f800000 where a value is NaN
+  __device__ __forceinline__ uint32_t top() const {
+    const float v[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+    uint32_t m = 0;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) m = max(m, __float_as_uint(v[e]) & 0x7fffffffu);
+    return m;
+  }
+  __device__ __forceinline__ void tame(float most);
+  __device__ __forceinline__ void store(float* dst) const {        // to shared memory
+    reinterpret_cast<float4*>(dst)[0] = a;
+    reinterpret_cast<float4*>(dst)[1] = b;
+  }
+};
+
+template <>
+struct Row8<__nv_bfloat16> {
+  uint4 u;
+  __device__ __forceinline__ void load(const __nv_bfloat16* src) { u = __ldcg(reinterpret_cast<const uint4*>(src)); }
+  __device__ __forceinline__ void zero() { u = make_uint4(0, 0, 0, 0); }
+  __device__ __forceinline__ void get(float (&x)[8]) const {
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int t = 0; t < 4; ++t) {
+      x[2 * t] = __uint_as_float(w[t] << 16);
+      x[2 * t + 1] = __uint_as_float(w[t] & 0xffff0000u);
+    }
+  }
+  __device__ __forceinline__ uint32_t top() const {
+    const uint32_t m = __vmaxu2(__vmaxu2(u.x & 0x7fff7fffu, u.y & 0x7fff7fffu), __vmaxu2(u.z & 0x7fff7fffu, u.w & 0x7fff7fffu));
+    return max(m << 16, m & 0xffff0000u);
+  }
+  __device__ __forceinline__ void tame(float most);
+  __device__ __forceinline__ void store(__nv_bfloat16* dst) const { *reinterpret_cast<uint4*>(dst) = u; }
+};
+
+// The rare groups: a value that is not a number counts as 0, magnitudes end
+// at `most` (7 steps of the largest scale, a bf16 number too).
+__device__ __forceinline__ float tame1(float x, float most) { return x != x ? 0.f : fminf(fmaxf(x, -most), most); }
+__device__ __forceinline__ void Row8<float>::tame(float most) {
+  a = make_float4(tame1(a.x, most), tame1(a.y, most), tame1(a.z, most), tame1(a.w, most));
+  b = make_float4(tame1(b.x, most), tame1(b.y, most), tame1(b.z, most), tame1(b.w, most));
 }
-
-template <>
-__device__ __forceinline__ void load_row8<__nv_bfloat16>(const __nv_bfloat16* src, float (&x)[8]) {
-  const uint4 u = __ldcg(reinterpret_cast<const uint4*>(src));
-  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+__device__ __forceinline__ void Row8<__nv_bfloat16>::tame(float most) {
+  uint32_t* w = &u.x;
 #pragma unroll
   for (int t = 0; t < 4; ++t) {
-    x[2 * t] = __uint_as_float(w[t] << 16);
-    x[2 * t + 1] = __uint_as_float(w[t] & 0xffff0000u);
+    const uint32_t lo = __float_as_uint(tame1(__uint_as_float(w[t] << 16), most));
+    const uint32_t hi = __float_as_uint(tame1(__uint_as_float(w[t] & 0xffff0000u), most));
+    w[t] = (lo >> 16) | (hi & 0xffff0000u);
   }
 }
+constexpr float kMost = 7.f * 65536.f * 1.875f;  // 7 steps of the largest scale
 
-__device__ __forceinline__ void store_row8(float* dst, const float (&x)[8]) {
-  reinterpret_cast<float4*>(dst)[0] = make_float4(x[0], x[1], x[2], x[3]);
-  reinterpret_cast<float4*>(dst)[1] = make_float4(x[4], x[5], x[6], x[7]);
+// two adjacent values of a staged row
+__device__ __forceinline__ void two(const float* p, float& x, float& y) {
+  const float2 v = *reinterpret_cast<const float2*>(p);
+  x = v.x;
+  y = v.y;
 }
-__device__ __forceinline__ void store_row8(__nv_bfloat16* dst, const float (&x)[8]) {
-  uint4 u;
-  __nv_bfloat162 h[4];
-#pragma unroll
-  for (int t = 0; t < 4; ++t) h[t] = __floats2bfloat162_rn(x[2 * t], x[2 * t + 1]);   // exact: 7 significant bits
-  u.x = *reinterpret_cast<uint32_t*>(&h[0]);
-  u.y = *reinterpret_cast<uint32_t*>(&h[1]);
-  u.z = *reinterpret_cast<uint32_t*>(&h[2]);
-  u.w = *reinterpret_cast<uint32_t*>(&h[3]);
-  *reinterpret_cast<uint4*>(dst) = u;
+__device__ __forceinline__ void two(const __nv_bfloat16* p, float& x, float& y) {
+  const uint32_t w = *reinterpret_cast<const uint32_t*>(p);
+  x = __uint_as_float(w << 16);
+  y = __uint_as_float(w & 0xffff0000u);
 }
-
-__device__ __forceinline__ float no_nan(float x) { return x != x ? 0.f : x; }
 
 // smallest code whose 7 steps reach amax (255 if none): a guess from amax / 7
 // in rounded arithmetic, then stepped to the exact answer (7 s is exact)
@@ -75,101 +122,129 @@ __device__ __forceinline__ uint32_t scale_code(float amax) {
   return (uint32_t)c;
 }
 
-// q + 8 for x on the grid of step s (inv = 1 / s, rounded)
-__device__ __forceinline__ uint32_t code_of(float x, float s, float inv) {
-  float q = fminf(fmaxf(rintf(x * inv), -8.f), 8.f);
-  const float r = fmaf(-q, s, x), half = 0.5f * s, a = fabsf(r);
-  const bool odd = ((int)q) & 1;
-  if (a > half || (a == half && odd)) q += copysignf(1.f, r);
-  q = fminf(fmaxf(q, -7.f), 7.f);
-  return (uint32_t)((int)q + 8);
+constexpr float kMagic = 12582912.f;             // 1.5 x 2^23: x + kMagic is x rounded to a whole number
+constexpr uint32_t kMagicBits = 0x4B400000u;
+
+// bits kMagicBits + q of x on the grid of step s (inv = 1 / s, rounded); |x| <= 7 s
+__device__ __forceinline__ uint32_t steps_of(float x, float s, float inv) {
+  float t = fmaf(x, inv, kMagic);
+  const float r = fmaf(kMagic - t, s, x);
+  // too far, or half way with an odd q: one step on (the bound is s / 2, and for an odd q the float below it)
+  const float bound = __uint_as_float(__float_as_uint(0.5f * s) - (__float_as_uint(t) & 1u));
+  if (fabsf(r) > bound) t += copysignf(1.f, r);
+  return __float_as_uint(t);
 }
 
-__device__ __forceinline__ uint32_t pack8(const uint32_t (&u)[8]) {
-  uint32_t w = 0;
-#pragma unroll
-  for (int e = 0; e < 8; ++e) w |= u[e] << ((e >> 1) * 4 + (e & 1) * 16);
-  return w;
+__host__ __device__ constexpr int value_bit(int e) { return (e >> 1) * 4 + (e & 1) * 16; }
+
+// sum over e of (kMagicBits + 8's complement) << bit(e): what pack leaves on top of the codes q + 8
+__host__ __device__ constexpr uint32_t pack_excess() {
+  uint32_t c = 0;
+  for (int e = 0; e < 8; ++e) c += (kMagicBits - 8u) << value_bit(e);
+  return c;
 }
 
 // Writes the positions i of one block whose s_row[i] >= 0: row s_row[i] of
-// the head's k_rows / v_rows [rows, d].  xs: [16][d] floats of shared memory.
+// the head's k_rows / v_rows [rows, D].  xs: [16][D] of shared memory.
 // Called by all kThreads threads; ends with a barrier.
-template <typename T>
-__device__ void store_block(const T* k_rows, const T* v_rows, int d, uint8_t* kb, uint8_t* vb, const int* s_row,
-                            float* xs, uint32_t* s_code) {
+template <typename T, int D>
+__device__ __forceinline__ void store_block(const T* k_rows, const T* v_rows, uint8_t* kb, uint8_t* vb, const int* s_row,
+                                            T* xs, float2* s_step) {
+  constexpr int IT = D / 64;                     // 8-value pieces per thread, of K and of V
   const int tid = threadIdx.x;
+  Row8<T> kx[IT], vx[IT];
+  const int vi = tid >> 3, vrow = s_row[vi];
+#pragma unroll
+  for (int q = 0; q < IT; ++q) {
+    if (vrow >= 0)
+      vx[q].load(v_rows + (int64_t)vrow * D + ((tid & 7) + 8 * q) * 8);
+    else
+      vx[q].zero();
+  }
+#pragma unroll
+  for (int q = 0; q < IT; ++q) {
+    const int e = tid + q * kThreads, row = s_row[(e >> 2) & 15];
+    if (row >= 0)
+      kx[q].load(k_rows + (int64_t)row * D + (e >> 6) * kGroup + (e & 3) * 8);
+    else
+      kx[q].zero();
+  }
   // V: stage the rows and take each position's scale (8 threads a position)
   {
-    const int i = tid >> 3, part = tid & 7;
-    const int row = s_row[i];
-    float amax = 0.f;
-    if (row >= 0)
-      for (int c = part; c < d / 8; c += 8) {
-        float x[8];
-        load_row8<T>(v_rows + (int64_t)row * d + c * 8, x);
+    uint32_t top = 0;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          x[e] = no_nan(x[e]);
-          amax = fmaxf(amax, fabsf(x[e]));
-        }
-        store_row8(xs + i * d + c * 8, x);
+    for (int q = 0; q < IT; ++q) top = max(top, vx[q].top());
+#pragma unroll
+    for (int off = 1; off < 8; off <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, off));
+    if (top > __float_as_uint(kMost)) {                // NaN, infinity or beyond the largest scale
+      top = 0;
+#pragma unroll
+      for (int q = 0; q < IT; ++q) {
+        vx[q].tame(kMost);
+        top = max(top, vx[q].top());
       }
 #pragma unroll
-    for (int off = 1; off < 8; off <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, off));
-    if (part == 0 && row >= 0) {
-      const uint32_t code = scale_code(amax);
-      s_code[i] = code;
-      vb[v_scale(d, i)] = (uint8_t)code;
+      for (int off = 1; off < 8; off <<= 1) top = max(top, __shfl_xor_sync(0xffu << (tid & 24), top, off));
+    }
+#pragma unroll
+    for (int q = 0; q < IT; ++q) vx[q].store(xs + vi * D + ((tid & 7) + 8 * q) * 8);
+    if ((tid & 7) == 0) {
+      const uint32_t code = scale_code(__uint_as_float(top));
+      const float s = scale_of(code);
+      s_step[vi] = make_float2(s, 1.f / s);            // (a position not written: zeros on the smallest grid)
+      if (vrow >= 0) vb[v_scale(D, vi)] = (uint8_t)code;
     }
   }
   // K: 4 lanes a group of 32 channels, 8 positions a warp
-  for (int e = tid; e < 2 * d; e += kThreads) {
-    const int sub = e & 3, i = (e >> 2) & 15, c = e >> 6;
-    const int row = s_row[i];
-    float x[8];
-    float amax = 0.f;
-    if (row >= 0) {
-      load_row8<T>(k_rows + (int64_t)row * d + c * kGroup + sub * 8, x);
 #pragma unroll
-      for (int t = 0; t < 8; ++t) {
-        x[t] = no_nan(x[t]);
-        amax = fmaxf(amax, fabsf(x[t]));
-      }
+  for (int q = 0; q < IT; ++q) {
+    const int e = tid + q * kThreads, sub = e & 3, i = (e >> 2) & 15, c = e >> 6;
+    uint32_t top = kx[q].top();
+    top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+    top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+    if (top > __float_as_uint(kMost)) {
+      kx[q].tame(kMost);
+      top = kx[q].top();
+      top = max(top, __shfl_xor_sync(0xfu << (tid & 28), top, 1));
+      top = max(top, __shfl_xor_sync(0xfu << (tid & 28), top, 2));
     }
-    amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
-    amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
-    if (row >= 0) {
-      const uint32_t code = scale_code(amax);
+    if (s_row[i] >= 0) {
+      const uint32_t code = scale_code(__uint_as_float(top));
       const float s = scale_of(code), inv = 1.f / s;
-      uint32_t u[8];
+      float x[8];
+      kx[q].get(x);
+      uint32_t w = 0;
 #pragma unroll
-      for (int t = 0; t < 8; ++t) u[t] = code_of(x[t], s, inv);
-      *reinterpret_cast<uint32_t*>(kb + k_code(c, i) + sub * 4) = pack8(u);
-      if (sub == 0) kb[k_scale(d, c, i)] = (uint8_t)code;
+      for (int t = 0; t < 8; ++t) w += steps_of(x[t], s, inv) << value_bit(t);
+      *reinterpret_cast<uint32_t*>(kb + k_code(c, i) + sub * 4) = w - pack_excess();
+      if (sub == 0) kb[k_scale(D, c, i)] = (uint8_t)code;
     }
   }
   __syncthreads();
-  // V: a thread per channel gathers its 16 positions
-  uint32_t keep_lo = 0, keep_hi = 0;                   // nibbles of positions not written
+  // V: a thread gathers 8 positions (half h of the block) of two channels
+  const int h = tid >> 6;
+  uint32_t keep = 0;                                   // nibbles of positions not written
 #pragma unroll
-  for (int i = 0; i < 16; ++i)
-    if (s_row[i] < 0) (i < 8 ? keep_lo : keep_hi) |= 15u << (((i & 7) >> 1) * 4 + (i & 1) * 16);
-  for (int ch = tid; ch < d; ch += kThreads) {
-    uint2* dst = reinterpret_cast<uint2*>(vb + v_code(ch));
+  for (int i = 0; i < 8; ++i)
+    if (s_row[8 * h + i] < 0) keep |= 15u << value_bit(i);
+#pragma unroll 1
+  for (int ch = 2 * (tid & 63); ch < D; ch += kThreads) {
     uint32_t w[2] = {0u, 0u};
-    if (keep_lo | keep_hi) {
-      const uint2 old = __ldcg(dst);           // through L2: the line's other blocks change meanwhile
-      w[0] = old.x & keep_lo;
-      w[1] = old.y & keep_hi;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float2 st = s_step[8 * h + i];
+      float x, y;
+      two(xs + (8 * h + i) * D + ch, x, y);
+      w[0] += steps_of(x, st.x, st.y) << value_bit(i);
+      w[1] += steps_of(y, st.x, st.y) << value_bit(i);
     }
 #pragma unroll
-    for (int i = 0; i < 16; ++i)
-      if (s_row[i] >= 0) {
-        const float s = scale_of(s_code[i]);
-        w[i >> 3] |= code_of(xs[i * d + ch], s, 1.f / s) << (((i & 7) >> 1) * 4 + (i & 1) * 16);
-      }
-    *dst = make_uint2(w[0], w[1]);
+    for (int e = 0; e < 2; ++e) {
+      uint32_t* dst = reinterpret_cast<uint32_t*>(vb + v_code(ch + e)) + h;
+      w[e] -= pack_excess();
+      if (keep) w[e] = (w[e] & ~keep) | (__ldcg(dst) & keep);      // through L2: the line's other blocks change meanwhile
+      *dst = w[e];
+    }
   }
   __syncthreads();
 }
@@ -199,11 +274,11 @@ __device__ bool seq_range(const Kv4RowsParams& p, int b, bool lead, int64_t* r0,
 }
 
 // grid (blocks of the longest sequence, KV head, sequence)
-template <typename T>
+template <typename T, int D>
 __global__ __launch_bounds__(kThreads) void kv4_append_kernel(const Kv4RowsParams p) {
-  extern __shared__ float4 dyn[];
+  __shared__ __align__(16) T xs[16 * D];
   __shared__ int s_row[16];
-  __shared__ uint32_t s_code[16];
+  __shared__ float2 s_step[16];
   dep_wait();
   dep_launch();
   const int g = blockIdx.y, b = blockIdx.z, tid = threadIdx.x;
@@ -212,9 +287,9 @@ __global__ __launch_bounds__(kThreads) void kv4_append_kernel(const Kv4RowsParam
   if (!seq_range(p, b, tid == 0 && blockIdx.x == 0 && g == 0, &r0, &n, &start)) return;
   const int64_t blk = start / kPageSize + blockIdx.x;
   if (blk * kPageSize >= start + n) return;
-  uint8_t* kb = const_cast<uint8_t*>(block_at(p.k4, k_block_bytes(p.d), b, g, blk, p.Hkv, p.max_pages, p.page_table,
+  uint8_t* kb = const_cast<uint8_t*>(block_at(p.k4, k_block_bytes(D), b, g, blk, p.Hkv, p.max_pages, p.page_table,
                                               p.num_pages));
-  uint8_t* vb = const_cast<uint8_t*>(block_at(p.v4, v_block_bytes(p.d), b, g, blk, p.Hkv, p.max_pages, p.page_table,
+  uint8_t* vb = const_cast<uint8_t*>(block_at(p.v4, v_block_bytes(D), b, g, blk, p.Hkv, p.max_pages, p.page_table,
                                               p.num_pages));
   if (!kb) {
     if (tid == 0) set_status(p.status, TV_DEV_BAD_PAGE);
@@ -225,58 +300,92 @@ __global__ __launch_bounds__(kThreads) void kv4_append_kernel(const Kv4RowsParam
     s_row[tid] = i >= 0 && i < n ? (int)i : -1;
   }
   __syncthreads();
-  const T* k = reinterpret_cast<const T*>(p.k) + ((int64_t)g * p.rows + r0) * p.d;
-  const T* v = reinterpret_cast<const T*>(p.v) + ((int64_t)g * p.rows + r0) * p.d;
-  store_block<T>(k, v, p.d, kb, vb, s_row, reinterpret_cast<float*>(dyn), s_code);
+  const T* k = reinterpret_cast<const T*>(p.k) + ((int64_t)g * p.rows + r0) * D;
+  const T* v = reinterpret_cast<const T*>(p.v) + ((int64_t)g * p.rows + r0) * D;
+  store_block<T, D>(k, v, kb, vb, s_row, xs, s_step);
 }
 
-template <typename T>
+__device__ __forceinline__ uint32_t fma_bf16x2(uint32_t a, uint32_t b, uint32_t c) {
+  uint32_t r;
+  asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(c));
+  return r;
+}
+
+// pair j of a word times the bf16 pair of scales s2, exact
+__device__ __forceinline__ uint32_t pair_value(uint32_t w, int j, uint32_t s2) {
+  return fma_bf16x2(((w >> (4 * j)) & 0x000F000Fu) | 0x43004300u, s2, fma_bf16x2(s2, 0xC308C308u, 0x80008000u));
+}
+__device__ __forceinline__ uint32_t scale_bits(uint32_t code) { return (code << 4) + 0x3800u; }   // as bf16
+
+// 8 bf16 values to a row
+__device__ __forceinline__ void put8(__nv_bfloat16* dst, const uint4& u) { *reinterpret_cast<uint4*>(dst) = u; }
+__device__ __forceinline__ void put8(float* dst, const uint4& u) {
+  reinterpret_cast<uint4*>(dst)[0] = make_uint4(u.x << 16, u.x & 0xffff0000u, u.y << 16, u.y & 0xffff0000u);
+  reinterpret_cast<uint4*>(dst)[1] = make_uint4(u.z << 16, u.z & 0xffff0000u, u.w << 16, u.w & 0xffff0000u);
+}
+
+template <typename T, int D>
 __global__ __launch_bounds__(kThreads) void kv4_read_kernel(const Kv4RowsParams p) {
-  extern __shared__ float4 dyn[];
-  float* xs = reinterpret_cast<float*>(dyn);
+  constexpr int IT = D / 64, PITCH = D + 8;      // (the pad keeps 16-byte rows and spreads the banks)
+  __shared__ __align__(16) uint16_t xs[16 * PITCH];
   dep_wait();
   dep_launch();
-  const int g = blockIdx.y, b = blockIdx.z, tid = threadIdx.x, d = p.d;
+  const int g = blockIdx.y, b = blockIdx.z, tid = threadIdx.x;
   int64_t r0, start;
   int n;
   if (!seq_range(p, b, tid == 0 && blockIdx.x == 0 && g == 0, &r0, &n, &start)) return;
   const int64_t blk = start / kPageSize + blockIdx.x;
   const int64_t first = blk * kPageSize - start;       // row of the block's position 0 (may be negative)
   if (first >= n) return;
-  const uint8_t* kb = block_at(p.k4, k_block_bytes(d), b, g, blk, p.Hkv, p.max_pages, p.page_table, p.num_pages);
-  const uint8_t* vb = block_at(p.v4, v_block_bytes(d), b, g, blk, p.Hkv, p.max_pages, p.page_table, p.num_pages);
+  const uint8_t* kb = block_at(p.k4, k_block_bytes(D), b, g, blk, p.Hkv, p.max_pages, p.page_table, p.num_pages);
+  const uint8_t* vb = block_at(p.v4, v_block_bytes(D), b, g, blk, p.Hkv, p.max_pages, p.page_table, p.num_pages);
   if (!kb) {
     if (tid == 0) set_status(p.status, TV_DEV_BAD_PAGE);
     return;
   }
-  T* k = reinterpret_cast<T*>(p.k_out) + ((int64_t)g * p.rows + r0) * d;
-  T* v = reinterpret_cast<T*>(p.v_out) + ((int64_t)g * p.rows + r0) * d;
-  for (int ch = tid; ch < d; ch += kThreads) {
-    const uint2 w = *reinterpret_cast<const uint2*>(vb + v_code(ch));
+  T* k = reinterpret_cast<T*>(p.k_out) + ((int64_t)g * p.rows + r0) * D;
+  T* v = reinterpret_cast<T*>(p.v_out) + ((int64_t)g * p.rows + r0) * D;
+  // every load first
+  constexpr int CT = D / kThreads;               // V channels per thread
+  uint2 vw[CT];
+  uint32_t kw[IT], kc[IT];
+  const uint4 vsc = __ldcg(reinterpret_cast<const uint4*>(vb + v_scale(D, 0)));
 #pragma unroll
-    for (int i = 0; i < 16; ++i)
-      xs[i * d + ch] = (float)(nibble(i < 8 ? w.x : w.y, i & 7) - 8) * scale_of(vb[v_scale(d, i)]);
+  for (int q = 0; q < CT; ++q) vw[q] = __ldcg(reinterpret_cast<const uint2*>(vb + v_code(tid + q * kThreads)));
+#pragma unroll
+  for (int q = 0; q < IT; ++q) {
+    const int e = tid + q * kThreads, sub = e & 3, i = (e >> 2) & 15, c = e >> 6;
+    kw[q] = __ldcg(reinterpret_cast<const uint32_t*>(kb + k_code(c, i)) + sub);
+    kc[q] = __ldcg(kb + k_scale(D, c, i));
   }
-  for (int e = tid; e < 2 * d; e += kThreads) {
-    const int sub = e & 3, i = (e >> 2) & 15, c = e >> 6;
+#pragma unroll
+  for (int q = 0; q < CT; ++q) {
+    const uint32_t sc[4] = {vsc.x, vsc.y, vsc.z, vsc.w};
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {                      // positions 2 j, 2 j + 1
+      const uint32_t two = sc[j >> 1] >> (16 * (j & 1));
+      const uint32_t s2 = scale_bits(two & 255u) | (scale_bits((two >> 8) & 255u) << 16);
+      const uint32_t x = pair_value(j < 4 ? vw[q].x : vw[q].y, j & 3, s2);
+      xs[(2 * j) * PITCH + tid + q * kThreads] = (uint16_t)x;
+      xs[(2 * j + 1) * PITCH + tid + q * kThreads] = (uint16_t)(x >> 16);
+    }
+  }
+#pragma unroll
+  for (int q = 0; q < IT; ++q) {
+    const int e = tid + q * kThreads, sub = e & 3, i = (e >> 2) & 15, c = e >> 6;
     const int64_t row = first + i;
     if (row < 0 || row >= n) continue;
-    const uint32_t w = *reinterpret_cast<const uint32_t*>(kb + k_code(c, i) + sub * 4);
-    const float s = scale_of(kb[k_scale(d, c, i)]);
-    float x[8];
-#pragma unroll
-    for (int t = 0; t < 8; ++t) x[t] = (float)(nibble(w, t) - 8) * s;
-    store_row8(k + row * d + c * kGroup + sub * 8, x);
+    const uint32_t s2 = scale_bits(kc[q]) * 0x00010001u;
+    put8(k + row * D + c * kGroup + sub * 8, make_uint4(pair_value(kw[q], 0, s2), pair_value(kw[q], 1, s2),
+                                                        pair_value(kw[q], 2, s2), pair_value(kw[q], 3, s2)));
   }
   __syncthreads();
-  for (int e = tid; e < 2 * d; e += kThreads) {
-    const int c8 = e % (d / 8), i = e / (d / 8);
+#pragma unroll
+  for (int q = 0; q < IT; ++q) {
+    const int e = tid + q * kThreads, c8 = e % (D / 8), i = e / (D / 8);
     const int64_t row = first + i;
     if (row < 0 || row >= n) continue;
-    const float4 lo = reinterpret_cast<const float4*>(xs + i * d + c8 * 8)[0];
-    const float4 hi = reinterpret_cast<const float4*>(xs + i * d + c8 * 8)[1];
-    const float x[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
-    store_row8(v + row * d + c8 * 8, x);
+    put8(v + row * D + c8 * 8, *reinterpret_cast<const uint4*>(xs + i * PITCH + c8 * 8));
   }
 }
 
@@ -289,14 +398,14 @@ __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.w
 // heads c, c + C, ...  The rule is tree_accept_commit's: node c matches when
 // its draft is its parent's target argmax; the end of the path is the deepest
 // node whose whole root path matches, the smallest index among equals.
-template <typename T>
+template <typename T, int D>
 __global__ __launch_bounds__(kThreads) void kv4_commit_kernel(const Kv4CommitParams p) {
-  extern __shared__ float4 dyn[];
+  __shared__ __align__(16) T xs[16 * D];
   __shared__ int s_par[kMaxNodes], s_draft[kMaxNodes], s_am[kMaxNodes], s_path[kMaxNodes];
   __shared__ uint64_t s_anc[kMaxNodes];
   __shared__ uint32_t s_match[2];
   __shared__ int s_key[2], s_pid[kMaxNodes / kPageSize + 1], s_bad, s_row[16];
-  __shared__ uint32_t s_code[16];
+  __shared__ float2 s_step[16];
   dep_wait();
   dep_launch();
   const int b = blockIdx.y, tid = threadIdx.x, lane = tid & 31;
@@ -388,8 +497,8 @@ __global__ __launch_bounds__(kThreads) void kv4_commit_kernel(const Kv4CommitPar
   if (ok) {
     const int first = P / kPageSize, last = (P + k) / kPageSize;
     for (int g = blockIdx.x; g < p.Hkv; g += gridDim.x) {
-      const T* kr = reinterpret_cast<const T*>(p.k_tree) + ((int64_t)g * p.R + o0) * p.d;
-      const T* vr = reinterpret_cast<const T*>(p.v_tree) + ((int64_t)g * p.R + o0) * p.d;
+      const T* kr = reinterpret_cast<const T*>(p.k_tree) + ((int64_t)g * p.R + o0) * D;
+      const T* vr = reinterpret_cast<const T*>(p.v_tree) + ((int64_t)g * p.R + o0) * D;
       for (int blk = first; blk <= last; ++blk) {
         if (tid < 16) {
           const int t = blk * kPageSize + tid - P;
@@ -398,8 +507,7 @@ __global__ __launch_bounds__(kThreads) void kv4_commit_kernel(const Kv4CommitPar
         __syncthreads();
         const int64_t at = p.page_table ? (int64_t)s_pid[blk - first] * p.Hkv + g
                                         : ((int64_t)b * p.Hkv + g) * p.max_pages + blk;
-        store_block<T>(kr, vr, p.d, p.k4 + at * k_block_bytes(p.d), p.v4 + at * v_block_bytes(p.d), s_row,
-                       reinterpret_cast<float*>(dyn), s_code);
+        store_block<T, D>(kr, vr, p.k4 + at * k_block_bytes(D), p.v4 + at * v_block_bytes(D), s_row, xs, s_step);
       }
     }
   }
@@ -409,18 +517,20 @@ __global__ __launch_bounds__(kThreads) void kv4_commit_kernel(const Kv4CommitPar
 
 }  // namespace
 
+// kernel<T, D> for a dtype and head_dim
+#define TV_KV4_PICK(kernel, dtype, d)                                                                     \
+  ((dtype) == TV_F32 ? ((d) == 128 ? kernel<float, 128> : ((d) == 256 ? kernel<float, 256> : kernel<float, 512>)) \
+                     : ((d) == 128 ? kernel<__nv_bfloat16, 128>                                           \
+                                   : ((d) == 256 ? kernel<__nv_bfloat16, 256> : kernel<__nv_bfloat16, 512>)))
+
 cudaError_t launch_kv4_append(const Kv4RowsParams& p, int dtype, cudaStream_t s) {
   const dim3 grid((unsigned)((p.max_rows + kPageSize - 1) / kPageSize + 1), p.Hkv, p.B);
-  const size_t smem = (size_t)kPageSize * p.d * 4;
-  return dtype == TV_F32 ? launch_dep(kv4_append_kernel<float>, grid, dim3(kThreads), smem, s, p)
-                         : launch_dep(kv4_append_kernel<__nv_bfloat16>, grid, dim3(kThreads), smem, s, p);
+  return launch_dep(TV_KV4_PICK(kv4_append_kernel, dtype, p.d), grid, dim3(kThreads), 0, s, p);
 }
 
 cudaError_t launch_kv4_read(const Kv4RowsParams& p, int dtype, cudaStream_t s) {
   const dim3 grid((unsigned)((p.max_rows + kPageSize - 1) / kPageSize + 1), p.Hkv, p.B);
-  const size_t smem = (size_t)kPageSize * p.d * 4;
-  return dtype == TV_F32 ? launch_dep(kv4_read_kernel<float>, grid, dim3(kThreads), smem, s, p)
-                         : launch_dep(kv4_read_kernel<__nv_bfloat16>, grid, dim3(kThreads), smem, s, p);
+  return launch_dep(TV_KV4_PICK(kv4_read_kernel, dtype, p.d), grid, dim3(kThreads), 0, s, p);
 }
 
 cudaError_t launch_kv4_commit(const Kv4CommitParams& p, int dtype, cudaStream_t s) {
@@ -428,7 +538,6 @@ cudaError_t launch_kv4_commit(const Kv4CommitParams& p, int dtype, cudaStream_t 
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(C, p.B);
   cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = (size_t)kPageSize * p.d * 4;
   cfg.stream = s;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -439,8 +548,7 @@ cudaError_t launch_kv4_commit(const Kv4CommitParams& p, int dtype, cudaStream_t 
   attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  return dtype == TV_F32 ? cudaLaunchKernelEx(&cfg, kv4_commit_kernel<float>, p)
-                         : cudaLaunchKernelEx(&cfg, kv4_commit_kernel<__nv_bfloat16>, p);
+  return cudaLaunchKernelEx(&cfg, TV_KV4_PICK(kv4_commit_kernel, dtype, p.d), p);
 }
 
 }  // namespace tv
