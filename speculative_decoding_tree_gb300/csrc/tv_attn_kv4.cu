@@ -9,8 +9,7 @@
 //
 // Both products are taken transposed, so that the cache's values are the A
 // operand and go from registers into tensor memory, never through shared
-// memory, and so that N = 16, 32 or 64 query rows cost N columns instead of a
-// 128-row tile:
+// memory, and so that N = 16 .. 128 query rows cost N columns:
 //   S^T [128 keys x N rows]     = K  [keys x d]        Q^T   (A: tensor memory, B: Q in shared memory)
 //   O^T [128 channels x N rows] += V^T [channels x keys] P^T  (A: tensor memory, B: P in shared memory)
 // A lane of an A operand is a key of K and a channel of V: the cache's K
@@ -30,13 +29,14 @@
 // reference by more than 60 (log2) takes the true column maximum and rescales
 // O.  Tiles whose mask hides keys from some rows start from the true maximum.
 //
-// Every compute warp does every step of a tile (expand K, softmax, expand V),
-// one of them issues the MMAs, and a separate warp copies the packed blocks
-// ahead into a ring; 4, 2 or 1 such CTAs share an SM (128, 256 or 512 columns
-// of tensor memory), so that one's products and waits run beside another's
-// arithmetic.  A first build with a warp group per step and a persistent CTA
-// per SM was bound by its hand-offs and by instruction fetch over five kinds
-// of loops (64 sequences x 1 row over up to 16384 keys: 422 us).
+// Every compute warp does every step of a tile: expand K (a tile ahead where
+// tensor memory has room for two score tiles), softmax, expand V; one warp
+// issues the MMAs and one copies the packed blocks ahead into a ring.  4, 2 or
+// 1 such CTAs share an SM (128, 256 or 512 columns of tensor memory), so that
+// one's products and waits run beside another's arithmetic.  A first build with
+// a warp group per step and a persistent CTA per SM was bound by its hand-offs
+// and by instruction fetch over five kinds of loops (64 sequences x 1 row over
+// up to 16384 keys: 422 us against 264 us).
 //
 // Every mbarrier wait is bounded (1 s); on a timeout the CTA raises
 // TV_DEV_TIMEOUT, waits for its own copies and MMAs, frees tensor memory and
@@ -45,6 +45,7 @@
 
 #include <climits>
 #include <mutex>
+#include <type_traits>
 
 #include "tc_ptx.cuh"
 #include "tv_kv4.cuh"
@@ -58,35 +59,40 @@ constexpr int BK = 128;                          // keys per tile
 constexpr int kBlocks = BK / kPageSize;          // cache blocks per tile
 constexpr uint64_t kWaitNs = 1000000000ull;
 constexpr float kHeadroom = 60.0f;               // log2: a weight above 2^60 moves the reference
-constexpr uint32_t kHeader = 4096;
+constexpr uint32_t kHeader = 6144;
 
 // head_dim D, N query rows per tile
 template <int D, int N>
 struct Cfg {
   static constexpr int CPT = D / 128;                       // 128-channel chunks of a tile
   static constexpr int KB = kv4::k_block_bytes(D), VB = kv4::v_block_bytes(D);
-  // tensor memory columns: scores, outputs, A operands of 64 columns
+  // tensor memory columns: scores (two tiles where they fit), outputs, A operands of 64 columns
   static constexpr int USED = N + CPT * N + 64;
-  static constexpr int TCOLS = USED <= 128 ? 128 : (USED <= 256 ? 256 : 512);
-  static constexpr int NS = TCOLS - N - CPT * N >= 128 ? 2 : 1;   // A operands
-  static constexpr uint32_t T_S = 0, T_O = N, T_A = N + CPT * N;
+  static constexpr int TCOLS = USED <= 128 && N < 32 ? 128 : (USED <= 256 ? 256 : 512);
+  static constexpr bool PIPE = TCOLS >= 2 * N + CPT * N + 64;
+  static_assert(PIPE || CPT > 1, "the V slot is read (scales) after its first chunk is expanded");
+  static constexpr int T_S = 0, T_O = N * (PIPE ? 2 : 1), T_A = T_O + CPT * N;
+  static constexpr int NS = TCOLS - T_A >= 128 ? 2 : 1;     // A operands
   static constexpr int CTAS = 512 / TCOLS;                  // per SM
   static constexpr int GPT = TCOLS / 128;                   // warp groups of 128 lanes
   static constexpr int HC = N / GPT < 16 ? 16 : N / GPT;    // rows per softmax thread
-  static constexpr int kCompute = 128 * GPT, kThreads = kCompute + 32;
-  // ring slots: (D, N) with the shared memory of CTAS CTAs per SM
-  static constexpr int NK = D == 128 ? (N == 64 ? 4 : 2) : (D == 256 ? (N == 16 ? 1 : 2) : (N == 64 ? 2 : 1));
+  static constexpr int kWarps = 4 * GPT, kCompute = 32 * kWarps, kThreads = kCompute + 64;
+  // ring slots that the shared memory of CTAS CTAs per SM holds
+  static constexpr int NK = D == 128 ? (N == 128 ? 6 : (N == 64 ? 4 : (N == 32 ? 4 : 2)))
+                                     : (D == 256 ? (N == 16 ? 1 : 2) : (N == 64 ? 2 : 1));
   static constexpr int NV = D == 256 && N == 64 ? 1 : NK;
-  static constexpr uint32_t Q_BYTES = N * D * 2, P_PITCH = 2 * N, P_BYTES = BK * P_PITCH;
-  static constexpr uint32_t P_SWIZZLE = N == 64 ? 2 : (N == 32 ? 4 : 6);   // 128, 64, 32-byte rows
+  static constexpr int P_COLS = N < 64 ? N : 64;            // columns of a P box: rows of 32, 64 or 128 bytes
+  static constexpr uint32_t P_PITCH = 2 * P_COLS, P_BOX = BK * P_PITCH, P_BYTES = BK * 2 * N;
+  static constexpr uint32_t P_SWIZZLE = P_COLS == 64 ? 2 : (P_COLS == 32 ? 4 : 6);
+  static constexpr uint32_t Q_BYTES = N * D * 2;
   static constexpr uint32_t K_SLOT = kBlocks * KB, V_SLOT = kBlocks * VB;
   static constexpr uint32_t SMEM = kHeader + Q_BYTES + P_BYTES + NK * K_SLOT + NV * V_SLOT;
   static_assert(T_A + NS * 64 <= TCOLS, "tensor memory");
   static_assert(CTAS * (SMEM + 1024) <= 228 * 1024 && SMEM <= 232448, "shared memory");
-  // barriers
-  static constexpr int kKFull = 0, kKEmpty = NK, kVFull = 2 * NK, kVEmpty = 2 * NK + NV, kA = 2 * (NK + NV), kQ = kA + NS,
-                       kFin = kQ + 1, kBars = kFin + 1;
-  static_assert(kBars * 8 <= 256, "barriers overflow their area");
+  // barriers: ring slots, A operands written and multiplied, scores done, products done, queries, end
+  static constexpr int kKFull = 0, kKEmpty = NK, kVFull = 2 * NK, kVEmpty = 2 * NK + NV, kAFull = 2 * (NK + NV),
+                       kADone = kAFull + NS, kS = kADone + NS, kPV = kS + 2, kQ = kPV + 1, kFin = kQ + 1, kBars = kFin + 1;
+  static_assert(kBars * 8 <= 512, "barriers overflow their area");
 };
 
 __device__ __forceinline__ float ex2(float x) {
@@ -195,21 +201,59 @@ __device__ __forceinline__ void tmem_st_x8(uint32_t a, const uint32_t (&r)[8]) {
       : "memory");
 }
 
-// the compute warps' barrier, with the OR of a predicate over them
-template <int THREADS>
-__device__ __forceinline__ bool team_or(bool v) {
+// Barrier of THREADS threads with the OR of a predicate over them: id 1, the
+// compute warps; id 2, they and the MMA warp.
+template <int ID, int THREADS>
+__device__ __forceinline__ bool bar_or(bool v) {
   uint32_t r;
   asm volatile(
       "{\n"
       ".reg .pred p, q;\n"
       "setp.ne.u32 p, %1, 0;\n"
-      "bar.red.or.pred q, 1, %2, p;\n"
+      "bar.red.or.pred q, %2, %3, p;\n"
       "selp.u32 %0, 1, 0, q;\n"
       "}\n"
       : "=r"(r)
-      : "r"((uint32_t)v), "n"(THREADS)
+      : "r"((uint32_t)v), "n"(ID), "n"(THREADS)
       : "memory");
   return r != 0;
+}
+
+// 16 bytes global -> shared; cp_async_arrive: an arrival on an mbarrier when
+// the thread's copies so far have landed
+__device__ __forceinline__ void cp_async16(uint32_t dst, const uint8_t* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async_arrive(uint32_t bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void st_shared16(uint32_t dst, uint32_t v) {
+  asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(dst), "r"(v) : "memory");
+}
+
+// pairs of fp32 numbers in one operation
+__device__ __forceinline__ uint64_t pack2(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void unpack2(uint64_t v, float& a, float& b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
 }
 
 struct MaxOp { static __device__ __forceinline__ float f(float a, float b) { return fmaxf(a, b); } };
@@ -234,18 +278,18 @@ __device__ __forceinline__ float reduce_columns(float (&v)[HC]) {
   return v[0];
 }
 
-// shared memory: barriers (0..255), then these
+// shared memory: barriers (0..511), then these
 struct Shared {
-  alignas(16) float nm[64];                      // -reference of each row (-inf: not a row)
+  alignas(16) float nm[128];                     // -reference of each row (-inf: not a row)
   float red[16][32];                             // per-warp column results
-  float inv[64];
-  uint64_t anc[64];
-  int dep[64];
+  float inv[128];
+  uint64_t anc[128];
+  int dep[128];
   uint32_t none[4];                              // rows of a group without a reference yet
   uint32_t tmem;
   int abort_flag;
 };
-static_assert(256 + sizeof(Shared) <= kHeader, "header");
+static_assert(512 + sizeof(Shared) <= kHeader, "header");
 
 // mbar_sleep_wait with the polling loop out of line: the many waits would
 // otherwise fill the instruction cache
@@ -263,7 +307,7 @@ tv_attn_kv4_kernel(const __grid_constant__ AttnParams p, const __grid_constant__
   constexpr int CPT = C::CPT, NS = C::NS, HC = C::HC;
   constexpr unsigned kAll = 0xffffffffu;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
-  Shared& sh = *reinterpret_cast<Shared*>(smem_raw + 256);
+  Shared& sh = *reinterpret_cast<Shared*>(smem_raw + 512);
   uint8_t* sQ = smem_raw + kHeader;
   uint8_t* sP = sQ + C::Q_BYTES;
   uint8_t* sK = sP + C::P_BYTES;
@@ -280,7 +324,11 @@ tv_attn_kv4_kernel(const __grid_constant__ AttnParams p, const __grid_constant__
     return;
   }
   if (tid == 0) {
-    for (int i = 0; i < C::kBars; ++i) mbar_init(bar(i), 1);
+    for (int i = 0; i < C::kBars; ++i) {
+      const bool by_warp = (i >= C::kKEmpty && i < C::kVFull) || (i >= C::kVEmpty && i < C::kADone);
+      const bool by_lane = i < C::kKEmpty || (i >= C::kVFull && i < C::kVEmpty);
+      mbar_init(bar(i), by_lane ? 32 : (by_warp ? C::kWarps : 1));   // the copying lanes, the compute warps, or one
+    }
     *abort_flag = 0;
     fence_barrier_init();
   }
@@ -297,7 +345,7 @@ tv_attn_kv4_kernel(const __grid_constant__ AttnParams p, const __grid_constant__
     tmem_alloc(smem_u32(&sh.tmem), C::TCOLS);
     tmem_relinquish();
   }
-  if (tid == C::kCompute) tma_prefetch_desc(&tm_q);
+  if (tid == C::kCompute + 32) tma_prefetch_desc(&tm_q);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -329,7 +377,7 @@ tv_attn_kv4_kernel(const __grid_constant__ AttnParams p, const __grid_constant__
 
   if (!active) {
     // nothing to do for this CTA: straight to teardown
-  } else if (warp == C::kCompute / 32) {
+  } else if (warp == C::kWarps + 1) {
     // ============================================================ loads
     if (lane == 0) {
       mbar_expect_tx(bar(C::kQ), (uint32_t)p.rows_per_tile * 128u * (D / 64));
@@ -338,60 +386,37 @@ tv_attn_kv4_kernel(const __grid_constant__ AttnParams p, const __grid_constant__
     }
     const uint8_t* k4 = reinterpret_cast<const uint8_t*>(p.k_cache);
     const uint8_t* v4 = reinterpret_cast<const uint8_t*>(p.v_cache);
-    // Block of lane l: block l % 8 of tile 4 q + l / 8.  ids(q) are page ids
-    // (or, contiguous, block numbers), kNone where nothing is loaded (past the
-    // end, or seen by no row); they are read four tiles before their use and
-    // nothing looks at them until then.
+    // Four lanes copy one block, 16 bytes a lane and instruction, addresses at
+    // constant offsets: a bulk copy per block cost more instructions (one
+    // lane's operands at a time) than the copies of all lanes together.
+    const int blk_of_lane = lane >> 2;
+    // ids(t): page id of the lane's block of tile t (or, contiguous, the block
+    // number), kNone where nothing is loaded (past the end, or seen by no
+    // row), read two tiles before its use
     constexpr int kNone = INT_MIN;
-    auto ids = [&](int q) -> int {
-      const int t = 4 * q + (lane >> 3), off = (lane & 7) * kPageSize;
+    auto ids = [&](int t) -> int {
+      const int off = blk_of_lane * kPageSize;
       if (t >= npt || (t == npt - 1 && off >= tail)) return kNone;
       const int64_t pos = tile_pos(t) + off;
       if (WIN && pos >= p.sinks && pos + kPageSize <= first_pos) return kNone;
       const int64_t blk = pos / kPageSize;
       return p.paged ? p.page_table[(int64_t)b * p.max_pages + blk] : (int)blk;
     };
-    // one tile's blocks (lane l: block l % 8, its index, -1 none, -2 a bad page) into a ring slot
-    auto load = [&](uint8_t* slot, uint32_t full, const uint8_t* src, uint32_t bytes, int64_t blk) {
-      if (__any_sync(kAll, blk == -2)) {
-        // a bad page reads as zeros
-        set_status(p.status, TV_DEV_BAD_PAGE);
-        if (blk == -2 && lane < kBlocks)
-          for (uint32_t o = 0; o < bytes; o += 16)
-            *reinterpret_cast<uint4*>(slot + lane * bytes + o) = make_uint4(0x88888888u, 0x88888888u, 0x88888888u, 0x88888888u);
-        fence_proxy_async_smem();
-        __syncwarp();
-      }
-      const uint32_t nb = (uint32_t)__popc(__ballot_sync(kAll, blk >= 0) & 0xffu);
-      const uint32_t dst = smem_u32(slot);
-      if (!p.paged && !WIN) {
-        // contiguous: the tile's blocks are adjacent
-        const int64_t b0 = __shfl_sync(kAll, blk, 0);
-        if (elect_one()) {
-          mbar_expect_tx(full, nb * bytes);
-          bulk_load(dst, src + b0 * bytes, nb * bytes, full);
-        }
-      } else {
-        if (elect_one()) mbar_expect_tx(full, nb * bytes);
-        __syncwarp();
-#pragma unroll
-        for (int q = 0; q < kBlocks; ++q) {
-          const int64_t bq = __shfl_sync(kAll, blk, q);
-          if (bq >= 0 && elect_one()) bulk_load(dst + q * bytes, src + bq * bytes, bytes, full);
-        }
-      }
-      __syncwarp();
+    const uint32_t k_dst = smem_u32(sK) + blk_of_lane * C::KB + (lane & 3) * 16;
+    const uint32_t v_dst = smem_u32(sV) + blk_of_lane * C::VB + (lane & 3) * 16;
+    // BYTES of a block, starting at the lane's 16
+    auto copy = [&](uint32_t dst, const uint8_t* src, auto bytes) {
+      constexpr int kChunks = decltype(bytes)::value / 16;
+#pragma unroll 17
+      for (int i = 0; i < kChunks / 4; ++i) cp_async16(dst + i * 64, src + i * 64);
+      if (kChunks % 4 > (lane & 3)) cp_async16(dst + kChunks / 4 * 64, src + kChunks / 4 * 64);
     };
-    int next = ids(0), cur = kNone, ks = 0, vs = 0, kp = 1, vp = 1, loaded = 0;
+    int id0 = ids(0), id1 = ids(1), ks = 0, vs = 0, kp = 1, vp = 1;
     bool ok = true;
     for (int t = 0; t < npt; ++t) {
-      if ((t & 3) == 0) {
-        cur = next;
-        next = ids((t >> 2) + 1);
-      }
-      if (t >= C::NK) ok = wait_on(bar(C::kKEmpty + ks), kp, abort_flag);
-      if (!__all_sync(kAll, ok)) break;
-      const int raw = __shfl_sync(kAll, cur, (t & 3) * 8 + (lane & 7));
+      const int raw = id0;
+      id0 = id1;
+      id1 = ids(t + 2);
       int64_t blk = -1;
       if (raw != kNone) {
         if (!p.paged)
@@ -399,17 +424,25 @@ tv_attn_kv4_kernel(const __grid_constant__ AttnParams p, const __grid_constant__
         else
           blk = raw >= 0 && raw < p.num_pages ? (int64_t)raw * p.Hkv + g : -2;
       }
-      load(sK + ks * C::K_SLOT, bar(C::kKFull + ks), k4, C::KB, blk);
-      if (t >= C::NV) ok = wait_on(bar(C::kVEmpty + vs), vp, abort_flag);
-      if (!__all_sync(kAll, ok)) {
-        if (lane == 0) {                           // K of this tile is on its way: wait for it here
-          int spare = 0;
-          wait_on(bar(C::kKFull + ks), (t / C::NK) & 1, &spare);
+      // a bad page is flagged and reads as zeros
+      if (blk == -2) set_status(p.status, TV_DEV_BAD_PAGE);
+      auto put = [&](uint32_t dst, const uint8_t* src, auto bytes, uint32_t full) {
+        if (blk >= 0) {
+          copy(dst, src + blk * decltype(bytes)::value + (lane & 3) * 16, bytes);
+          cp_async_arrive(full);
+          return;
         }
-        break;
-      }
-      load(sV + vs * C::V_SLOT, bar(C::kVFull + vs), v4, C::VB, blk);
-      loaded = t + 1;
+        if (blk == -2)
+          for (uint32_t o = 0; o + (lane & 3) * 16 < (uint32_t)decltype(bytes)::value; o += 64) st_shared16(dst + o, 0x88888888u);
+        mbar_arrive(full);
+      };
+      // (K of this tile never waits for V of the one before: the compute warps take it first)
+      if (t >= C::NK) ok = wait_on(bar(C::kKEmpty + ks), kp, abort_flag);
+      if (!__all_sync(kAll, ok)) break;
+      put(k_dst + ks * C::K_SLOT, k4, std::integral_constant<int, C::KB>(), bar(C::kKFull + ks));
+      if (t >= C::NV) ok = wait_on(bar(C::kVEmpty + vs), vp, abort_flag);
+      if (!__all_sync(kAll, ok)) break;
+      put(v_dst + vs * C::V_SLOT, v4, std::integral_constant<int, C::VB>(), bar(C::kVFull + vs));
       if (++ks == C::NK) {
         ks = 0;
         kp ^= 1;
@@ -420,11 +453,69 @@ tv_attn_kv4_kernel(const __grid_constant__ AttnParams p, const __grid_constant__
       }
     }
     // every copy this warp started has landed before the CTA exits
+    asm volatile("cp.async.wait_all;" ::: "memory");
     if (lane == 0) {
       int spare = 0;
       wait_on(bar(C::kQ), 0, &spare);
-      for (int i = max(0, loaded - C::NK); i < loaded; ++i) wait_on(bar(C::kKFull + i % C::NK), (i / C::NK) & 1, &spare);
-      for (int i = max(0, loaded - C::NV); i < loaded; ++i) wait_on(bar(C::kVFull + i % C::NV), (i / C::NV) & 1, &spare);
+    }
+    __syncwarp();
+  } else if (warp == C::kWarps) {
+    // ============================================================ MMA issue
+    constexpr uint32_t ID_QK = idesc_bf16_f32(128, N, 0, 0), ID_PV = idesc_bf16_f32(128, N, 0, 1);
+    const uint64_t q_desc = smem_desc(smem_u32(sQ), 16, 1024, 2);
+    const uint64_t p_desc = smem_desc(smem_u32(sP), C::P_BOX, 8 * C::P_PITCH, C::P_SWIZZLE);
+    bool ok = __all_sync(kAll, wait_on(bar(C::kQ), 0, abort_flag));
+    uint32_t slot = 0, par = 0;                              // next A operand and its phase
+    auto operand = [&]() {
+      ok = __all_sync(kAll, wait_on(bar(C::kAFull + slot), par, abort_flag)) && ok;
+      tc_fence_after();
+    };
+    auto advance = [&]() {
+      if (++slot == NS) {
+        slot = 0;
+        par ^= 1;
+      }
+    };
+    auto scores_of = [&](int t) {
+      const uint32_t buf = C::PIPE ? (uint32_t)t & 1u : 0u;
+#pragma unroll 1
+      for (int c = 0; c < CPT; ++c) {
+        operand();
+        if (elect_one()) {
+          mma8_ts<2, N * 8>(tmem + C::T_S + buf * N, tmem + C::T_A + slot * 64, q_desc + (uint32_t)c * (2 * N * 8), ID_QK,
+                            c > 0 ? 1u : 0u);
+          mma_commit(bar(C::kADone + slot));
+          if (c == CPT - 1) mma_commit(bar(C::kS + buf));
+        }
+        __syncwarp();
+        advance();
+      }
+    };
+    scores_of(0);
+    for (int t = 0; t < T; ++t) {
+      if (C::PIPE && t + 1 < T) scores_of(t + 1);
+      if (bar_or<2, C::kCompute + 32>(!ok)) {                // the tile's weights are in P, or (rare) need another pass
+        if (bar_or<2, C::kCompute + 32>(!ok)) break;
+        bar_or<2, C::kCompute + 32>(false);
+      }
+#pragma unroll 1
+      for (int c = 0; c < CPT; ++c) {
+        operand();
+        if (elect_one()) {
+          mma8_ts<C::P_PITCH, 4 * C::P_PITCH>(tmem + C::T_O + c * N, tmem + C::T_A + slot * 64, p_desc, ID_PV, t > 0 ? 1u : 0u);
+          mma_commit(bar(C::kADone + slot));
+          if (c == CPT - 1) mma_commit(bar(C::kPV));
+        }
+        __syncwarp();
+        advance();
+      }
+      if (!C::PIPE && t + 1 < T) scores_of(t + 1);
+    }
+    if (elect_one()) {
+      // every MMA this thread issued has finished before tensor memory is freed
+      int spare = 0;
+      mma_commit(bar(C::kFin));
+      wait_on(bar(C::kFin), 0, &spare);
     }
     __syncwarp();
   } else {
@@ -435,9 +526,6 @@ tv_attn_kv4_kernel(const __grid_constant__ AttnParams p, const __grid_constant__
     const float c2 = p.scale_log2;
     const int c0 = grp * HC, live = max(0, min(HC, nlive - c0));   // this group's softmax columns
     float* nm = sh.nm + c0;
-    constexpr uint32_t ID_QK = idesc_bf16_f32(128, N, 0, 0), ID_PV = idesc_bf16_f32(128, N, 0, 1);
-    const uint64_t q_desc = smem_desc(smem_u32(sQ), 16, 1024, 2);
-    const uint64_t p_desc = smem_desc(smem_u32(sP), 16, 8 * C::P_PITCH, C::P_SWIZZLE);
 
     if (c0 < N && row < HC) {
       const int m = m0 + c0 + row;
@@ -449,35 +537,52 @@ tv_attn_kv4_kernel(const __grid_constant__ AttnParams p, const __grid_constant__
       nm[row] = ok ? 0.f : -INFINITY;
     }
     if (row == 0) sh.none[grp] = live == 32 ? 0xffffffffu : (1u << live) - 1u;
-    float l[HC];
+    uint64_t l2[HC / 2];
 #pragma unroll
-    for (int j = 0; j < HC; ++j) l[j] = 0.f;
+    for (int j = 0; j < HC / 2; ++j) l2[j] = 0ull;
 
     const PairBits pair;
-    int item = 0, ks = 0, vs = 0, kp = 0, vp = 0;
-    bool good = true;
-    // the A operand of the next item is free once the MMAs of the item NS before are done
-    auto slot_ready = [&]() -> bool {
-      return item < NS || wait_on(bar(C::kA + item % NS), (item / NS - 1) & 1, abort_flag);
+    constexpr int H = 4 / C::GPT;                                  // 16-column pieces of an A operand per group
+    // this lane's bytes of a ring slot: K, row = key; V, row = channel
+    const uint8_t* k_lane = sK + (row >> 4) * C::KB + kv4::k_code(grp * H, row & 15);
+    const uint8_t* k_scale_lane = sK + (row >> 4) * C::KB + kv4::k_scale(D, grp * H, row & 15);
+    const uint8_t* v_lane = sV + kv4::v_code(row) + 2 * grp * H * C::VB;
+    const uint8_t* v_scale_lane = sV + (row >> 4) * C::VB + kv4::v_scale(D, row & 15);
+    uint8_t* prow = sP + (c0 / C::P_COLS) * C::P_BOX + row * C::P_PITCH;
+    const uint32_t swz = C::P_COLS == 64 ? (uint32_t)(row & 7) : (C::P_COLS == 32 ? (uint32_t)(row >> 1) & 3u : (uint32_t)(row >> 2) & 1u);
+
+    int ks = 0, vs = 0, kp = 0, vp = 0;
+    uint32_t slot = 0, par = 1;                                    // next A operand; its phase before (1: never used)
+    bool ok = true, good = true, used = false;
+    auto slot_ready = [&]() {                                      // the MMAs of the operand NS before are done
+      if (used) ok = wait_on(bar(C::kADone + slot), par, abort_flag) && ok;
+      __syncwarp();
+      tc_fence_after();
     };
-    for (int t = 0; t < T; ++t) {
+    auto slot_written = [&]() {
+      tmem_wait_st();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(C::kAFull + slot));
+      if (++slot == NS) {
+        slot = 0;
+        par ^= 1;
+        used = true;
+      }
+    };
+    auto expand_k = [&](int t) {
       const bool tree = t == npt;
-      bool ok = true;
-      // ---- S^T = K Q^T, 128 channels at a time
-      if (!tree) ok = wait_on(bar(C::kKFull + ks), kp, abort_flag);
+      if (!tree) ok = wait_on(bar(C::kKFull + ks), kp, abort_flag) && ok;
 #pragma unroll 1
-      for (int c = 0; c < CPT; ++c, ++item) {
-        ok = slot_ready() && ok;
-        __syncwarp();
-        tc_fence_after();
-        const uint32_t dst = a_base + (item % NS) * 64;
+      for (int c = 0; c < CPT; ++c) {
+        slot_ready();
+        const uint32_t dst = a_base + slot * 64 + grp * H * 16;
         if (!tree) {
           // lane = key: groups of 32 channels, 16 bytes and a scale each
-          const uint8_t* blk = sK + ks * C::K_SLOT + (row >> 4) * C::KB;
-          const uint8_t* code = blk + kv4::k_code(4 * c, row & 15);
-          const uint8_t* scale = blk + kv4::k_scale(D, 4 * c, row & 15);
+          const uint8_t* code = k_lane + ks * C::K_SLOT + c * 1024;
+          const uint8_t* scale = k_scale_lane + ks * C::K_SLOT + c * 64;
 #pragma unroll 1
-          for (int h = grp * (4 / C::GPT); h < (grp + 1) * (4 / C::GPT); ++h) {
+          for (int h = 0; h < H; ++h) {
             const uint4 w4 = *reinterpret_cast<const uint4*>(code + h * 256);
             const uint32_t s2 = (((uint32_t)scale[h * 16] << 4) + 0x3800u) * 0x00010001u;   // the scale as a bf16 pair
             const uint32_t o2 = fma_bf16x2(s2, kMinus136, kZero);
@@ -487,13 +592,16 @@ tv_attn_kv4_kernel(const __grid_constant__ AttnParams p, const __grid_constant__
             for (int e = 0; e < 16; ++e) r[e] = fma_bf16x2(pair(w[e >> 2], e & 3), s2, o2);
             tmem_st16(dst + 16 * h, r);
           }
+          if (c == CPT - 1) {
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(C::kKEmpty + ks));
+          }
         } else {
           // the tree's keys, rows of k_tree; rows past the tree are zeros
           const uint4* src = reinterpret_cast<const uint4*>(reinterpret_cast<const __nv_bfloat16*>(p.k_tree) +
-                                                            ((int64_t)g * p.R + o0 + row) * D + c * 128);
+                                                            ((int64_t)g * p.R + o0 + row) * D + c * 128) + 4 * grp * H;
 #pragma unroll 1
-          for (int i = 0; i < 4 / C::GPT; ++i) {
-            const int h = grp * (4 / C::GPT) + i;
+          for (int h = 0; h < H; ++h) {
             uint32_t r[16];
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
@@ -506,229 +614,222 @@ tv_attn_kv4_kernel(const __grid_constant__ AttnParams p, const __grid_constant__
             tmem_st16(dst + 16 * h, r);
           }
         }
-        tmem_wait_st();
-        tc_fence_before();
-        if (team_or<C::kCompute>(!ok)) { good = false; break; }
-        if (warp == 0) {
-          if (t == 0 && c == 0) wait_on(bar(C::kQ), 0, abort_flag);   // (on a timeout: noticed below)
-          tc_fence_after();
-          if (elect_one()) {
-            mma8_ts<2, N * 8>(tmem + C::T_S, tmem + C::T_A + (item % NS) * 64, q_desc + (uint32_t)c * (2 * N * 8), ID_QK,
-                              c > 0 ? 1u : 0u);
-            mma_commit(bar(C::kA + item % NS));
-            if (c == CPT - 1 && !tree) mbar_arrive(bar(C::kKEmpty + ks));
-          }
-          __syncwarp();
-        }
+        slot_written();
       }
-      if (!good) break;
-      const int last_k = item - 1;
-
-      // ---- V^T, 128 channels at a time; the first chunk is expanded while the scores are computed
-      if (!tree) ok = wait_on(bar(C::kVFull + vs), vp, abort_flag);
-      float sv = 1.f;                                              // V scale of the thread's key
-#pragma unroll 1
-      for (int c = 0; c < CPT; ++c, ++item) {
-        ok = slot_ready() && ok;
-        __syncwarp();
-        tc_fence_after();
-        const uint32_t dst = a_base + (item % NS) * 64;
-        if (!tree) {
-          // lane = channel: 8 bytes (16 keys) of each block
-          const uint8_t* src = sV + vs * C::V_SLOT + kv4::v_code(c * 128 + row);
-#pragma unroll 1
-          for (int h = grp * (4 / C::GPT); h < (grp + 1) * (4 / C::GPT); ++h) {
-            const uint2 x = *reinterpret_cast<const uint2*>(src + (2 * h) * C::VB);
-            const uint2 y = *reinterpret_cast<const uint2*>(src + (2 * h + 1) * C::VB);
-            const uint32_t w[4] = {x.x, x.y, y.x, y.y};
-            uint32_t r[16];
-#pragma unroll
-            for (int e = 0; e < 16; ++e) r[e] = fma_bf16x2(pair(w[e >> 2], e & 3), kOne, kMinus136);
-            tmem_st16(dst + 16 * h, r);
-          }
-          if (c == 0) sv = kv4::scale_of(sV[vs * C::V_SLOT + (row >> 4) * C::VB + kv4::v_scale(D, row & 15)]);
-        } else {
-          // the tree's values: channel `row` of every node, node pairs; zeros past the tree
-          const uint16_t* src = reinterpret_cast<const uint16_t*>(p.v_tree) + ((int64_t)g * p.R + o0) * D + c * 128 + row;
-#pragma unroll 1
-          for (int i = 0; i < 4 / C::GPT; ++i) {
-            const int h = grp * (4 / C::GPT) + i;
-            uint32_t r[16];
-#pragma unroll
-            for (int e = 0; e < 16; ++e) {
-              const int node = 32 * h + 2 * e;
-              const uint32_t lo = node < n ? __ldg(src + (int64_t)node * D) : 0u;
-              const uint32_t hi = node + 1 < n ? __ldg(src + (int64_t)(node + 1) * D) : 0u;
-              r[e] = lo | (hi << 16);
-            }
-            tmem_st16(dst + 16 * h, r);
-          }
-        }
-        if (c == 0) {
-          // ---- the softmax of the tile
-          ok = wait_on(bar(C::kA + last_k % NS), (last_k / NS) & 1, abort_flag) && ok;
-          __syncwarp();
-          tc_fence_after();
-          float s[HC];
-          auto scores = [&]() {                                    // the masked scores, from tensor memory
-            {
-              uint32_t r[HC];
-              ld_cols(tmem + lane_base + C::T_S + c0, r);
-#pragma unroll
-              for (int j = 0; j < HC; ++j) s[j] = __uint_as_float(r[j]);
-            }
-            if (tree) {
-              const int kd = WIN && row < n ? p.depth[o0 + row] : 0;
-#pragma unroll
-              for (int j = 0; j < HC; ++j) {
-                bool vis = row < kMaxNodes && ((sh.anc[c0 + j] >> (row & 63)) & 1ull);
-                if (WIN) vis = vis && (P + kd < p.sinks || sh.dep[c0 + j] - (int64_t)kd < p.window);
-                if (!vis) s[j] = -INFINITY;
-              }
-              return;
-            }
-            if (WIN) {
-              const int64_t p0 = tile_pos(t), pos = p0 + row;
-              if (p0 < P + kMaxNodes - p.window) {
-#pragma unroll
-                for (int j = 0; j < HC; ++j)
-                  if (!(pos < p.sinks || pos >= first_pos + sh.dep[c0 + j])) s[j] = -INFINITY;
-              }
-            }
-            if (t == npt - 1 && row >= tail) {
-#pragma unroll
-              for (int j = 0; j < HC; ++j) s[j] = -INFINITY;
-            }
-          };
-          if (c0 < N) scores();
-          const bool by_row = tree || (WIN && tile_pos(t) < P + kMaxNodes - p.window);
-          if (t == 0 && !by_row) {
-            // every row sees key 0: its scores are the references
-            if (row == 0 && c0 < N) {
-#pragma unroll
-              for (int j = 0; j < HC; ++j)
-                if (j < live) nm[j] = -s[j] * c2;
-              sh.none[grp] = 0;
-            }
-            team_or<C::kCompute>(false);
-          }
-          // weights into the P tile (key rows of 2 N bytes, swizzled) and, kept for the sums, in s
-          auto weights = [&]() -> float {
-            float xm = -INFINITY;
-            uint8_t* prow = sP + row * C::P_PITCH;
-            const uint32_t swz = N == 64 ? (uint32_t)(row & 7) : (N == 32 ? (uint32_t)(row >> 1) & 3u : (uint32_t)(row >> 2) & 1u);
-#pragma unroll
-            for (int j8 = 0; j8 < HC / 8; ++j8) {
-              const float4 na = reinterpret_cast<const float4*>(nm)[2 * j8], nb = reinterpret_cast<const float4*>(nm)[2 * j8 + 1];
-              const float nn[8] = {na.x, na.y, na.z, na.w, nb.x, nb.y, nb.z, nb.w};
-              uint32_t w[4];
-#pragma unroll
-              for (int e = 0; e < 8; ++e) {
-                const float x = fmaf(s[8 * j8 + e], c2, nn[e]);
-                xm = fmaxf(xm, x);
-                s[8 * j8 + e] = ex2(x);
-              }
-#pragma unroll
-              for (int e = 0; e < 4; ++e) w[e] = pack_bf16(s[8 * j8 + 2 * e] * sv, s[8 * j8 + 2 * e + 1] * sv);
-              *reinterpret_cast<uint4*>(prow + (((uint32_t)(c0 / 8 + j8) ^ swz) * 16)) = make_uint4(w[0], w[1], w[2], w[3]);
-            }
-            return xm;
-          };
-          float xm = -INFINITY;
-          if (c0 < N) xm = weights();
-          fence_proxy_async_smem();
-          tmem_wait_st();
-          tc_fence_before();
-          if (__builtin_expect(team_or<C::kCompute>(!ok || xm > kHeadroom || (c0 < N && sh.none[grp] != 0)), 0)) {
-            // a wait gave up, a score is far above its reference, or a row has
-            // none yet: move the references to the columns' maxima (O holds
-            // the finished products of every earlier tile) and start again
-            if (team_or<C::kCompute>(!ok)) { good = false; break; }
-            tc_fence_after();
-            if (c0 < N) {
-              scores();
-#pragma unroll
-              for (int j = 0; j < HC; ++j) s[j] = fmaf(s[j], c2, nm[j]);
-              const float top = reduce_columns<MaxOp>(s);
-              if (lane < HC) sh.red[warp][lane] = top;
-            }
-            const uint32_t none = sh.none[grp];
-            team_or<C::kCompute>(false);
-            if (c0 < N) {
-              const int j0 = lane & (HC - 1);
-              const bool fresh = (none >> j0) & 1u;                // no reference, weights or sum yet
-              const float mx = fmaxf(fmaxf(sh.red[4 * grp][j0], sh.red[4 * grp + 1][j0]),
-                                     fmaxf(sh.red[4 * grp + 2][j0], sh.red[4 * grp + 3][j0]));
-              const bool moves = lane < live && mx != -INFINITY && (fresh || mx > 0.f);
-              const float d = moves ? mx : 0.f, alpha = moves && !fresh ? ex2(-d) : 1.f;
-              const uint32_t found = __ballot_sync(kAll, lane < live && mx != -INFINITY);
-#pragma unroll
-              for (int j = 0; j < HC; ++j) l[j] *= __shfl_sync(kAll, alpha, j);
-              if (t > 0 && __any_sync(kAll, alpha != 1.f)) {
-#pragma unroll 1
-                for (int q = 0; q < CPT * (HC / 8); ++q) {
-                  const int cc = q / (HC / 8), j8 = q % (HC / 8) * 8;
-                  const uint32_t at = tmem + lane_base + C::T_O + cc * N + c0 + j8;
-                  uint32_t r[8];
-                  tmem_ld_x8(at, r);
-#pragma unroll
-                  for (int j = 0; j < 8; ++j)
-                    r[j] = __float_as_uint(__uint_as_float(r[j]) * __shfl_sync(kAll, alpha, j8 + j));
-                  tmem_st_x8(at, r);
-                }
-              }
-              if ((warp & 3) == 0) {
-                if (lane < HC) nm[lane] -= d;
-                if (lane == 0) sh.none[grp] = none & ~found;
-              }
-            }
-            team_or<C::kCompute>(false);
-            if (c0 < N) {
-              scores();
-              weights();
-            }
-            fence_proxy_async_smem();
-            tc_fence_before();
-            team_or<C::kCompute>(false);
-          }
-#pragma unroll
-          for (int j = 0; j < HC; ++j) l[j] += s[j];
-        } else {
-          tmem_wait_st();
-          tc_fence_before();
-          if (team_or<C::kCompute>(!ok)) { good = false; break; }
-        }
-        if (warp == 0) {
-          tc_fence_after();
-          if (elect_one()) {
-            mma8_ts<2 * N, 8 * N>(tmem + C::T_O + c * N, tmem + C::T_A + (item % NS) * 64, p_desc, ID_PV, t > 0 ? 1u : 0u);
-            mma_commit(bar(C::kA + item % NS));
-            if (c == CPT - 1 && !tree) mbar_arrive(bar(C::kVEmpty + vs));
-          }
-          __syncwarp();
-        }
-      }
-      if (!good) break;
-      if (++ks == C::NK) {
+      if (!tree && ++ks == C::NK) {
         ks = 0;
         kp ^= 1;
       }
-      if (++vs == C::NV) {
+    };
+    auto expand_v = [&](int t, int c) {
+      const bool tree = t == npt;
+      if (!tree && c == 0) ok = wait_on(bar(C::kVFull + vs), vp, abort_flag) && ok;
+      slot_ready();
+      const uint32_t dst = a_base + slot * 64 + grp * H * 16;
+      if (!tree) {
+        // lane = channel: 8 bytes (16 keys) of each block
+        const uint8_t* src = v_lane + vs * C::V_SLOT + c * 1024;
+#pragma unroll 1
+        for (int h = 0; h < H; ++h) {
+          const uint2 x = *reinterpret_cast<const uint2*>(src + (2 * h) * C::VB);
+          const uint2 y = *reinterpret_cast<const uint2*>(src + (2 * h + 1) * C::VB);
+          const uint32_t w[4] = {x.x, x.y, y.x, y.y};
+          uint32_t r[16];
+#pragma unroll
+          for (int e = 0; e < 16; ++e) r[e] = fma_bf16x2(pair(w[e >> 2], e & 3), kOne, kMinus136);
+          tmem_st16(dst + 16 * h, r);
+        }
+        if (c == CPT - 1) {
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(C::kVEmpty + vs));
+        }
+      } else {
+        // the tree's values: channel `row` of every node, node pairs; zeros past the tree
+        const uint16_t* src = reinterpret_cast<const uint16_t*>(p.v_tree) + ((int64_t)g * p.R + o0) * D + c * 128 + row;
+#pragma unroll 1
+        for (int h = 0; h < H; ++h) {
+          uint32_t r[16];
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            const int node = 32 * (grp * H + h) + 2 * e;
+            const uint32_t lo = node < n ? __ldg(src + (int64_t)node * D) : 0u;
+            const uint32_t hi = node + 1 < n ? __ldg(src + (int64_t)(node + 1) * D) : 0u;
+            r[e] = lo | (hi << 16);
+          }
+          tmem_st16(dst + 16 * h, r);
+        }
+      }
+      slot_written();
+    };
+
+    expand_k(0);
+    for (int t = 0; t < T; ++t) {
+      const bool tree = t == npt;
+      if (C::PIPE && t + 1 < T) expand_k(t + 1);
+      if (!C::PIPE) expand_v(t, 0);                                // beside the scores' product
+      // ---- the softmax of the tile
+      const uint32_t buf = C::PIPE ? (uint32_t)t & 1u : 0u;
+      ok = wait_on(bar(C::kS + buf), C::PIPE ? (t >> 1) & 1 : t & 1, abort_flag) && ok;
+      float sv = 1.f;                                              // V scale of the thread's key
+      if (!tree) {
+        ok = wait_on(bar(C::kVFull + vs), vp, abort_flag) && ok;
+        sv = kv4::scale_of(v_scale_lane[vs * C::V_SLOT]);
+      }
+      if (t > 0) ok = wait_on(bar(C::kPV), (t - 1) & 1, abort_flag) && ok;   // P is free, O holds the tiles before
+      __syncwarp();
+      tc_fence_after();
+      float s[HC];
+      auto scores = [&]() {                                        // the masked scores, from tensor memory
+        {
+          uint32_t r[HC];
+          ld_cols(tmem + lane_base + C::T_S + buf * N + c0, r);
+#pragma unroll
+          for (int j = 0; j < HC; ++j) s[j] = __uint_as_float(r[j]);
+        }
+        if (__builtin_expect(tree, 0)) {
+          const int kd = WIN && row < n ? p.depth[o0 + row] : 0;
+#pragma unroll
+          for (int j = 0; j < HC; ++j) {
+            bool vis = row < kMaxNodes && ((sh.anc[c0 + j] >> (row & 63)) & 1ull);
+            if (WIN) vis = vis && (P + kd < p.sinks || sh.dep[c0 + j] - (int64_t)kd < p.window);
+            if (!vis) s[j] = -INFINITY;
+          }
+          return;
+        }
+        if (WIN) {
+          const int64_t p0 = tile_pos(t), pos = p0 + row;
+          if (p0 < P + kMaxNodes - p.window) {
+#pragma unroll
+            for (int j = 0; j < HC; ++j)
+              if (!(pos < p.sinks || pos >= first_pos + sh.dep[c0 + j])) s[j] = -INFINITY;
+          }
+        }
+        if (__builtin_expect(t == npt - 1 && row >= tail, 0)) {
+#pragma unroll
+          for (int j = 0; j < HC; ++j) s[j] = -INFINITY;
+        }
+      };
+      const bool mine = live > 0;
+      if (mine) scores();
+      const bool by_row = tree || (WIN && tile_pos(t) < P + kMaxNodes - p.window);
+      if (__builtin_expect(t == 0 && !by_row, 0)) {
+        // every row sees key 0: its scores are the references
+        if (row == 0 && mine) {
+#pragma unroll
+          for (int j = 0; j < HC; ++j)
+            if (j < live) nm[j] = -s[j] * c2;
+          sh.none[grp] = 0;
+        }
+        bar_or<1, C::kCompute>(false);
+      }
+      // weights into the P tile and, kept for the sums, in s
+      auto weights = [&]() -> float {
+        float xm = -INFINITY;
+        const uint64_t cc = pack2(c2, c2), vv = pack2(sv, sv);
+#pragma unroll
+        for (int j8 = 0; j8 < HC / 8; ++j8) {
+          const ulonglong2 na = reinterpret_cast<const ulonglong2*>(nm)[2 * j8], nb = reinterpret_cast<const ulonglong2*>(nm)[2 * j8 + 1];
+          const uint64_t nn[4] = {na.x, na.y, nb.x, nb.y};
+          uint32_t w[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            float& x = s[8 * j8 + 2 * e];
+            float& y = s[8 * j8 + 2 * e + 1];
+            unpack2(fma2(pack2(x, y), cc, nn[e]), x, y);
+            xm = fmaxf(fmaxf(xm, x), y);
+            x = ex2(x);
+            y = ex2(y);
+            float a, b2;
+            unpack2(mul2(pack2(x, y), vv), a, b2);
+            w[e] = pack_bf16(a, b2);
+          }
+          *reinterpret_cast<uint4*>(prow + (((uint32_t)((c0 % C::P_COLS) / 8 + j8) ^ swz) * 16)) = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+        return xm;
+      };
+      float xm = -INFINITY;
+      if (mine) xm = weights();
+      fence_proxy_async_smem();
+      tc_fence_before();
+      if (__builtin_expect(bar_or<2, C::kCompute + 32>(!ok || xm > kHeadroom || (mine && sh.none[grp] != 0)), 0)) {
+        // a wait gave up, a score is far above its reference, or a row has
+        // none yet: move the references to the columns' maxima (O holds the
+        // finished products of every earlier tile) and start again
+        if (bar_or<2, C::kCompute + 32>(!ok)) {
+          good = false;
+          break;
+        }
+        tc_fence_after();
+        if (mine) {
+          scores();
+#pragma unroll
+          for (int j = 0; j < HC; ++j) s[j] = fmaf(s[j], c2, nm[j]);
+          const float top = reduce_columns<MaxOp>(s);
+          if (lane < HC) sh.red[warp][lane] = top;
+        }
+        const uint32_t none = sh.none[grp];
+        bar_or<1, C::kCompute>(false);
+        if (mine) {
+          const int j0 = lane & (HC - 1);
+          const bool fresh = (none >> j0) & 1u;                    // no reference, weights or sum yet
+          const float mx = fmaxf(fmaxf(sh.red[4 * grp][j0], sh.red[4 * grp + 1][j0]),
+                                 fmaxf(sh.red[4 * grp + 2][j0], sh.red[4 * grp + 3][j0]));
+          const bool moves = lane < live && mx != -INFINITY && (fresh || mx > 0.f);
+          const float d = moves ? mx : 0.f, alpha = moves && !fresh ? ex2(-d) : 1.f;
+          const uint32_t found = __ballot_sync(kAll, lane < live && mx != -INFINITY);
+#pragma unroll
+          for (int j = 0; j < HC / 2; ++j)
+            l2[j] = mul2(l2[j], pack2(__shfl_sync(kAll, alpha, 2 * j), __shfl_sync(kAll, alpha, 2 * j + 1)));
+          if (t > 0 && __any_sync(kAll, alpha != 1.f)) {
+#pragma unroll 1
+            for (int q = 0; q < CPT * (HC / 8); ++q) {
+              const int cc = q / (HC / 8), j8 = q % (HC / 8) * 8;
+              const uint32_t at = tmem + lane_base + C::T_O + cc * N + c0 + j8;
+              uint32_t r[8];
+              tmem_ld_x8(at, r);
+#pragma unroll
+              for (int j = 0; j < 8; ++j)
+                r[j] = __float_as_uint(__uint_as_float(r[j]) * __shfl_sync(kAll, alpha, j8 + j));
+              tmem_st_x8(at, r);
+            }
+          }
+          if ((warp & 3) == 0) {
+            if (lane < HC) nm[lane] -= d;
+            if (lane == 0) sh.none[grp] = none & ~found;
+          }
+        }
+        bar_or<1, C::kCompute>(false);
+        if (mine) {
+          scores();
+          weights();
+        }
+        fence_proxy_async_smem();
+        tc_fence_before();
+        bar_or<2, C::kCompute + 32>(false);
+      }
+#pragma unroll
+      for (int j = 0; j < HC / 2; ++j) l2[j] = add2(l2[j], pack2(s[2 * j], s[2 * j + 1]));
+      // ---- V^T, 128 channels at a time
+#pragma unroll 1
+      for (int c = C::PIPE ? 0 : 1; c < CPT; ++c) expand_v(t, c);
+      if (!tree && ++vs == C::NV) {
         vs = 0;
         vp ^= 1;
       }
+      if (!C::PIPE && t + 1 < T) expand_k(t + 1);
     }
 
     // ---- epilogue: the sums over the keys, then the rows of O / l
     if (good) {
-      const int last = item - 1;
-      bool ok = wait_on(bar(C::kA + last % NS), (last / NS) & 1, abort_flag);
-      ok = ok && !*abort_flag;                                     // (the wait for the queries)
+      ok = wait_on(bar(C::kPV), (T - 1) & 1, abort_flag) && ok;
       __syncwarp();
       tc_fence_after();
+      float l[HC];
+#pragma unroll
+      for (int j = 0; j < HC / 2; ++j) unpack2(l2[j], l[2 * j], l[2 * j + 1]);
       const float sum = reduce_columns<SumOp>(l);
       if (lane < HC) sh.red[warp][lane] = sum;
-      good = !team_or<C::kCompute>(!ok);
+      good = !bar_or<1, C::kCompute>(!ok);
     }
     if (good) {
       const bool direct = p.out != nullptr && nch == 1;
@@ -739,7 +840,7 @@ tv_attn_kv4_kernel(const __grid_constant__ AttnParams p, const __grid_constant__
         if (!direct)
           p.ml_part[slot0 + (int64_t)row * p.splits] = make_float2(((sh.none[grp] >> row) & 1u) ? -INFINITY : -nm[row], L);
       }
-      team_or<C::kCompute>(false);
+      bar_or<1, C::kCompute>(false);
       if (live > 0) {
 #pragma unroll 1
         for (int c = 0; c < CPT; ++c) {
@@ -765,13 +866,6 @@ tv_attn_kv4_kernel(const __grid_constant__ AttnParams p, const __grid_constant__
         }
       }
     }
-    if (warp == 0 && elect_one()) {
-      // every MMA this thread issued has finished before tensor memory is freed
-      int spare = 0;
-      mma_commit(bar(C::kFin));
-      wait_on(bar(C::kFin), 0, &spare);
-    }
-    __syncwarp();
   }
 
   // ---------------------------------------------------------------- teardown
@@ -828,6 +922,9 @@ template <int D, bool WIN>
 cudaError_t launch_n(const AttnParams& p, int N, cudaStream_t s) {
   if (N == 16) return launch_t<D, 16, WIN>(p, s);
   if (N == 32) return launch_t<D, 32, WIN>(p, s);
+  if constexpr (D < 512) {
+    if (N == 128) return launch_t<D, 128, WIN>(p, s);
+  }
   return launch_t<D, 64, WIN>(p, s);
 }
 
@@ -840,19 +937,20 @@ cudaError_t launch_d(const AttnParams& p, int N, cudaStream_t s) {
 
 template <int D>
 int ctas_of(int N) {
-  return N == 16 ? Cfg<D, 16>::CTAS : (N == 32 ? Cfg<D, 32>::CTAS : Cfg<D, 64>::CTAS);
+  return N == 16 ? Cfg<D, 16>::CTAS : (N == 32 ? Cfg<D, 32>::CTAS : (N == 64 ? Cfg<D, 64>::CTAS : 1));
 }
 
 }  // namespace
 
 bool kv4_tc_supported(const tv_desc* d, int G) { return d->dtype == TV_BF16 && G <= 64; }
 
-// columns (query rows) of a tile: the smallest of 16, 32 and 64 that holds a
-// sequence's rows, or a node's group of heads
-int kv4_tc_columns(int max_nodes, int G) {
+// Columns (query rows) of a tile: the smallest of 16, 32, 64 and, up to
+// head_dim 256, 128 that holds a sequence's rows.
+int kv4_tc_columns(int max_nodes, int G, int d) {
   const int rows = max_nodes * G;
   if (rows <= 16) return 16;
-  return rows <= 32 ? 32 : 64;
+  if (rows <= 32) return 32;
+  return rows <= 64 || d == 512 ? 64 : 128;
 }
 
 int kv4_tc_ctas_per_sm(int d, int N) { return d == 128 ? ctas_of<128>(N) : (d == 256 ? ctas_of<256>(N) : ctas_of<512>(N)); }

@@ -269,7 +269,7 @@ cudaError_t launch_tree_mask(const int32_t* parents, const int32_t* offs, uint64
 bool tc_supported(const tv_desc* d, int G);
 int tc_key_tile(int d);
 bool kv4_tc_supported(const tv_desc* d, int G);   // the same for the 4-bit cache's kernel
-int kv4_tc_columns(int max_nodes, int G);         // its query-row columns per tile (16, 32, 64)
+int kv4_tc_columns(int max_nodes, int G, int d);  // its query-row columns per tile (16 .. 128)
 int kv4_tc_ctas_per_sm(int d, int columns);
 int kv4_tc_key_tile();
 int kv4_rows_tiles(const tv_desc* d, int G);      // the register kernel's 8-row tiles, 0: not applicable

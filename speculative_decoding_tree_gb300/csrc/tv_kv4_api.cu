@@ -38,7 +38,7 @@ int make_window_plan(const tv_desc* d, const tv_window* w, bool kv4, Plan* p) {
   } else if (kv4 && kv4_tc_supported(d, G)) {
     kernel = 4;
     step = key_tile = kv4_tc_key_tile();
-    const int cols = kv4_tc_columns(d->max_nodes, G);
+    const int cols = kv4_tc_columns(d->max_nodes, G, d->head_dim);
     rows_per_tile = cols / G * G;
     ctas_per_sm = kv4_tc_ctas_per_sm(d->head_dim, cols);
   }
@@ -145,7 +145,7 @@ int attention(const tv_desc* d, const tv_window* w, bool kv4, const void* q, con
   a.out = out;                                       // one-chunk sequences are finished by the split pass
   const cudaStream_t s = as_stream(stream);
   const cudaError_t e = p.pub.kernel == 5   ? launch_attn_kv4_rows(a, kv4_rows_tiles(d, p.G), s)
-                        : p.pub.kernel == 4 ? launch_attn_kv4(a, kv4_tc_columns(d->max_nodes, p.G), s)
+                        : p.pub.kernel == 4 ? launch_attn_kv4(a, kv4_tc_columns(d->max_nodes, p.G, d->head_dim), s)
                         : kv4               ? launch_attn_simt_kv4(a, d->dtype, s)
                         : p.pub.kernel == 1 ? launch_attn_tc_window(a, s)
                                             : launch_attn_simt_window(a, d->dtype, s);
