@@ -282,7 +282,7 @@ __device__ __forceinline__ float reduce_columns(float (&v)[HC]) {
 struct Shared {
   alignas(16) float nm[128];                     // -reference of each row (-inf: not a row)
   float red[16][32];                             // per-warp column results
-  float inv[128];
+  alignas(16) float inv[128];
   uint64_t anc[128];
   int dep[128];
   uint32_t none[4];                              // rows of a group without a reference yet
@@ -841,26 +841,41 @@ tv_attn_kv4_kernel(const __grid_constant__ AttnParams p, const __grid_constant__
           p.ml_part[slot0 + (int64_t)row * p.splits] = make_float2(((sh.none[grp] >> row) & 1u) ? -INFINITY : -nm[row], L);
       }
       bar_or<1, C::kCompute>(false);
-      if (live > 0) {
+      // TMEM lane = channel of the chunk: a warp stores 128 bytes of a row at a time
+      const float4* inv4 = reinterpret_cast<const float4*>(sh.inv + c0);
 #pragma unroll 1
-        for (int c = 0; c < CPT; ++c) {
-          uint32_t r[HC];
-          ld_cols(tmem + lane_base + C::T_O + c * N + c0, r);
-          const int ch = c * 128 + row;                            // TMEM lane = channel of the chunk
+      for (int c = 0; c < CPT && live > 0; ++c) {
+        uint32_t r[HC];
+        ld_cols(tmem + lane_base + C::T_O + c * N + c0, r);
+        const int ch = c * 128 + row;
+        if (!direct) {
+          float* dst = p.o_part + slot0 * D + ch;
+          const int64_t step = (int64_t)p.splits * D;
+#pragma unroll
+          for (int j = 0; j < HC; j += 4) {
+            const float4 w = inv4[j / 4];
+            const float f[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              if (j + e < live) *dst = __uint_as_float(r[j + e]) * f[e];
+              dst += step;
+            }
+          }
+        } else {
+          int node = (m0 + c0) / p.G, head = (m0 + c0) % p.G;
 #pragma unroll
           for (int j = 0; j < HC; ++j) {
             if (j < live) {
+              const int64_t e = ((int64_t)(o0 + node) * p.Hq + g * p.G + head) * D + ch;
               const float v = __uint_as_float(r[j]) * sh.inv[c0 + j];
-              if (direct) {
-                const int m = m0 + c0 + j;
-                const int64_t e = ((int64_t)(o0 + m / p.G) * p.Hq + g * p.G + m % p.G) * D + ch;
-                if (p.out_bf16)
-                  reinterpret_cast<__nv_bfloat16*>(p.out)[e] = __float2bfloat16_rn(v);
-                else
-                  reinterpret_cast<float*>(p.out)[e] = v;
-              } else {
-                p.o_part[(slot0 + (int64_t)j * p.splits) * D + ch] = v;
-              }
+              if (p.out_bf16)
+                reinterpret_cast<__nv_bfloat16*>(p.out)[e] = __float2bfloat16_rn(v);
+              else
+                reinterpret_cast<float*>(p.out)[e] = v;
+            }
+            if (++head == p.G) {
+              head = 0;
+              ++node;
             }
           }
         }
