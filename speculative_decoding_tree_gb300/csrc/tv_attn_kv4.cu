@@ -73,6 +73,8 @@ struct Cfg {
   static_assert(PIPE || CPT > 1, "the V slot is read (scales) after its first chunk is expanded");
   static constexpr int T_S = 0, T_O = N * (PIPE ? 2 : 1), T_A = T_O + CPT * N;
   static constexpr int NS = TCOLS - T_A >= 128 ? 2 : 1;     // A operands
+  // one chunk and an operand each for K and V: V is expanded before the softmax, so that its product can start at once
+  static constexpr bool V_FIRST = PIPE && CPT == 1 && NS == 2;
   static constexpr int CTAS = 512 / TCOLS;                  // per SM
   static constexpr int GPT = TCOLS / 128;                   // warp groups of 128 lanes
   static constexpr int HC = N / GPT < 16 ? 16 : N / GPT;    // rows per softmax thread
@@ -325,7 +327,7 @@ tv_attn_kv4_kernel(const __grid_constant__ AttnParams p, const __grid_constant__
   }
   if (tid == 0) {
     for (int i = 0; i < C::kBars; ++i) {
-      const bool by_warp = (i >= C::kKEmpty && i < C::kVFull) || (i >= C::kVEmpty && i < C::kADone);
+      const bool by_warp = i >= C::kAFull && i < C::kADone;
       const bool by_lane = i < C::kKEmpty || (i >= C::kVFull && i < C::kVEmpty);
       mbar_init(bar(i), by_lane ? 32 : (by_warp ? C::kWarps : 1));   // the copying lanes, the compute warps, or one
     }
@@ -466,6 +468,7 @@ tv_attn_kv4_kernel(const __grid_constant__ AttnParams p, const __grid_constant__
     const uint64_t p_desc = smem_desc(smem_u32(sP), C::P_BOX, 8 * C::P_PITCH, C::P_SWIZZLE);
     bool ok = __all_sync(kAll, wait_on(bar(C::kQ), 0, abort_flag));
     uint32_t slot = 0, par = 0;                              // next A operand and its phase
+    int ks = 0, vs = 0;                                      // ring slots: free once every compute warp has expanded them
     auto operand = [&]() {
       ok = __all_sync(kAll, wait_on(bar(C::kAFull + slot), par, abort_flag)) && ok;
       tc_fence_after();
@@ -485,11 +488,15 @@ tv_attn_kv4_kernel(const __grid_constant__ AttnParams p, const __grid_constant__
           mma8_ts<2, N * 8>(tmem + C::T_S + buf * N, tmem + C::T_A + slot * 64, q_desc + (uint32_t)c * (2 * N * 8), ID_QK,
                             c > 0 ? 1u : 0u);
           mma_commit(bar(C::kADone + slot));
-          if (c == CPT - 1) mma_commit(bar(C::kS + buf));
+          if (c == CPT - 1) {
+            mma_commit(bar(C::kS + buf));
+            if (t != npt) mbar_arrive(bar(C::kKEmpty + ks));
+          }
         }
         __syncwarp();
         advance();
       }
+      if (++ks == C::NK) ks = 0;
     };
     scores_of(0);
     for (int t = 0; t < T; ++t) {
@@ -504,11 +511,15 @@ tv_attn_kv4_kernel(const __grid_constant__ AttnParams p, const __grid_constant__
         if (elect_one()) {
           mma8_ts<C::P_PITCH, 4 * C::P_PITCH>(tmem + C::T_O + c * N, tmem + C::T_A + slot * 64, p_desc, ID_PV, t > 0 ? 1u : 0u);
           mma_commit(bar(C::kADone + slot));
-          if (c == CPT - 1) mma_commit(bar(C::kPV));
+          if (c == CPT - 1) {
+            mma_commit(bar(C::kPV));
+            if (t != npt) mbar_arrive(bar(C::kVEmpty + vs));
+          }
         }
         __syncwarp();
         advance();
       }
+      if (++vs == C::NV) vs = 0;
       if (!C::PIPE && t + 1 < T) scores_of(t + 1);
     }
     if (elect_one()) {
@@ -552,12 +563,10 @@ tv_attn_kv4_kernel(const __grid_constant__ AttnParams p, const __grid_constant__
     const uint32_t swz = C::P_COLS == 64 ? (uint32_t)(row & 7) : (C::P_COLS == 32 ? (uint32_t)(row >> 1) & 3u : (uint32_t)(row >> 2) & 1u);
 
     int ks = 0, vs = 0, kp = 0, vp = 0;
-    uint32_t slot = 0, par = 1;                                    // next A operand; its phase before (1: never used)
-    bool ok = true, good = true, used = false;
-    auto slot_ready = [&]() {                                      // the MMAs of the operand NS before are done
-      if (used) ok = wait_on(bar(C::kADone + slot), par, abort_flag) && ok;
-      __syncwarp();
-      tc_fence_after();
+    uint32_t slot = 0, par = 1;                                    // next A operand; the phase of its use before
+    bool bad = false, good = true;                                 // a wait gave up; all warps went on
+    auto wait = [&](int i, uint32_t parity) {
+      if (__builtin_expect(!mbar_try_wait_hint(bar(i), parity), 0)) bad |= !wait_long(bar(i), parity, abort_flag);
     };
     auto slot_written = [&]() {
       tmem_wait_st();
@@ -567,15 +576,20 @@ tv_attn_kv4_kernel(const __grid_constant__ AttnParams p, const __grid_constant__
       if (++slot == NS) {
         slot = 0;
         par ^= 1;
-        used = true;
       }
     };
+    // Before an A operand is written, the MMAs that read it last (NS operands
+    // before) are done.  Ahead of the scores (PIPE), K's first NS chunks follow
+    // V of two tiles back, or K of the tile before, whose products the loop has
+    // waited for; so does V where it goes first.
     auto expand_k = [&](int t) {
       const bool tree = t == npt;
-      if (!tree) ok = wait_on(bar(C::kKFull + ks), kp, abort_flag) && ok;
+      if (!tree) wait(C::kKFull + ks, kp);
 #pragma unroll 1
       for (int c = 0; c < CPT; ++c) {
-        slot_ready();
+        if (c >= NS || (!C::PIPE && t > 0)) wait(C::kADone + slot, par);
+        __syncwarp();
+        tc_fence_after();
         const uint32_t dst = a_base + slot * 64 + grp * H * 16;
         if (!tree) {
           // lane = key: groups of 32 channels, 16 bytes and a scale each
@@ -591,10 +605,6 @@ tv_attn_kv4_kernel(const __grid_constant__ AttnParams p, const __grid_constant__
 #pragma unroll
             for (int e = 0; e < 16; ++e) r[e] = fma_bf16x2(pair(w[e >> 2], e & 3), s2, o2);
             tmem_st16(dst + 16 * h, r);
-          }
-          if (c == CPT - 1) {
-            __syncwarp();
-            if (lane == 0) mbar_arrive(bar(C::kKEmpty + ks));
           }
         } else {
           // the tree's keys, rows of k_tree; rows past the tree are zeros
@@ -623,8 +633,10 @@ tv_attn_kv4_kernel(const __grid_constant__ AttnParams p, const __grid_constant__
     };
     auto expand_v = [&](int t, int c) {
       const bool tree = t == npt;
-      if (!tree && c == 0) ok = wait_on(bar(C::kVFull + vs), vp, abort_flag) && ok;
-      slot_ready();
+      if ((!C::PIPE || C::V_FIRST) && !tree && c == 0) wait(C::kVFull + vs, vp);
+      if (!C::V_FIRST) wait(C::kADone + slot, par);
+      __syncwarp();
+      tc_fence_after();
       const uint32_t dst = a_base + slot * 64 + grp * H * 16;
       if (!tree) {
         // lane = channel: 8 bytes (16 keys) of each block
@@ -638,10 +650,6 @@ tv_attn_kv4_kernel(const __grid_constant__ AttnParams p, const __grid_constant__
 #pragma unroll
           for (int e = 0; e < 16; ++e) r[e] = fma_bf16x2(pair(w[e >> 2], e & 3), kOne, kMinus136);
           tmem_st16(dst + 16 * h, r);
-        }
-        if (c == CPT - 1) {
-          __syncwarp();
-          if (lane == 0) mbar_arrive(bar(C::kVEmpty + vs));
         }
       } else {
         // the tree's values: channel `row` of every node, node pairs; zeros past the tree
@@ -665,17 +673,24 @@ tv_attn_kv4_kernel(const __grid_constant__ AttnParams p, const __grid_constant__
     expand_k(0);
     for (int t = 0; t < T; ++t) {
       const bool tree = t == npt;
-      if (C::PIPE && t + 1 < T) expand_k(t + 1);
-      if (!C::PIPE) expand_v(t, 0);                                // beside the scores' product
-      // ---- the softmax of the tile
       const uint32_t buf = C::PIPE ? (uint32_t)t & 1u : 0u;
-      ok = wait_on(bar(C::kS + buf), C::PIPE ? (t >> 1) & 1 : t & 1, abort_flag) && ok;
+      if (C::PIPE) {
+        wait(C::kS + buf, (t >> 1) & 1);
+        if (C::V_FIRST && t + 1 < T) expand_k(t + 1);
+        if (t > 0) wait(C::kPV, (t - 1) & 1);                      // P is free, O holds the tiles before
+        if (!C::V_FIRST && t + 1 < T) expand_k(t + 1);
+        if (C::V_FIRST) expand_v(t, 0);
+      } else {
+        expand_v(t, 0);                                            // beside the scores' product
+        wait(C::kS, t & 1);
+        if (t > 0) wait(C::kPV, (t - 1) & 1);
+      }
+      // ---- the softmax of the tile
       float sv = 1.f;                                              // V scale of the thread's key
       if (!tree) {
-        ok = wait_on(bar(C::kVFull + vs), vp, abort_flag) && ok;
+        if (C::PIPE && !C::V_FIRST) wait(C::kVFull + vs, vp);
         sv = kv4::scale_of(v_scale_lane[vs * C::V_SLOT]);
       }
-      if (t > 0) ok = wait_on(bar(C::kPV), (t - 1) & 1, abort_flag) && ok;   // P is free, O holds the tiles before
       __syncwarp();
       tc_fence_after();
       float s[HC];
@@ -751,11 +766,11 @@ tv_attn_kv4_kernel(const __grid_constant__ AttnParams p, const __grid_constant__
       if (mine) xm = weights();
       fence_proxy_async_smem();
       tc_fence_before();
-      if (__builtin_expect(bar_or<2, C::kCompute + 32>(!ok || xm > kHeadroom || (mine && sh.none[grp] != 0)), 0)) {
+      if (__builtin_expect(bar_or<2, C::kCompute + 32>(bad || xm > kHeadroom || (mine && sh.none[grp] != 0)), 0)) {
         // a wait gave up, a score is far above its reference, or a row has
         // none yet: move the references to the columns' maxima (O holds the
         // finished products of every earlier tile) and start again
-        if (bar_or<2, C::kCompute + 32>(!ok)) {
+        if (bar_or<2, C::kCompute + 32>(bad)) {
           good = false;
           break;
         }
@@ -811,7 +826,7 @@ tv_attn_kv4_kernel(const __grid_constant__ AttnParams p, const __grid_constant__
       for (int j = 0; j < HC / 2; ++j) l2[j] = add2(l2[j], pack2(s[2 * j], s[2 * j + 1]));
       // ---- V^T, 128 channels at a time
 #pragma unroll 1
-      for (int c = C::PIPE ? 0 : 1; c < CPT; ++c) expand_v(t, c);
+      for (int c = C::PIPE && !C::V_FIRST ? 0 : 1; c < CPT; ++c) expand_v(t, c);
       if (!tree && ++vs == C::NV) {
         vs = 0;
         vp ^= 1;
@@ -821,7 +836,7 @@ tv_attn_kv4_kernel(const __grid_constant__ AttnParams p, const __grid_constant__
 
     // ---- epilogue: the sums over the keys, then the rows of O / l
     if (good) {
-      ok = wait_on(bar(C::kPV), (T - 1) & 1, abort_flag) && ok;
+      wait(C::kPV, (T - 1) & 1);
       __syncwarp();
       tc_fence_after();
       float l[HC];
@@ -829,7 +844,7 @@ tv_attn_kv4_kernel(const __grid_constant__ AttnParams p, const __grid_constant__
       for (int j = 0; j < HC / 2; ++j) unpack2(l2[j], l[2 * j], l[2 * j + 1]);
       const float sum = reduce_columns<SumOp>(l);
       if (lane < HC) sh.red[warp][lane] = sum;
-      good = !bar_or<1, C::kCompute>(!ok);
+      good = !bar_or<1, C::kCompute>(bad);
     }
     if (good) {
       const bool direct = p.out != nullptr && nch == 1;
