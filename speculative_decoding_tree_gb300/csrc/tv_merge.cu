@@ -81,25 +81,25 @@ __global__ __launch_bounds__(kMergeThreads) void merge_slab_kernel(MergeParams p
   if (!valid && tid == 0) set_status(p.status, TV_DEV_BAD_OFFSETS);
   if (!live) return;
 
-  const int crow = min(RS, p.tile_stride - r0);     // rows gathered (inside the tile)
   const int64_t slot0 = partial_slot(0, b, g, rt, r0, p.Hkv, p.row_tiles, p.tile_stride, S);
   const PT* src = reinterpret_cast<const PT*>(p.o_part);
   const uint32_t bar_a = smem_u32(&bar);
-  // batch of splits [s0, s0 + nb) of the slab's rows into shared memory: one
-  // copy when the batch holds every split (the slab is contiguous), else one
-  // per row
+  // batch of splits [s0, s0 + nb) of the slab's live rows into shared memory:
+  // one copy when the batch holds every split of the grid (the slab is
+  // contiguous), else one per row; splits that a shorter sequence does not have
+  // are not read
   auto gather = [&](int s0, int nb) {
     if (tid == 0) {
-      mbar_expect_tx(bar_a, (uint32_t)(crow * nb * D * sizeof(PT)));
+      mbar_expect_tx(bar_a, (uint32_t)(rows * nb * D * sizeof(PT)));
       if (nb == S)
-        bulk_load(smem_u32(so), src + slot0 * D, (uint32_t)(crow * S * D * sizeof(PT)), bar_a);
+        bulk_load(smem_u32(so), src + slot0 * D, (uint32_t)(rows * S * D * sizeof(PT)), bar_a);
       else
-        for (int r = 0; r < crow; ++r)
+        for (int r = 0; r < rows; ++r)
           bulk_load(smem_u32(so + (size_t)r * SB * D), src + (slot0 + (int64_t)r * S + s0) * D,
                     (uint32_t)(nb * D * sizeof(PT)), bar_a);
     }
   };
-  gather(0, min(SB, S));
+  gather(0, min(SB, nch));
 
   constexpr int C4 = D / 4;                         // float4 columns per row
   const int items = rows * C4;
@@ -115,7 +115,7 @@ __global__ __launch_bounds__(kMergeThreads) void merge_slab_kernel(MergeParams p
   int phase = 0;
   for (int s0 = 0; s0 < nch && ok; s0 += SB, ++phase) {
     const int nb = min(SB, nch - s0);
-    if (s0 > 0) gather(s0, min(SB, S - s0));
+    if (s0 > 0) gather(s0, nb);
     for (int e = tid; e < rows * nb; e += kMergeThreads) {   // (m, l) of the batch, plain loads
       const int r = e / nb, j = e % nb;
       sml[r * SB + j] = p.ml_part[slot0 + (int64_t)r * S + s0 + j];
