@@ -1,6 +1,6 @@
 // Split-KV tree-verify attention over a 4-bit cache (tree_kv4.h) for few query
-// rows: up to 8 or 16 rows per KV head (plain decoding, short chains), bf16
-// queries and tree K/V, fp32 accumulation and softmax.
+// rows: up to 8 per KV head (plain decoding, short chains), bf16 queries and
+// tree K/V, fp32 accumulation and softmax.
 //
 // With so few rows the pass is bound by the cache's bytes, provided that the
 // expansion of the codes costs little beside it: 46 values a clock and SM
@@ -9,9 +9,10 @@
 // lanes that need them, expands a word's pairs there (mask, and one fused
 // multiply-add: see tv_attn_kv4.cu) and multiplies with mma.sync.m16n8k16,
 // whose row granularity (8 query rows) fits where a tcgen05 operand would have
-// to go through tensor memory.  tcgen05's build of the same call (128-lane
-// operands written to tensor memory, two barriers a tile) took 264 us on 64
-// sequences x 4 rows over up to 16384 keys; the floor of its bytes is 90 us.
+// to go through tensor memory.  64 sequences x 4 rows over up to 16384 keys:
+// @@ROWS us (the floor of its bytes is 90), @@TC with tcgen05's 16-column tile.  From
+// 9 rows on that tile is the faster one: 64 x 16 rows 214 us, 242 with two
+// mma.sync columns here.
 //
 //   S^T [16 keys x 8 rows]     = K  [16 keys x 16 channels]      Q^T
 //   O^T [16 channels x 8 rows] += V^T [16 channels x 16 keys]    P^T
@@ -42,6 +43,7 @@ namespace tv {
 namespace {
 
 constexpr int kSpan = 64;                        // keys per span
+constexpr int kRows = 8;                         // query rows of a KV head: an mma.sync column each
 constexpr int kWarps = 4;
 constexpr float kHeadroom = 60.0f;               // log2: a weight above 2^60 moves the reference
 
@@ -97,35 +99,34 @@ __device__ __forceinline__ uint4 ldg16(const uint8_t* p) {
 }
 __device__ __forceinline__ uint32_t word(const uint4& v, int i) { return i == 0 ? v.x : (i == 1 ? v.y : (i == 2 ? v.z : v.w)); }
 
-// head_dim D, NT tiles of 8 query rows
-template <int D, int NT>
+template <int D>
 struct Cfg {
   static constexpr int CPT = D / 128;
-  static constexpr int CTAS = D == 128 && NT == 1 ? 3 : 2;    // per SM (registers)
+  static constexpr int CTAS = D == 128 ? 3 : 2;               // per SM (registers)
   static constexpr bool QREG = D <= 256;                      // queries in registers, else in shared memory
   static constexpr int OUT_PITCH = D + 8;
-  static constexpr int SMEM = kWarps * 8 * NT * OUT_PITCH * 4 > CPT * 8 * 32 * 8 * NT ? kWarps * 8 * NT * OUT_PITCH * 4
-                                                                                     : CPT * 8 * 32 * 8 * NT;
+  static constexpr int SMEM = kWarps * 8 * OUT_PITCH * 4 > CPT * 8 * 32 * 8 ? kWarps * 8 * OUT_PITCH * 4
+                                                                                     : CPT * 8 * 32 * 8;
 };
 
-template <int D, int NT, bool WIN>
-__global__ void __launch_bounds__(32 * kWarps, Cfg<D, NT>::CTAS) tv_attn_kv4_rows_kernel(const __grid_constant__ AttnParams p) {
-  using C = Cfg<D, NT>;
+template <int D, bool WIN>
+__global__ void __launch_bounds__(32 * kWarps, Cfg<D>::CTAS) tv_attn_kv4_rows_kernel(const __grid_constant__ AttnParams p) {
+  using C = Cfg<D>;
   constexpr int CPT = C::CPT, KB = kv4::k_block_bytes(D), VB = kv4::v_block_bytes(D);
   constexpr unsigned kAll = 0xffffffffu;
   extern __shared__ __align__(16) float smem[];
-  __shared__ float s_m[kWarps][8 * NT], s_l[kWarps][8 * NT];
+  __shared__ float s_m[kWarps][8], s_l[kWarps][8];
   dep_wait();
   dep_launch();
-  const int g_head = blockIdx.y / p.splits, s_id = blockIdx.y % p.splits, b = blockIdx.z, rt = blockIdx.x;
+  const int g_head = blockIdx.y / p.splits, s_id = blockIdx.y % p.splits, b = blockIdx.z;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
   const int64_t Praw = p.prefix_len[b];
   int o0, n;
   if (!seq_rows(p.node_offsets, b, p.R, p.max_nodes, p.status, &o0, &n)) return;
-  const int m0 = rt * p.rows_per_tile, live = min(p.rows_per_tile, n * p.G - m0);
+  const int live = n * p.G;                        // rows of this sequence, kRows at most
   if (live <= 0) return;
   const int64_t P = clamp_prefix(Praw, p.max_prefix, p.capacity);
-  if (P != Praw && tid == 0 && rt == 0 && s_id == 0 && g_head == 0) set_status(p.status, TV_DEV_BAD_PREFIX);
+  if (P != Praw && tid == 0 && s_id == 0 && g_head == 0) set_status(p.status, TV_DEV_BAD_PREFIX);
   const KeyMap km = key_map(P, WIN ? p.window : 0, p.sinks, p.map_tile);
   const int nch = num_chunks(km.len, p.chunk, p.tree_tile);
   if (s_id >= nch) return;
@@ -137,34 +138,29 @@ __global__ void __launch_bounds__(32 * kWarps, Cfg<D, NT>::CTAS) tv_attn_kv4_row
   const uint8_t* k4 = reinterpret_cast<const uint8_t*>(p.k_cache);
   const uint8_t* v4 = reinterpret_cast<const uint8_t*>(p.v_cache);
 
-  // query row r of the tile: its address
-  auto q_row = [&](int r) -> const __nv_bfloat16* {
-    const int m = m0 + r;
-    return reinterpret_cast<const __nv_bfloat16*>(p.q) + ((int64_t)(o0 + m / p.G) * p.Hq + g_head * p.G + m % p.G) * D;
-  };
+  // element offset of query row r (node r / G, head r % G of the group) in q and out
+  auto row_at = [&](int r) -> int64_t { return ((int64_t)(o0 + r / p.G) * p.Hq + g_head * p.G + r % p.G) * D; };
   // Q^T fragments: k-step j of chunk c takes channels 32 t + 8 (j / 2) + 4 (j % 2) .. + 3 of row g
-  uint32_t q[C::QREG ? CPT : 1][NT][8][2];
+  uint32_t q[C::QREG ? CPT : 1][8][2];
   uint2* sq = reinterpret_cast<uint2*>(smem);
 #pragma unroll
-  for (int c = 0; c < CPT; ++c)
+  for (int c = 0; c < CPT; ++c) {
+    const uint4* src = reinterpret_cast<const uint4*>(reinterpret_cast<const __nv_bfloat16*>(p.q) +
+                                                      row_at(g < live ? g : 0) + c * 128 + 32 * t);
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-      const int r = nt * 8 + g;
-      const uint4* src = reinterpret_cast<const uint4*>(q_row(r < live ? r : 0) + c * 128 + 32 * t);
-#pragma unroll
-      for (int w = 0; w < 4; ++w) {
-        const uint4 v = r < live ? __ldg(src + w) : make_uint4(0, 0, 0, 0);
-        if (C::QREG) {
-          q[C::QREG ? c : 0][nt][2 * w][0] = v.x;
-          q[C::QREG ? c : 0][nt][2 * w][1] = v.y;
-          q[C::QREG ? c : 0][nt][2 * w + 1][0] = v.z;
-          q[C::QREG ? c : 0][nt][2 * w + 1][1] = v.w;
-        } else if (warp == 0) {
-          sq[((c * NT + nt) * 8 + 2 * w) * 32 + lane] = make_uint2(v.x, v.y);
-          sq[((c * NT + nt) * 8 + 2 * w + 1) * 32 + lane] = make_uint2(v.z, v.w);
-        }
+    for (int w = 0; w < 4; ++w) {
+      const uint4 v = g < live ? __ldg(src + w) : make_uint4(0, 0, 0, 0);
+      if (C::QREG) {
+        q[C::QREG ? c : 0][2 * w][0] = v.x;
+        q[C::QREG ? c : 0][2 * w][1] = v.y;
+        q[C::QREG ? c : 0][2 * w + 1][0] = v.z;
+        q[C::QREG ? c : 0][2 * w + 1][1] = v.w;
+      } else if (warp == 0) {
+        sq[(c * 8 + 2 * w) * 32 + lane] = make_uint2(v.x, v.y);
+        sq[(c * 8 + 2 * w + 1) * 32 + lane] = make_uint2(v.z, v.w);
       }
     }
+  }
   if (!C::QREG) __syncthreads();
 
   // The blocks a lane reads of span sp: block g / 2 (K, and the V scales of its
@@ -192,22 +188,17 @@ __global__ void __launch_bounds__(32 * kWarps, Cfg<D, NT>::CTAS) tv_attn_kv4_row
     return 0;
   };
 
-  float o[CPT][8][NT][4];
-  float nm[NT][2], l[NT][2];                       // rows 2 t, 2 t + 1 of each tile
+  float o[CPT][8][4];
+  float nm[2], l[2];                               // rows 2 t, 2 t + 1
   int refs = 0;                                    // references: 0 none yet, 1 of some rows, 2 of all
 #pragma unroll
   for (int c = 0; c < CPT; ++c)
 #pragma unroll
     for (int i = 0; i < 8; ++i)
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) o[c][i][nt][e] = 0.f;
-#pragma unroll
-  for (int nt = 0; nt < NT; ++nt) {
-    nm[nt][0] = nm[nt][1] = 0.f;
-    l[nt][0] = l[nt][1] = 0.f;
-  }
+      for (int e = 0; e < 4; ++e) o[c][i][e] = 0.f;
+  nm[0] = nm[1] = 0.f;
+  l[0] = l[1] = 0.f;
 
   // pieces of a span: K of each 128-channel chunk, then V; piece i sits in
   // buf[i & 1] and is loaded once piece i - 2 has been used
@@ -239,16 +230,13 @@ __global__ void __launch_bounds__(32 * kWarps, Cfg<D, NT>::CTAS) tv_attn_kv4_row
   };
 
   // S^T of one chunk from its expanded operand
-  float s[4][NT][4];
+  float s[4][4];
   auto qk_step = [&](int c, int j, int mt, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3) {
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-      if (C::QREG) {
-        mma(s[mt][nt], a0, a1, a2, a3, q[C::QREG ? c : 0][nt][j][0], q[C::QREG ? c : 0][nt][j][1]);
-      } else {
-        const uint2 qq = sq[((c * NT + nt) * 8 + j) * 32 + lane];
-        mma(s[mt][nt], a0, a1, a2, a3, qq.x, qq.y);
-      }
+    if (C::QREG) {
+      mma(s[mt], a0, a1, a2, a3, q[C::QREG ? c : 0][j][0], q[C::QREG ? c : 0][j][1]);
+    } else {
+      const uint2 qq = sq[(c * 8 + j) * 32 + lane];
+      mma(s[mt], a0, a1, a2, a3, qq.x, qq.y);
     }
   };
   auto qk = [&](const uint4 (&r)[8], const uint4& sc, int c) {
@@ -275,79 +263,71 @@ __global__ void __launch_bounds__(32 * kWarps, Cfg<D, NT>::CTAS) tv_attn_kv4_row
   auto key_of = [&](int mt, int h) -> int { return 16 * (g >> 1) + 2 * (2 * mt + h) + (g & 1); };
 
   // weights of the (masked) scores: sums, and the V-scaled weights as P^T fragments
-  uint32_t pb[4][NT][2];
+  uint32_t pb[4][2];
   auto softmax = [&](bool masked, const uint4& sc, bool scaled) {
-#pragma unroll
-    for (int mt = 0; mt < 4; ++mt)
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) s[mt][nt][e] *= p.scale_log2;
     if (refs == 0 && !masked) {
       // the warp's first key (lane g = 0) gives the references
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        nm[nt][0] = -__shfl_sync(kAll, s[0][nt][0], t);
-        nm[nt][1] = -__shfl_sync(kAll, s[0][nt][1], t);
-      }
+      nm[0] = -p.scale_log2 * __shfl_sync(kAll, s[0][0], t);
+      nm[1] = -p.scale_log2 * __shfl_sync(kAll, s[0][1], t);
       refs = 2;
     }
     float xm = -INFINITY;
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
+    for (int mt = 0; mt < 4; ++mt)
 #pragma unroll
-      for (int mt = 0; mt < 4; ++mt)
-        xm = fmaxf(xm, fmaxf(fmaxf(s[mt][nt][0], s[mt][nt][2]) + nm[nt][0], fmaxf(s[mt][nt][1], s[mt][nt][3]) + nm[nt][1]));
+      for (int e = 0; e < 4; ++e) {
+        s[mt][e] = fmaf(s[mt][e], p.scale_log2, nm[e & 1]);
+        xm = fmaxf(xm, s[mt][e]);
+      }
     if (refs != 2 || __any_sync(kAll, xm > kHeadroom)) {
       // move the references to the largest score so far; with masked scores a
       // row may still have none (reference 0, no weights, nothing in O)
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
+      for (int e = 0; e < 2; ++e) {
+        float mx = -INFINITY;
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          float mx = -INFINITY;
+        for (int mt = 0; mt < 4; ++mt) mx = fmaxf(mx, fmaxf(s[mt][e], s[mt][e + 2]));
 #pragma unroll
-          for (int mt = 0; mt < 4; ++mt) mx = fmaxf(mx, fmaxf(s[mt][nt][e], s[mt][nt][e + 2]));
+        for (int off = 4; off < 32; off <<= 1) mx = fmaxf(mx, __shfl_xor_sync(kAll, mx, off));
+        float sum = l[e];
 #pragma unroll
-          for (int off = 4; off < 32; off <<= 1) mx = fmaxf(mx, __shfl_xor_sync(kAll, mx, off));
-          float sum = l[nt][e];
+        for (int off = 4; off < 32; off <<= 1) sum += __shfl_xor_sync(kAll, sum, off);
+        const bool fresh = sum == 0.f;                               // no weights yet
+        const float shift = mx == -INFINITY ? 0.f : (fresh ? mx : fmaxf(mx, 0.f));
+        const float alpha = fresh ? 1.f : ex2(-shift);
+        nm[e] -= shift;
+        l[e] *= alpha;
 #pragma unroll
-          for (int off = 4; off < 32; off <<= 1) sum += __shfl_xor_sync(kAll, sum, off);
-          const bool fresh = sum == 0.f;                             // no weights yet
-          const float to = mx == -INFINITY ? nm[nt][e] : (fresh ? -mx : fminf(nm[nt][e], -mx));
-          const float alpha = fresh ? 1.f : ex2(to - nm[nt][e]);
-          nm[nt][e] = to;
-          l[nt][e] *= alpha;
-#pragma unroll
-          for (int c = 0; c < CPT; ++c)
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              o[c][i][nt][e] *= alpha;
-              o[c][i][nt][e + 2] *= alpha;
-            }
+        for (int mt = 0; mt < 4; ++mt) {
+          s[mt][e] -= shift;
+          s[mt][e + 2] -= shift;
         }
+#pragma unroll
+        for (int c = 0; c < CPT; ++c)
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            o[c][i][e] *= alpha;
+            o[c][i][e + 2] *= alpha;
+          }
+      }
       // every row has a reference once the warp has seen an unmasked span;
       // until then the next span takes this path again
       if (refs != 2) refs = masked ? 1 : 2;
     }
 #pragma unroll
     for (int mt = 0; mt < 4; ++mt) {
-      float sv[2] = {1.f, 1.f};
+      float w[4], sv[2] = {1.f, 1.f};
       if (scaled) {
 #pragma unroll
         for (int h = 0; h < 2; ++h) sv[h] = kv4::scale_of((word(sc, mt) >> (16 * h + 8 * (g & 1))) & 255u);
       }
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        float w[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          w[e] = ex2(s[mt][nt][e] + nm[nt][e & 1]);
-          l[nt][e & 1] += w[e];
-        }
-        pb[mt][nt][0] = transpose8x8(pack_bf16(w[0] * sv[0], w[1] * sv[0]));
-        pb[mt][nt][1] = transpose8x8(pack_bf16(w[2] * sv[1], w[3] * sv[1]));
+      for (int e = 0; e < 4; ++e) {
+        w[e] = ex2(s[mt][e]);
+        l[e & 1] += w[e];
       }
+      pb[mt][0] = transpose8x8(pack_bf16(w[0] * sv[0], w[1] * sv[0]));
+      pb[mt][1] = transpose8x8(pack_bf16(w[2] * sv[1], w[3] * sv[1]));
     }
   };
   auto pv = [&](const uint4 (&r)[8], int c) {
@@ -359,17 +339,14 @@ __global__ void __launch_bounds__(32 * kWarps, Cfg<D, NT>::CTAS) tv_attn_kv4_row
         const int e = 2 * (mt & 1);
         const uint32_t a0 = fma_bf16x2(pair(we, e), kOne, kMinus136), a1 = fma_bf16x2(pair(wo, e), kOne, kMinus136);
         const uint32_t a2 = fma_bf16x2(pair(we, e + 1), kOne, kMinus136), a3 = fma_bf16x2(pair(wo, e + 1), kOne, kMinus136);
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) mma(o[c][i][nt], a0, a1, a2, a3, pb[mt][nt][0], pb[mt][nt][1]);
+        mma(o[c][i], a0, a1, a2, a3, pb[mt][0], pb[mt][1]);
       }
   };
   auto clear_s = [&]() {
 #pragma unroll
     for (int mt = 0; mt < 4; ++mt)
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) s[mt][nt][e] = 0.f;
+      for (int e = 0; e < 4; ++e) s[mt][e] = 0.f;
   };
 
   // ---------------------------------------------------------------- the warp's prefix spans
@@ -411,29 +388,24 @@ __global__ void __launch_bounds__(32 * kWarps, Cfg<D, NT>::CTAS) tv_attn_kv4_row
       for (int mt = 0; mt < 4; ++mt)
 #pragma unroll
         for (int h = 0; h < 2; ++h)
-          if (v0 + key_of(mt, h) >= k_end) {
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) s[mt][nt][2 * h] = s[mt][nt][2 * h + 1] = -INFINITY;
-          }
+          if (v0 + key_of(mt, h) >= k_end) s[mt][2 * h] = s[mt][2 * h + 1] = -INFINITY;
     }
     if (WIN) {
       const int64_t p0 = km.pos(v0);
       if (p0 < P + kMaxNodes - p.window) {
         masked = true;
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
+        for (int e = 0; e < 2; ++e) {
+          const int r = 2 * t + e;
+          const int64_t lo = first_pos + (r < live ? p.depth[o0 + r / p.G] : 0);
 #pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const int r = nt * 8 + 2 * t + e;
-            const int64_t lo = first_pos + (r < live ? p.depth[o0 + (m0 + r) / p.G] : 0);
+          for (int mt = 0; mt < 4; ++mt)
 #pragma unroll
-            for (int mt = 0; mt < 4; ++mt)
-#pragma unroll
-              for (int h = 0; h < 2; ++h) {
-                const int64_t pos = p0 + key_of(mt, h);
-                if (!(pos < p.sinks || pos >= lo)) s[mt][nt][2 * h + e] = -INFINITY;
-              }
-          }
+            for (int h = 0; h < 2; ++h) {
+              const int64_t pos = p0 + key_of(mt, h);
+              if (!(pos < p.sinks || pos >= lo)) s[mt][2 * h + e] = -INFINITY;
+            }
+        }
       }
     }
     softmax(masked, vsc, true);
@@ -457,7 +429,7 @@ __global__ void __launch_bounds__(32 * kWarps, Cfg<D, NT>::CTAS) tv_attn_kv4_row
   }
 
   // ---------------------------------------------------------------- the tree
-  // (at most 16 nodes here: rows <= 16), as one span of bf16 rows in the same
+  // (at most 8 nodes: rows <= 8), as one span of bf16 rows in the same
   // layout: nodes sit in block 0, lanes g < 2 (K) and t = 0 (V)
   if (nsp < total && warp == nsp % kWarps) {
     clear_s();
@@ -485,36 +457,32 @@ __global__ void __launch_bounds__(32 * kWarps, Cfg<D, NT>::CTAS) tv_attn_kv4_row
       }
     }
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
+    for (int e = 0; e < 2; ++e) {
+      const int r = 2 * t + e;
+      const int node = r / p.G;
+      const uint64_t anc = r < live ? p.anc[o0 + node] : 0ull;
+      const int dep = WIN && r < live ? p.depth[o0 + node] : 0;
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const int r = nt * 8 + 2 * t + e;
-        const int node = (m0 + r) / p.G;
-        const uint64_t anc = r < live ? p.anc[o0 + node] : 0ull;
-        const int dep = WIN && r < live ? p.depth[o0 + node] : 0;
+      for (int mt = 0; mt < 4; ++mt)
 #pragma unroll
-        for (int mt = 0; mt < 4; ++mt)
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const int key = key_of(mt, h);
-            bool vis = key < n && ((anc >> key) & 1ull);
-            if (WIN && vis) {
-              const int kd = p.depth[o0 + key];
-              vis = P + kd < p.sinks || dep - (int64_t)kd < p.window;
-            }
-            if (!vis) s[mt][nt][2 * h + e] = -INFINITY;
+        for (int h = 0; h < 2; ++h) {
+          const int key = key_of(mt, h);
+          bool vis = key < n && ((anc >> key) & 1ull);
+          if (WIN && vis) {
+            const int kd = p.depth[o0 + key];
+            vis = P + kd < p.sinks || dep - (int64_t)kd < p.window;
           }
-      }
+          if (!vis) s[mt][2 * h + e] = -INFINITY;
+        }
+    }
     softmax(true, vsc, false);
 #pragma unroll
     for (int c = 0; c < CPT; ++c)
 #pragma unroll 1
       for (int i = 0; i < 8; ++i) {
-        float acc[NT][4];
+        float acc[4];
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) acc[nt][e] = 0.f;
+        for (int e = 0; e < 4; ++e) acc[e] = 0.f;
 #pragma unroll
         for (int mt = 0; mt < 4; ++mt) {
           uint32_t a[4];
@@ -528,17 +496,14 @@ __global__ void __launch_bounds__(32 * kWarps, Cfg<D, NT>::CTAS) tv_attn_kv4_row
             a[2 * h] = __byte_perm(x, y, 0x5410);
             a[2 * h + 1] = __byte_perm(x, y, 0x7632);
           }
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt) mma(acc[nt], a[0], a[1], a[2], a[3], pb[mt][nt][0], pb[mt][nt][1]);
+          mma(acc, a[0], a[1], a[2], a[3], pb[mt][0], pb[mt][1]);
         }
         // (o's index must be known when compiling)
 #pragma unroll
         for (int ii = 0; ii < 8; ++ii)
           if (ii == i) {
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-              for (int e = 0; e < 4; ++e) o[c][ii][nt][e] += acc[nt][e];
+            for (int e = 0; e < 4; ++e) o[c][ii][e] += acc[e];
           }
       }
   }
@@ -546,29 +511,27 @@ __global__ void __launch_bounds__(32 * kWarps, Cfg<D, NT>::CTAS) tv_attn_kv4_row
   // ---------------------------------------------------------------- the warps' results joined
   // lane (g, t): rows 2 t, 2 t + 1, channels 16 i + 2 g, + 1 of each chunk
   if (!C::QREG) __syncthreads();                                   // the queries' shared memory is free
-  float* so = smem + warp * 8 * NT * C::OUT_PITCH;
+  float* so = smem + warp * 8 * C::OUT_PITCH;
 #pragma unroll
-  for (int nt = 0; nt < NT; ++nt)
+  for (int e = 0; e < 2; ++e) {
+    float sum = l[e];
 #pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      float sum = l[nt][e];
-#pragma unroll
-      for (int off = 4; off < 32; off <<= 1) sum += __shfl_xor_sync(kAll, sum, off);
-      const int r = nt * 8 + 2 * t + e;
-      if (g == 0) {
-        s_m[warp][r] = sum == 0.f ? -INFINITY : -nm[nt][e];    // (a NaN sum has to show)
-        s_l[warp][r] = sum;
-      }
-#pragma unroll
-      for (int c = 0; c < CPT; ++c)
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-          *reinterpret_cast<float2*>(so + r * C::OUT_PITCH + c * 128 + 16 * i + 2 * g) =
-              make_float2(o[c][i][nt][e], o[c][i][nt][e + 2]);
+    for (int off = 4; off < 32; off <<= 1) sum += __shfl_xor_sync(kAll, sum, off);
+    const int r = 2 * t + e;
+    if (g == 0) {
+      s_m[warp][r] = sum == 0.f ? -INFINITY : -nm[e];    // (a NaN sum has to show)
+      s_l[warp][r] = sum;
     }
+#pragma unroll
+    for (int c = 0; c < CPT; ++c)
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        *reinterpret_cast<float2*>(so + r * C::OUT_PITCH + c * 128 + 16 * i + 2 * g) =
+            make_float2(o[c][i][e], o[c][i][e + 2]);
+  }
   __syncthreads();
   const bool direct = p.out != nullptr && nch == 1;
-  const int64_t slot0 = partial_slot(s_id, b, g_head, rt, 0, p.Hkv, p.row_tiles, p.tile_stride, p.splits);
+  const int64_t slot0 = partial_slot(s_id, b, g_head, 0, 0, p.Hkv, p.row_tiles, p.tile_stride, p.splits);
   for (int r = warp; r < live; r += kWarps) {
     float M = -INFINITY, L = 0.f, wt[kWarps];
 #pragma unroll
@@ -579,14 +542,13 @@ __global__ void __launch_bounds__(32 * kWarps, Cfg<D, NT>::CTAS) tv_attn_kv4_row
       L += wt[w] * s_l[w][r];
     }
     const float inv = L == 0.f ? 0.f : 1.f / L;
-    const int m = m0 + r;
-    const int64_t row = ((int64_t)(o0 + m / p.G) * p.Hq + g_head * p.G + m % p.G) * D;
+    const int64_t row = row_at(r);
     if (!direct && lane == 0) p.ml_part[slot0 + (int64_t)r * p.splits] = make_float2(M, L);
     for (int ch = lane * 4; ch < D; ch += 128) {
       float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
       for (int w = 0; w < kWarps; ++w) {
-        const float4 x = *reinterpret_cast<const float4*>(smem + (w * 8 * NT + r) * C::OUT_PITCH + ch);
+        const float4 x = *reinterpret_cast<const float4*>(smem + (w * 8 + r) * C::OUT_PITCH + ch);
         const float f = wt[w] * inv;
         a.x = fmaf(f, x.x, a.x);
         a.y = fmaf(f, x.y, a.y);
@@ -605,38 +567,31 @@ __global__ void __launch_bounds__(32 * kWarps, Cfg<D, NT>::CTAS) tv_attn_kv4_row
   }
 }
 
-template <int D, int NT, bool WIN>
+template <int D, bool WIN>
 cudaError_t launch_t(const AttnParams& p, cudaStream_t st) {
-  const cudaError_t e = ensure_max_dynamic_smem<tv_attn_kv4_rows_kernel<D, NT, WIN>>(Cfg<D, NT>::SMEM);
+  const cudaError_t e = ensure_max_dynamic_smem<tv_attn_kv4_rows_kernel<D, WIN>>(Cfg<D>::SMEM);
   if (e != cudaSuccess) return e;
-  return launch_dep(tv_attn_kv4_rows_kernel<D, NT, WIN>, dim3(p.row_tiles, p.Hkv * p.splits, p.B), dim3(32 * kWarps),
-                    Cfg<D, NT>::SMEM, st, p);
+  return launch_dep(tv_attn_kv4_rows_kernel<D, WIN>, dim3(1, p.Hkv * p.splits, p.B), dim3(32 * kWarps),
+                    Cfg<D>::SMEM, st, p);
 }
 
 template <bool WIN>
-cudaError_t launch_d(const AttnParams& p, int tiles, cudaStream_t s) {
-  if (p.d == 128) return tiles == 1 ? launch_t<128, 1, WIN>(p, s) : launch_t<128, 2, WIN>(p, s);
-  if (p.d == 256) return launch_t<256, 1, WIN>(p, s);
-  return launch_t<512, 1, WIN>(p, s);
+cudaError_t launch_d(const AttnParams& p, cudaStream_t s) {
+  if (p.d == 128) return launch_t<128, WIN>(p, s);
+  if (p.d == 256) return launch_t<256, WIN>(p, s);
+  return launch_t<512, WIN>(p, s);
 }
 
 }  // namespace
 
-// 8-row tiles of the register kernel for a sequence's rows, 0 where it does
-// not apply: 16 rows only at head_dim 128 (O would not fit the registers)
-int kv4_rows_tiles(const tv_desc* d, int G) {
-  const int rows = d->max_nodes * G;
-  if (d->dtype != TV_BF16) return 0;
-  if (rows <= 8) return 1;
-  return rows <= 16 && d->head_dim == 128 ? 2 : 0;
-}
+bool kv4_rows_supported(const tv_desc* d, int G) { return d->dtype == TV_BF16 && d->max_nodes * G <= kRows; }
 
-int kv4_rows_ctas_per_sm(int d, int tiles) { return d == 128 && tiles == 1 ? Cfg<128, 1>::CTAS : 2; }
+int kv4_rows_ctas_per_sm(int d) { return d == 128 ? Cfg<128>::CTAS : Cfg<256>::CTAS; }
 
 int kv4_rows_key_tile() { return kSpan; }
 
-cudaError_t launch_attn_kv4_rows(const AttnParams& p, int tiles, cudaStream_t s) {
-  return p.window > 0 ? launch_d<true>(p, tiles, s) : launch_d<false>(p, tiles, s);
+cudaError_t launch_attn_kv4_rows(const AttnParams& p, cudaStream_t s) {
+  return p.window > 0 ? launch_d<true>(p, s) : launch_d<false>(p, s);
 }
 
 }  // namespace tv

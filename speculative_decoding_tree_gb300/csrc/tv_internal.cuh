@@ -257,7 +257,7 @@ cudaError_t launch_attn_tc_window(const AttnParams& p, cudaStream_t s);
 cudaError_t launch_attn_tc2(const AttnParams& p, cudaStream_t s);
 cudaError_t launch_attn_tcp(const AttnParams& p, cudaStream_t s);
 cudaError_t launch_attn_kv4(const AttnParams& p, int columns, cudaStream_t s);
-cudaError_t launch_attn_kv4_rows(const AttnParams& p, int tiles, cudaStream_t s);
+cudaError_t launch_attn_kv4_rows(const AttnParams& p, cudaStream_t s);
 int64_t tcp_units(const AttnParams& p);
 cudaError_t launch_merge(const MergeParams& p, cudaStream_t s);
 cudaError_t launch_tree_mask(const int32_t* parents, const int32_t* offs, uint64_t* anc, int32_t* depth,
@@ -272,8 +272,8 @@ bool kv4_tc_supported(const tv_desc* d, int G);   // the same for the 4-bit cach
 int kv4_tc_columns(int max_nodes, int G, int d);  // its query-row columns per tile (16 .. 128)
 int kv4_tc_ctas_per_sm(int d, int columns);
 int kv4_tc_key_tile();
-int kv4_rows_tiles(const tv_desc* d, int G);      // the register kernel's 8-row tiles, 0: not applicable
-int kv4_rows_ctas_per_sm(int d, int tiles);
+bool kv4_rows_supported(const tv_desc* d, int G); // the register kernel's: bf16, at most 8 rows
+int kv4_rows_ctas_per_sm(int d);
 int kv4_rows_key_tile();
 
 }  // namespace tv

@@ -22,19 +22,18 @@ int make_window_plan(const tv_desc* d, const tv_window* w, bool kv4, Plan* p) {
   const int G = d->num_q_heads / d->num_kv_heads;
   // kernel: CUDA cores (0), one tensor-core CTA per row tile (1), and for the
   // 4-bit cache tcgen05 (4) or, for few rows, registers only (5)
-  const int r_tiles = kv4 ? kv4_rows_tiles(d, G) : 0;
   int kernel = 0, key_tile = 32, rows_per_tile = 4 * (1024 / d->head_dim), ctas_per_sm = 1;
   int step = 32;                                     // keys a chunk grows by
   if (!kv4 && tc_supported(d, G)) {
     kernel = 1;
     step = key_tile = tc_key_tile(d->head_dim);
     rows_per_tile = (128 / G) * G;
-  } else if (r_tiles > 0) {
+  } else if (kv4 && kv4_rows_supported(d, G)) {
     kernel = 5;
     key_tile = kv4_rows_key_tile();
     step = 4 * key_tile;                             // a span for each warp
-    rows_per_tile = 8 * r_tiles / G * G;
-    ctas_per_sm = kv4_rows_ctas_per_sm(d->head_dim, r_tiles);
+    rows_per_tile = d->max_nodes * G;
+    ctas_per_sm = kv4_rows_ctas_per_sm(d->head_dim);
   } else if (kv4 && kv4_tc_supported(d, G)) {
     kernel = 4;
     step = key_tile = kv4_tc_key_tile();
@@ -63,7 +62,12 @@ int make_window_plan(const tv_desc* d, const tv_window* w, bool kv4, Plan* p) {
     while (c <= tiles && num_chunks(L, (int)(c * step), tree_tile) > want) ++c;
     chunk = c * step;
   } else {
-    chunk = align_up(1920, step);
+    // ragged batch: about four waves of CTAs when the sequences are half the
+    // longest on average, but no chunk below 1920 keys (make_plan's): 64
+    // sequences x 4 rows 163 us with 1920, 156 with 2816 and 163 with 4096
+    // keys; x 32 rows 315 / 297 / 289; 16 trees of 64 .. 256 rows 177 / 184 / 182
+    const double even = (double)units * L / (8.0 * slots);
+    chunk = align_up(even < 1920 ? 1920 : (even > 8192 ? 8192 : (int64_t)even), step);
   }
   if (chunk > (int64_t)1 << 30) return TV_ERR_OVERFLOW;
   const int splits = num_chunks(L, (int)chunk, tree_tile);
@@ -144,7 +148,7 @@ int attention(const tv_desc* d, const tv_window* w, bool kv4, const void* q, con
   a.depth = depth;
   a.out = out;                                       // one-chunk sequences are finished by the split pass
   const cudaStream_t s = as_stream(stream);
-  const cudaError_t e = p.pub.kernel == 5   ? launch_attn_kv4_rows(a, kv4_rows_tiles(d, p.G), s)
+  const cudaError_t e = p.pub.kernel == 5   ? launch_attn_kv4_rows(a, s)
                         : p.pub.kernel == 4 ? launch_attn_kv4(a, kv4_tc_columns(d->max_nodes, p.G, d->head_dim), s)
                         : kv4               ? launch_attn_simt_kv4(a, d->dtype, s)
                         : p.pub.kernel == 1 ? launch_attn_tc_window(a, s)

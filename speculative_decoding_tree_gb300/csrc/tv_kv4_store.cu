@@ -3,12 +3,13 @@
 //
 // Quantisation of a group with largest magnitude A (32 channels of K, all
 // channels of V at one position): the smallest scale s with 7 s >= A, then
-// q = round(x / s) to even, |q| <= 7, u = q + 8.  x / s is taken as x times
-// the reciprocal, rounded to a whole number by adding 1.5 x 2^23 in one fused
-// multiply-add (no conversion instruction: those run at a quarter of the
-// rate), and corrected by the exact residual x - q s (it has no more bits than
-// x): the result is that of exact arithmetic, ties included.  The sum's low
-// bits are q, so eight of them pack by multiply-adds.
+// q = round(x / s) to even, |q| <= 7, u = q + 8, as in exact arithmetic, ties
+// included.  x / s is taken as x times the reciprocal and rounded to a whole
+// number by adding 1.5 x 2^23 (no conversion instruction: those run at a
+// quarter of the rate).  An fp32 value's result is then corrected by the exact
+// residual x - q s (it has no more bits than x); a bf16 value needs none
+// (steps_of).  The sum's low bits are q, so eight of them pack by
+// multiply-adds.
 //
 // One CTA handles the 16-position block of one KV head, K and V, and issues
 // all its loads before the first use.  K is quantised where it is loaded: four
@@ -111,28 +112,40 @@ __device__ __forceinline__ void two(const __nv_bfloat16* p, float& x, float& y) 
   y = __uint_as_float(w & 0xffff0000u);
 }
 
-// smallest code whose 7 steps reach amax (255 if none): a guess from amax / 7
-// in rounded arithmetic, then stepped to the exact answer (7 s is exact)
+// smallest code whose 7 steps reach amax <= kMost: the code below amax / 7
+// (taken a little low, so never above the answer's predecessor), and one more
+// for each of the next two that still falls short (7 s is exact)
 __device__ __forceinline__ uint32_t scale_code(float amax) {
-  const int bits = __float_as_int(amax * (1.f / 7.f));
-  int c = (bits - (112 << 23)) >> 20;
-  c = c < 0 ? 0 : (c > 255 ? 255 : c);
-  while (c < 255 && 7.f * scale_of((uint32_t)c) < amax) ++c;
-  while (c > 0 && 7.f * scale_of((uint32_t)c - 1) >= amax) --c;
-  return (uint32_t)c;
+  const int bits = __float_as_int(amax * (0.99999f / 7.f));
+  const uint32_t c = (uint32_t)max((bits >> 20) - (112 << 3), 0);
+  const float s = scale_of(c), next = scale_of(c + 1);
+  return c + (7.f * s < amax ? 1u : 0u) + (7.f * next < amax ? 1u : 0u);
 }
 
 constexpr float kMagic = 12582912.f;             // 1.5 x 2^23: x + kMagic is x rounded to a whole number
 constexpr uint32_t kMagicBits = 0x4B400000u;
 
 // bits kMagicBits + q of x on the grid of step s (inv = 1 / s, rounded); |x| <= 7 s
-__device__ __forceinline__ uint32_t steps_of(float x, float s, float inv) {
+template <typename T>
+__device__ __forceinline__ uint32_t steps_of(float x, float s, float inv);
+template <>
+__device__ __forceinline__ uint32_t steps_of<float>(float x, float s, float inv) {
   float t = fmaf(x, inv, kMagic);
   const float r = fmaf(kMagic - t, s, x);
   // too far, or half way with an odd q: one step on (the bound is s / 2, and for an odd q the float below it)
   const float bound = __uint_as_float(__float_as_uint(0.5f * s) - (__float_as_uint(t) & 1u));
   if (fabsf(r) > bound) t += copysignf(1.f, r);
   return __float_as_uint(t);
+}
+// x is a bf16 number: x / s = X 2^k / (8 + m) with X < 256.  Where that is near
+// a half (2 q + 1) / 2 it is the half, or at least 2^(k + 1) / (2 (8 + m)) away
+// with k >= -6: more than 2^-10.  So rounding x inv (off by 7 x 2^-24 at most)
+// to the grid of 2^-13 first finds each half exactly and moves nothing across
+// one; the second sum then rounds to whole numbers, halves to even.
+template <>
+__device__ __forceinline__ uint32_t steps_of<__nv_bfloat16>(float x, float, float inv) {
+  constexpr float kFine = 1536.f;                // 1.5 x 2^10: the sum's last bit is 2^-13
+  return __float_as_uint(fmaf(x, inv, kFine) + (kMagic - kFine));
 }
 
 __host__ __device__ constexpr int value_bit(int e) { return (e >> 1) * 4 + (e & 1) * 16; }
@@ -215,7 +228,7 @@ __device__ __forceinline__ void store_block(const T* k_rows, const T* v_rows, ui
       kx[q].get(x);
       uint32_t w = 0;
 #pragma unroll
-      for (int t = 0; t < 8; ++t) w += steps_of(x[t], s, inv) << value_bit(t);
+      for (int t = 0; t < 8; ++t) w += steps_of<T>(x[t], s, inv) << value_bit(t);
       *reinterpret_cast<uint32_t*>(kb + k_code(c, i) + sub * 4) = w - pack_excess();
       if (sub == 0) kb[k_scale(D, c, i)] = (uint8_t)code;
     }
@@ -235,8 +248,8 @@ __device__ __forceinline__ void store_block(const T* k_rows, const T* v_rows, ui
       const float2 st = s_step[8 * h + i];
       float x, y;
       two(xs + (8 * h + i) * D + ch, x, y);
-      w[0] += steps_of(x, st.x, st.y) << value_bit(i);
-      w[1] += steps_of(y, st.x, st.y) << value_bit(i);
+      w[0] += steps_of<T>(x, st.x, st.y) << value_bit(i);
+      w[1] += steps_of<T>(y, st.x, st.y) << value_bit(i);
     }
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
