@@ -41,7 +41,6 @@ struct Row8<float> {
     a = __ldcg(reinterpret_cast<const float4*>(src));
     b = __ldcg(reinterpret_cast<const float4*>(src) + 1);
   }
-  __device__ __forceinline__ void zero() { a = b = make_float4(0.f, 0.f, 0.f, 0.f); }
   __device__ __forceinline__ void get(float (&x)[8]) const {
     x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
     x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
@@ -65,7 +64,6 @@ template <>
 struct Row8<__nv_bfloat16> {
   uint4 u;
   __device__ __forceinline__ void load(const __nv_bfloat16* src) { u = __ldcg(reinterpret_cast<const uint4*>(src)); }
-  __device__ __forceinline__ void zero() { u = make_uint4(0, 0, 0, 0); }
   __device__ __forceinline__ void get(float (&x)[8]) const {
     const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
@@ -122,10 +120,17 @@ __device__ __forceinline__ uint32_t scale_code(float amax) {
   return c + (7.f * s < amax ? 1u : 0u) + (7.f * next < amax ? 1u : 0u);
 }
 
+// 1 / s within 2^-22 (steps_of allows for more)
+__device__ __forceinline__ float reciprocal(float s) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(s));
+  return r;
+}
+
 constexpr float kMagic = 12582912.f;             // 1.5 x 2^23: x + kMagic is x rounded to a whole number
 constexpr uint32_t kMagicBits = 0x4B400000u;
 
-// bits kMagicBits + q of x on the grid of step s (inv = 1 / s, rounded); |x| <= 7 s
+// bits kMagicBits + q of x on the grid of step s (inv = 1 / s within 2^-22); |x| <= 7 s
 template <typename T>
 __device__ __forceinline__ uint32_t steps_of(float x, float s, float inv);
 template <>
@@ -139,7 +144,7 @@ __device__ __forceinline__ uint32_t steps_of<float>(float x, float s, float inv)
 }
 // x is a bf16 number: x / s = X 2^k / (8 + m) with X < 256.  Where that is near
 // a half (2 q + 1) / 2 it is the half, or at least 2^(k + 1) / (2 (8 + m)) away
-// with k >= -6: more than 2^-10.  So rounding x inv (off by 7 x 2^-24 at most)
+// with k >= -6: more than 2^-10.  So rounding x inv (off by 7 x 2^-22 at most)
 // to the grid of 2^-13 first finds each half exactly and moves nothing across
 // one; the second sum then rounds to whole numbers, halves to even.
 template <>
@@ -166,22 +171,17 @@ __device__ __forceinline__ void store_block(const T* k_rows, const T* v_rows, ui
   constexpr int IT = D / 64;                     // 8-value pieces per thread, of K and of V
   const int tid = threadIdx.x;
   Row8<T> kx[IT], vx[IT];
+  // (a position not written loads row 0 and drops what comes of it)
   const int vi = tid >> 3, vrow = s_row[vi];
 #pragma unroll
-  for (int q = 0; q < IT; ++q) {
-    if (vrow >= 0)
-      vx[q].load(v_rows + (int64_t)vrow * D + ((tid & 7) + 8 * q) * 8);
-    else
-      vx[q].zero();
-  }
+  for (int q = 0; q < IT; ++q) vx[q].load(v_rows + (int64_t)max(vrow, 0) * D + ((tid & 7) + 8 * q) * 8);
+  const int ki = (tid >> 2) & 15, krow = s_row[ki];   // the same position in each piece
 #pragma unroll
   for (int q = 0; q < IT; ++q) {
-    const int e = tid + q * kThreads, row = s_row[(e >> 2) & 15];
-    if (row >= 0)
-      kx[q].load(k_rows + (int64_t)row * D + (e >> 6) * kGroup + (e & 3) * 8);
-    else
-      kx[q].zero();
+    const int c = (tid >> 6) + 2 * q;
+    kx[q].load(k_rows + (int64_t)max(krow, 0) * D + c * kGroup + (tid & 3) * 8);
   }
+  const uint32_t gone = __ballot_sync(0xffffffffu, s_row[tid & 15] < 0) & 0xffffu;   // positions not written
   // V: stage the rows and take each position's scale (8 threads a position)
   {
     uint32_t top = 0;
@@ -204,14 +204,14 @@ __device__ __forceinline__ void store_block(const T* k_rows, const T* v_rows, ui
     if ((tid & 7) == 0) {
       const uint32_t code = scale_code(__uint_as_float(top));
       const float s = scale_of(code);
-      s_step[vi] = make_float2(s, 1.f / s);            // (a position not written: zeros on the smallest grid)
+      s_step[vi] = make_float2(s, reciprocal(s));
       if (vrow >= 0) vb[v_scale(D, vi)] = (uint8_t)code;
     }
   }
   // K: 4 lanes a group of 32 channels, 8 positions a warp
 #pragma unroll
   for (int q = 0; q < IT; ++q) {
-    const int e = tid + q * kThreads, sub = e & 3, i = (e >> 2) & 15, c = e >> 6;
+    const int sub = tid & 3, c = (tid >> 6) + 2 * q;
     uint32_t top = kx[q].top();
     top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
     top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
@@ -221,25 +221,27 @@ __device__ __forceinline__ void store_block(const T* k_rows, const T* v_rows, ui
       top = max(top, __shfl_xor_sync(0xfu << (tid & 28), top, 1));
       top = max(top, __shfl_xor_sync(0xfu << (tid & 28), top, 2));
     }
-    if (s_row[i] >= 0) {
+    if (krow >= 0) {
       const uint32_t code = scale_code(__uint_as_float(top));
-      const float s = scale_of(code), inv = 1.f / s;
+      const float s = scale_of(code), inv = reciprocal(s);
       float x[8];
       kx[q].get(x);
       uint32_t w = 0;
 #pragma unroll
       for (int t = 0; t < 8; ++t) w += steps_of<T>(x[t], s, inv) << value_bit(t);
-      *reinterpret_cast<uint32_t*>(kb + k_code(c, i) + sub * 4) = w - pack_excess();
-      if (sub == 0) kb[k_scale(D, c, i)] = (uint8_t)code;
+      *reinterpret_cast<uint32_t*>(kb + k_code(c, ki) + sub * 4) = w - pack_excess();
+      if (sub == 0) kb[k_scale(D, c, ki)] = (uint8_t)code;
     }
   }
   __syncthreads();
   // V: a thread gathers 8 positions (half h of the block) of two channels
   const int h = tid >> 6;
   uint32_t keep = 0;                                   // nibbles of positions not written
+  if (gone) {
 #pragma unroll
-  for (int i = 0; i < 8; ++i)
-    if (s_row[8 * h + i] < 0) keep |= 15u << value_bit(i);
+    for (int i = 0; i < 8; ++i)
+      if ((gone >> (8 * h + i)) & 1u) keep |= 15u << value_bit(i);
+  }
 #pragma unroll 1
   for (int ch = 2 * (tid & 63); ch < D; ch += kThreads) {
     uint32_t w[2] = {0u, 0u};
