@@ -87,6 +87,9 @@ __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
   return *reinterpret_cast<uint32_t*>(&h);
 }
 
+// the lowest n bits, n clamped to 0 .. 64
+__device__ __forceinline__ uint64_t low_bits(int n) { return n >= 64 ? ~0ull : (n <= 0 ? 0ull : (1ull << n) - 1); }
+
 // WIN: a sliding window with sinks (KeyMap).  The chunk walks virtual keys; a
 // row's view is applied as a mask on the scores of the tiles that reach below
 // the last row's window, and V rows that no row sees are zeroed like the ones
@@ -344,10 +347,11 @@ tv_attn_tc_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ 
             }
             ++tail_uses;
             const int nu = z1 - z0, nz = nu + BN - ze;
-            for (int e = lane; e < 2 * nz * 8; e += 32) {
-              const int j = (e / 8) % nz;
-              const int bx = e / (nz * 8), r = j < nu ? z0 + j : ze + j - nu, q16 = e % 8;
-              *reinterpret_cast<uint4*>(dst + bx * BOX_BYTES + r * 128 + q16 * 16) = make_uint4(0, 0, 0, 0);
+            for (int i = lane >> 3; i < nz; i += 4) {        // eight lanes a row, both boxes
+              const int r = i < nu ? z0 + i : ze + i - nu;
+              uint8_t* at = dst + r * 128 + (lane & 7) * 16;
+              *reinterpret_cast<uint4*>(at) = make_uint4(0, 0, 0, 0);
+              *reinterpret_cast<uint4*>(at + BOX_BYTES) = make_uint4(0, 0, 0, 0);
             }
             fence_proxy_async_smem();
             __syncwarp();
@@ -476,25 +480,33 @@ tv_attn_tc_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ 
       }
       const bool tree = (t == npt);
       bool partial = tree || (t == npt - 1 && tail_valid < BN);
-      int rel_s = 0, rel_lo = 0;                            // WIN: visible keys are < rel_s or >= rel_lo
-      if (WIN && !tree) {
-        const int64_t p0 = tile_pos(t);
-        partial = partial || p0 < P + kMaxNodes - p.window;
-        rel_s = (int)min((int64_t)BN, max((int64_t)0, p.sinks - p0));
-        rel_lo = (int)min((int64_t)BN, max((int64_t)0, first_pos + dep - p0));
-      }
+      if (WIN && !tree) partial = partial || tile_pos(t) < P + kMaxNodes - p.window;
       if (partial) {
-        // tree tile: ancestor bits; last prefix tile: key range
-        const int lim = tree ? min(n, 64) : (t == npt - 1 ? tail_valid : BN);
-#pragma unroll
-        for (int e = 0; e < 64; ++e) {
-          const int key = kofs + e;
-          bool vis = key < lim;
-          if (tree) vis = vis && ((anc >> (key & 63)) & 1ull);
-          if (WIN && tree) vis = vis && (P + s_kdep[key & 63] < p.sinks || dep - (int64_t)s_kdep[key & 63] < p.window);
-          if (WIN && !tree) vis = vis && (key < rel_s || key >= rel_lo);
-          sv[e] = vis ? sv[e] : -INFINITY;
+        // the keys of this half that the row sees, one bit each: of the tree
+        // its ancestors, of the last prefix tile those below the end; with a
+        // window those below `sink` or from `lo` on (positions in a prefix
+        // tile, depths in the tree, where only a window below 64 hides any)
+        uint64_t vis;
+        if (tree) {
+          vis = half ? 0ull : anc & low_bits(n);
+          if (WIN && p.window < kMaxNodes) {
+            const int sink = (int)min((int64_t)kMaxNodes, max((int64_t)0, p.sinks - P));
+            const int lo = dep - (int)p.window + 1;
+#pragma unroll 1
+            for (int i = 0; i < n; ++i)
+              if (s_kdep[i] >= sink && s_kdep[i] < lo) vis &= ~(1ull << i);
+          }
+        } else {
+          vis = low_bits((t == npt - 1 ? tail_valid : BN) - kofs);
+          if (WIN) {
+            const int64_t p0 = tile_pos(t) + kofs;
+            const int sink = (int)min((int64_t)BN, max((int64_t)0, p.sinks - p0));
+            const int lo = (int)min((int64_t)BN, max((int64_t)0, first_pos + dep - p0));
+            vis &= low_bits(sink) | ~low_bits(lo);
+          }
         }
+#pragma unroll
+        for (int e = 0; e < 64; ++e) sv[e] = (vis >> e) & 1ull ? sv[e] : -INFINITY;
       }
       float mx8[8];
 #pragma unroll
