@@ -19,6 +19,8 @@
 //   warp 1      owns tensor memory; lane 0 issues tcgen05.mma:
 //               S(t) = Q K(t)^T into one of two 128-column TMEM buffers, then
 //               O += P(t-1) V(t-1) with P read from TMEM.
+//   warp 3      completes the V chunks whose rows past the prefix end, or seen
+//               by no row of the query tile, have to be zeros.
 //   warps 4-11  softmax, two threads per query row (its TMEM lane), each
 //               taking half of the tile's keys: load the S half-row, mask,
 //               exchange the half-row maxima, P = 2^(s*c - m) written back
@@ -59,7 +61,7 @@ constexpr uint32_t BOX_BYTES = BN * 128;        // one TMA box: 128 rows x 64 bf
 constexpr uint32_t CHUNK_BYTES = 2 * BOX_BYTES; // 128 keys x 128 columns
 constexpr uint64_t kWaitNs = 1000000000ull;
 constexpr float kRescaleThreshold = 8.0f;       // rescale O when the max grows by > 2^8
-constexpr int kThreads = 384;                   // warps 0 producer, 1 MMA, 2-3 idle, 4-11 softmax
+constexpr int kThreads = 384;                   // warps 0 producer, 1 MMA, 2 partials, 3 rows to zero, 4-11 softmax
 constexpr int kSoftmax = 256;
 constexpr int kSoftmaxWarps = kSoftmax / 32;   // barriers count warps: lane 0 arrives after __syncwarp                   // two warpgroups, each half of a row's keys
 constexpr uint32_t kHeader = 3072;              // barriers, TMEM address, row exchange (then 1 KB aligned)
@@ -70,7 +72,7 @@ struct Cfg {
   static constexpr int NS = D == 256 ? 5 : 6;     // ring slots
   static constexpr uint32_t Q_BYTES = BM * D * 2;
   static constexpr uint32_t RING_BYTES = NS * CHUNK_BYTES;
-  static constexpr int NBARS = 2 * NS + 12 + D / 32;   // ring, pipeline, epilogue boxes
+  static constexpr int NBARS = 2 * NS + 11 + D / 32;   // ring, pipeline, epilogue boxes
   static constexpr uint32_t SMEM = kHeader + Q_BYTES + RING_BYTES;
   static_assert(NBARS * 8 + 8 <= 256, "barriers overflow the header");
   static_assert(SMEM <= 232448, "shared memory over the 227 KB per-block limit");
@@ -111,19 +113,21 @@ tv_attn_tc_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ 
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   float* xch = reinterpret_cast<float*>(smem_raw + 256);        // [2 parity][2 half][128 rows]
   int* s_kdep = reinterpret_cast<int*>(smem_raw + 2304);        // [64] depths of the tree's nodes (WIN)
-  static_assert(2304 + 64 * 4 <= kHeader, "depths overflow the header");
+  uint64_t* tails = reinterpret_cast<uint64_t*>(smem_raw + 2560);   // [NS] V chunk landed, rows to be zeroed
+  static_assert(2560 + NS * 8 <= kHeader, "depths and tail barriers overflow the header");
   uint8_t* sQ = smem_raw + kHeader;
   uint8_t* ring = sQ + C::Q_BYTES;
   auto bar = [&](int i) { return smem_u32(&bars[i]); };
   auto FULL = [&](int i) { return bar(i); };
   auto EMPTY = [&](int i) { return bar(NS + i); };
+  auto TAIL = [&](int i) { return smem_u32(&tails[i]); };
   const int bq = 2 * NS;
-  const uint32_t Q_FULL = bar(bq), TAIL = bar(bq + 7), FIN = bar(bq + 8), XL = bar(bq + 11);
-  auto BOX = [&](int i) { return bar(bq + 12 + i); };     // epilogue box i staged (D / 32 boxes)
+  const uint32_t Q_FULL = bar(bq), FIN = bar(bq + 7), XL = bar(bq + 10);
+  auto BOX = [&](int i) { return bar(bq + 11 + i); };     // epilogue box i staged (D / 32 boxes)
   auto S_FULL = [&](int i) { return bar(bq + 1 + i); };   // QK(t) done, buffer t & 1
   auto P_FULL = [&](int i) { return bar(bq + 3 + i); };   // softmax wrote P(t), buffer t & 1
   auto O_DONE = [&](int i) { return bar(bq + 5 + i); };   // PV(t) done, alternating by t & 1
-  auto XCH = [&](int i) { return bar(bq + 9 + i); };      // row maxima exchanged for tile t, t & 1
+  auto XCH = [&](int i) { return bar(bq + 8 + i); };      // row maxima exchanged for tile t, t & 1
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   // the layout below needs the dynamic shared window to start 1 KB aligned
@@ -138,6 +142,7 @@ tv_attn_tc_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ 
     for (int i = 0; i < NS; ++i) {
       mbar_init(FULL(i), 1);
       mbar_init(EMPTY(i), 1);
+      mbar_init(TAIL(i), 1);
     }
     mbar_init(Q_FULL, 1);
     for (int i = 0; i < 2; ++i) {
@@ -146,7 +151,6 @@ tv_attn_tc_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ 
       mbar_init(O_DONE(i), 1);
       mbar_init(XCH(i), kSoftmaxWarps);
     }
-    mbar_init(TAIL, 1);
     mbar_init(FIN, 1);
     mbar_init(XL, kSoftmaxWarps);
     // box i: the 4 warps of one half, once per 32-column step it spans
@@ -256,6 +260,19 @@ tv_attn_tc_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ 
   const int T = npt + (has_tree ? 1 : 0);
   const int tail_valid = npt > 0 ? (int)(k_end - (k_begin + (int64_t)(npt - 1) * BN)) : BN;
 
+  // V rows of a prefix tile that have to be zeros: [z0, z1) (seen by no row)
+  // and [ze, BN) (past the end); false: none
+  auto zero_rows = [&](int tile, int* z0, int* z1, int* ze) -> bool {
+    *z0 = *z1 = 0;
+    *ze = tile == npt - 1 ? tail_valid : BN;
+    if (WIN) {
+      const int64_t p0 = tile_pos(tile);
+      *z0 = (int)min((int64_t)*ze, max((int64_t)0, p.sinks - p0));
+      *z1 = (int)min((int64_t)*ze, max((int64_t)*z0, first_pos - p0));
+    }
+    return *ze < BN || *z1 > *z0;
+  };
+
   if (!active) {
     // nothing to do for this CTA: straight to teardown
   } else if (warp == 0) {
@@ -265,7 +282,7 @@ tv_attn_tc_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ 
       for (int kb = 0; kb < D / 64; ++kb)
         tma_load_3d(smem_u32(sQ + kb * (BM * 128)), &tm_q, Q_FULL, kb * 64, g * G, o0 + m0 / G);
     }
-    int j = 0, tail_uses = 0;
+    int j = 0;
     bool ok = true;
     // paged cache: lane i < 8 owns page i of a key tile; page ids are read
     // well ahead of the copies that use them
@@ -298,17 +315,8 @@ tv_attn_tc_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ 
         const int tile = kind == 0 ? t : t - 1;
         if ((kind == 0 && t >= T) || (kind == 1 && t < 1)) continue;
         const bool tree = (tile == npt);
-        // V rows to zero: [z0, z1) (no row sees them) and [ze, BN) (past the end)
-        int z0 = 0, z1 = 0, ze = BN;
-        if (kind == 1 && !tree) {
-          if (tile == npt - 1) ze = tail_valid;
-          if (WIN) {
-            const int64_t p0 = tile_pos(tile);
-            z0 = (int)min((int64_t)ze, max((int64_t)0, p.sinks - p0));
-            z1 = (int)min((int64_t)ze, max((int64_t)z0, first_pos - p0));
-          }
-        }
-        const bool tail_fix = ze < BN || z1 > z0;
+        int z0, z1, ze;
+        const bool fix = kind == 1 && !tree && zero_rows(tile, &z0, &z1, &ze);   // warp 3 completes the chunk
         for (int c = 0; c < CPT && ok; ++c, ++j) {
           const int slot = j % NS, use = j / NS;
           if (use > 0 && !__all_sync(kAll, mbar_wait(EMPTY(slot), (use - 1) & 1, abort_flag, kWaitNs))) {
@@ -316,7 +324,7 @@ tv_attn_tc_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ 
             break;
           }
           uint8_t* dst = ring + slot * CHUNK_BYTES;
-          const uint32_t fb = tail_fix ? TAIL : FULL(slot);
+          const uint32_t fb = fix ? TAIL(slot) : FULL(slot);
           if (tree || !p.paged) {
             if (lane == 0) {
               mbar_expect_tx(fb, CHUNK_BYTES);
@@ -339,24 +347,6 @@ tv_attn_tc_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ 
             }
           }
           __syncwarp();
-          if (tail_fix) {
-            // rows past the prefix end (and unseen rows) become zeros before the MMA reads them
-            if (!__all_sync(kAll, mbar_wait(TAIL, tail_uses & 1, abort_flag, kWaitNs))) {
-              ok = false;
-              break;
-            }
-            ++tail_uses;
-            const int nu = z1 - z0, nz = nu + BN - ze;
-            for (int i = lane >> 3; i < nz; i += 4) {        // eight lanes a row, both boxes
-              const int r = i < nu ? z0 + i : ze + i - nu;
-              uint8_t* at = dst + r * 128 + (lane & 7) * 16;
-              *reinterpret_cast<uint4*>(at) = make_uint4(0, 0, 0, 0);
-              *reinterpret_cast<uint4*>(at + BOX_BYTES) = make_uint4(0, 0, 0, 0);
-            }
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(FULL(slot));
-          }
         }
       }
     }
@@ -443,6 +433,33 @@ tv_attn_tc_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ 
         }
       }
       if (issued) bulk_wait_read_all();
+    }
+  } else if (warp == 3) {
+    // ============================================================ rows to zero
+    // The V chunks with such rows complete here, so that the producer never
+    // waits for a copy to land.
+    uint32_t parity = 0;                          // one bit per slot
+    bool ok = true;
+    for (int u = 0; u < npt && ok; ++u) {
+      int z0, z1, ze;
+      if (!zero_rows(u, &z0, &z1, &ze)) continue;
+      for (int c = 0; c < CPT && ok; ++c) {
+        // the step of V(u) in the producer's order: K(0), K(1), V(0), K(2), ...
+        const int slot = ((min(u + 2, T) + u) * CPT + c) % NS;
+        ok = __all_sync(kAll, mbar_wait(TAIL(slot), (parity >> slot) & 1u, abort_flag, kWaitNs));
+        if (!ok) break;
+        parity ^= 1u << slot;
+        const int nu = z1 - z0, nz = nu + BN - ze;
+        for (int i = lane >> 3; i < nz; i += 4) {            // eight lanes a row, both boxes
+          const int r = i < nu ? z0 + i : ze + i - nu;
+          uint8_t* at = ring + slot * CHUNK_BYTES + r * 128 + (lane & 7) * 16;
+          *reinterpret_cast<uint4*>(at) = make_uint4(0, 0, 0, 0);
+          *reinterpret_cast<uint4*>(at + BOX_BYTES) = make_uint4(0, 0, 0, 0);
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(FULL(slot));
+      }
     }
   } else if (warp >= 4) {
     // ============================================================ softmax
