@@ -702,11 +702,19 @@ tv_attn_kv4_kernel(const __grid_constant__ AttnParams p, const __grid_constant__
           for (int j = 0; j < HC; ++j) s[j] = __uint_as_float(r[j]);
         }
         if (__builtin_expect(tree, 0)) {
-          const int kd = WIN && row < n ? p.depth[o0 + row] : 0;
+          // the key's bit of each row's ancestors; with a window also rows
+          // less than a window deeper than it
+          const uint32_t* word = reinterpret_cast<const uint32_t*>(sh.anc + c0) + ((row >> 5) & 1);
+          const uint32_t bit = row < kMaxNodes ? 1u << (row & 31) : 0u;
+          int lim = INT_MAX;
+          if (WIN && row < n) {
+            const int kd = p.depth[o0 + row];
+            if (P + kd >= p.sinks) lim = (int)min((int64_t)INT_MAX, kd + p.window);
+          }
 #pragma unroll
           for (int j = 0; j < HC; ++j) {
-            bool vis = row < kMaxNodes && ((sh.anc[c0 + j] >> (row & 63)) & 1ull);
-            if (WIN) vis = vis && (P + kd < p.sinks || sh.dep[c0 + j] - (int64_t)kd < p.window);
+            bool vis = (word[2 * j] & bit) != 0;
+            if (WIN) vis = vis && sh.dep[c0 + j] < lim;
             if (!vis) s[j] = -INFINITY;
           }
           return;
@@ -714,9 +722,11 @@ tv_attn_kv4_kernel(const __grid_constant__ AttnParams p, const __grid_constant__
         if (WIN) {
           const int64_t p0 = tile_pos(t), pos = p0 + row;
           if (p0 < P + kMaxNodes - p.window) {
+            // rows at most this deep see the key
+            const int lim = pos < p.sinks ? INT_MAX : (int)max((int64_t)-1, min((int64_t)INT_MAX, pos - first_pos));
 #pragma unroll
             for (int j = 0; j < HC; ++j)
-              if (!(pos < p.sinks || pos >= first_pos + sh.dep[c0 + j])) s[j] = -INFINITY;
+              if (sh.dep[c0 + j] > lim) s[j] = -INFINITY;
           }
         }
         if (__builtin_expect(t == npt - 1 && row >= tail, 0)) {
