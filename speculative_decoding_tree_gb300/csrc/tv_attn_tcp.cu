@@ -42,10 +42,11 @@
 //               both CTAs' shared memory to the other roles of both.
 //   warps 3-10  softmax (two threads per query row, each half of a tile's
 //               keys with its own running maximum, sum and O accumulator, so
-//               the two never wait for each other inside a unit), then each
+//               the two never wait for each other inside a unit; each
+//               writes its P over its own 64 S columns), then each
 //               unit's epilogue: the row's two threads exchange their
-//               maxima and sums once, combine the two accumulators and write
-//               the partial rows straight from registers.
+//               maxima and sums once, combine the two accumulators, write
+//               the partial rows straight from registers and meet again.
 // Barrier phases run on across units: slots by a slot counter, the S / P
 // buffers and O products by a tile counter, the epilogue's exchanges by an
 // exchange counter, per-unit barriers by a unit counter.  Every wait is bounded
@@ -505,7 +506,8 @@ tv_attn_tcp_kernel(const __grid_constant__ AttnParams p, const __grid_constant__
               for (int kq = 0; kq < BN / 32; ++kq) {  // 16 keys per step, 4 steps per half
                 const int kk = h * (BN / 32) + kq;
                 const uint64_t bd = smem_desc(vaddr + kk * (16 * 128), BOX_BYTES, 1024, 2);
-                mma_ts(tmem + 256 + (uint32_t)(h * D), pbuf + kk * 8, bd, ID_PV, (u > 0 || kq > 0) ? 1u : 0u);
+                mma_ts(tmem + 256 + (uint32_t)(h * D), pbuf + h * (BN / 2) + kq * 8, bd, ID_PV,
+                       (u > 0 || kq > 0) ? 1u : 0u);
               }
               mma_commit(O_DONE(h, ug & 1));
             }
@@ -529,7 +531,8 @@ tv_attn_tcp_kernel(const __grid_constant__ AttnParams p, const __grid_constant__
     // 64-127.  Each half keeps its own running maximum, sum and O
     // accumulator (TMEM columns 256 + 128 half), so the two threads of a row
     // meet only at the unit's end, where their (maximum, sum) pairs are
-    // exchanged through `xch` and the two accumulators combined.
+    // exchanged through `xch` and the two accumulators combined, and once
+    // more when both have read them.
     const int half = (warp - kFirstSoftmaxWarp) >> 2;
     const int r = (warp & 3) * 32 + lane;           // row in the tile == TMEM lane (warp % 4 picks the quarter)
     const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
@@ -643,7 +646,9 @@ tv_attn_tcp_kernel(const __grid_constant__ AttnParams p, const __grid_constant__
             const float2 la = up2(fadd2(fadd2(l4[0], l4[1]), fadd2(l4[2], l4[3])));
             l += la.x + la.y;
           }
-          tmem_st_x32(sbuf + half * 32, pk);          // P over the S columns, bf16 pairs
+          // P over the half's own S columns, bf16 pairs (the other half may
+          // not have read its scores yet)
+          tmem_st_x32(sbuf + kofs, pk);
         }
         tc_fence_before();
         __syncwarp();
@@ -704,7 +709,12 @@ tv_attn_tcp_kernel(const __grid_constant__ AttnParams p, const __grid_constant__
           }
         }
       }
+      // Both halves' threads read both accumulators: the next unit's first
+      // products, which a half's P alone lets go, wait until the other half
+      // has read them too.
       tc_fence_before();
+      if (epi) epi = exchange(0.f, m_p);
+      tc_fence_after();
       if (epi && !direct && tile_live && half == 0)
         p.ml_part[partial_slot(qe->s, qe->b, qe->g, my_rt, r, p.Hkv, p.row_tiles, BM, p.splits)] =
             make_float2(row_ok ? M : -INFINITY, row_ok ? L : 0.f);
