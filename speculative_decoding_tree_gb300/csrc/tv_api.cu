@@ -267,8 +267,13 @@ int launch_merge_from(const tv_desc* d, const Plan& pl, const int32_t* plen, con
   m.Hkv = d->num_kv_heads; m.G = pl.G; m.rows_per_tile = pl.pub.rows_per_tile;
   m.row_tiles = pl.pub.row_tiles; m.tile_stride = pl.tile_stride;
   m.window = pl.window; m.sinks = pl.sinks; m.map_tile = pl.map_tile;
-  merge_shape(d->batch * d->num_kv_heads * pl.pub.row_tiles, pl.tile_stride, d->head_dim, m.part_bf16 ? 2 : 4,
-              pl.pub.num_splits, num_sms(), &m.slab_rows, &m.batch_splits);
+  // the windowed and the 4-bit calls merge few rows of many splits more often
+  const bool few = pl.pub.kernel >= 4 || pl.window > 0;
+  const int rows = d->max_nodes * pl.G;
+  m.sparse = few ? 1 : 0;
+  m.tile_rows = few && rows < pl.pub.rows_per_tile ? rows : (few ? pl.pub.rows_per_tile : pl.tile_stride);
+  merge_shape(d->batch * d->num_kv_heads * pl.pub.row_tiles, m.tile_rows, d->head_dim, m.part_bf16 ? 2 : 4,
+              pl.pub.num_splits, num_sms(), few, &m.slab_rows, &m.batch_splits);
   return launch_merge(m, s) == cudaSuccess ? TV_OK : TV_ERR_CUDA;
 }
 

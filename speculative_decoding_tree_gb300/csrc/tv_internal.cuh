@@ -108,14 +108,17 @@ struct MergeParams {
   int64_t max_prefix, capacity;
   int chunk, tree_tile, splits;
   int early_reads;           // launched right after the split pass of the same call
-  int slab_rows;             // rows per merge CTA (2..32, a power of two, <= tile_stride)
+  int tile_rows;             // rows of a tile that can be live (grid), <= tile_stride
+  int slab_rows;             // rows per merge CTA (1..32, a power of two)
   int batch_splits;          // splits gathered into shared memory at once
+  int sparse;                // sequences may have far fewer splits than the grid
   int64_t window, sinks;     // as in AttnParams (0: the whole prefix)
   int map_tile;
 };
 
-// Merge CTA shape for `tiles` (sequence, KV head, row tile) triples.
-void merge_shape(int tiles, int tile_stride, int d, int esize, int splits, int sms, int* slab_rows,
+// Merge CTA shape for `tiles` (sequence, KV head, row tile) triples of up to
+// tile_rows rows each; `single` allows CTAs of one row.
+void merge_shape(int tiles, int tile_rows, int d, int esize, int splits, int sms, bool single, int* slab_rows,
                  int* batch_splits);
 
 // Number of key chunks (splits) of a sequence with a (clamped) prefix of P

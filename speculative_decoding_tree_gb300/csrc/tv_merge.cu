@@ -40,7 +40,8 @@ __device__ __forceinline__ float4 load4(const __nv_bfloat16* row, int c) {
   return make_float4(a.x, a.y, b.x, b.y);
 }
 
-template <int D, typename PT>
+// WIN: a windowed call (the chunks run over its virtual keys)
+template <int D, typename PT, bool WIN>
 __global__ __launch_bounds__(kMergeThreads) void merge_slab_kernel(MergeParams p) {
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ __align__(8) uint64_t bar;
@@ -72,7 +73,7 @@ __global__ __launch_bounds__(kMergeThreads) void merge_slab_kernel(MergeParams p
   const int nrows = n * p.G;
   const int m_first = rt * p.rows_per_tile + r0;
   const int64_t P = clamp_prefix(Praw, p.max_prefix, p.capacity);
-  const int nch = num_chunks(key_map(P, p.window, p.sinks, p.map_tile).len, p.chunk, p.tree_tile);
+  const int nch = num_chunks(WIN ? key_map(P, p.window, p.sinks, p.map_tile).len : P, p.chunk, p.tree_tile);
   // rows this CTA writes (none: empty slab, or the split pass wrote them)
   const bool live = valid && r0 < p.rows_per_tile && m_first < nrows && !(p.skip_single && nch == 1);
   const int rows = live ? min(RS, min(p.rows_per_tile - r0, nrows - m_first)) : 0;
@@ -85,13 +86,14 @@ __global__ __launch_bounds__(kMergeThreads) void merge_slab_kernel(MergeParams p
   const PT* src = reinterpret_cast<const PT*>(p.o_part);
   const uint32_t bar_a = smem_u32(&bar);
   // batch of splits [s0, s0 + nb) of the slab's live rows into shared memory:
-  // one copy when the batch holds every split of the grid (the slab is
-  // contiguous), else one per row; splits that a shorter sequence does not have
-  // are not read
+  // one copy when the buffer holds every split of the grid and (`sparse`) the
+  // sequence has most of them (the slab is contiguous; what it does not have
+  // is copied and not used), else one per row, of the sequence's splits alone
+  const bool whole = SB == S && (!p.sparse || 4 * nch >= 3 * S);
   auto gather = [&](int s0, int nb) {
     if (tid == 0) {
-      mbar_expect_tx(bar_a, (uint32_t)(rows * nb * D * sizeof(PT)));
-      if (nb == S)
+      mbar_expect_tx(bar_a, (uint32_t)(rows * (whole ? S : nb) * D * sizeof(PT)));
+      if (whole)
         bulk_load(smem_u32(so), src + slot0 * D, (uint32_t)(rows * S * D * sizeof(PT)), bar_a);
       else
         for (int r = 0; r < rows; ++r)
@@ -199,13 +201,13 @@ __global__ __launch_bounds__(kMergeThreads) void merge_slab_kernel(MergeParams p
   }
 }
 
-template <int D, typename PT>
+template <int D, typename PT, bool WIN = false>
 cudaError_t launch_merge_t(const MergeParams& p, cudaStream_t s) {
   const size_t smem = (size_t)p.batch_splits * p.slab_rows * (D * sizeof(PT) + 8 + 4);
-  cudaError_t e = ensure_max_dynamic_smem<merge_slab_kernel<D, PT>>((int)smem);
+  cudaError_t e = ensure_max_dynamic_smem<merge_slab_kernel<D, PT, WIN>>((int)smem);
   if (e != cudaSuccess) return e;
-  dim3 grid((p.tile_stride + p.slab_rows - 1) / p.slab_rows, p.Hkv * p.row_tiles, p.B);
-  return launch_dep(merge_slab_kernel<D, PT>, grid, dim3(kMergeThreads), smem, s, p);
+  dim3 grid((p.tile_rows + p.slab_rows - 1) / p.slab_rows, p.Hkv * p.row_tiles, p.B);
+  return launch_dep(merge_slab_kernel<D, PT, WIN>, grid, dim3(kMergeThreads), smem, s, p);
 }
 
 }  // namespace
@@ -216,20 +218,30 @@ cudaError_t launch_merge(const MergeParams& p, cudaStream_t s) {
     if (p.d == 256) return launch_merge_t<256, __nv_bfloat16>(p, s);
     return launch_merge_t<512, __nv_bfloat16>(p, s);
   }
+  if (p.window > 0) {
+    if (p.d == 128) return launch_merge_t<128, float, true>(p, s);
+    if (p.d == 256) return launch_merge_t<256, float, true>(p, s);
+    return launch_merge_t<512, float, true>(p, s);
+  }
   if (p.d == 128) return launch_merge_t<128, float>(p, s);
   if (p.d == 256) return launch_merge_t<256, float>(p, s);
   return launch_merge_t<512, float>(p, s);
 }
 
-void merge_shape(int tiles, int tile_stride, int d, int esize, int splits, int sms, int* slab_rows,
+void merge_shape(int tiles, int tile_rows, int d, int esize, int splits, int sms, bool single, int* slab_rows,
                  int* batch_splits) {
-  // the largest slab (32 rows at head_dim 128, else 16; then 8, 4, 2) that
-  // still gives every SM a CTA,
-  // then as many splits per batch as about 100 KB of shared memory holds
+  // the largest slab (32 rows at head_dim 128, else 16; then 8, 4, 2 and, for
+  // `single`, 1) that still gives every SM a CTA,
+  // then as many splits per batch as about 100 KB of shared memory holds (200
+  // KB for `single` where no SM gets a second CTA: few rows of many splits
+  // are bound by the latency of their batches; a chain of 4 tokens at
+  // head_dim 512 with 79 splits takes 24.4 us a call, 28.5 without both)
   int rs = max_slab_rows(d);
-  while (rs > 2 && (rs > tile_stride || (int64_t)tiles * ((tile_stride + rs - 1) / rs) < sms)) rs >>= 1;
+  const int least = single ? 1 : 2;
+  while (rs > least && (rs > tile_rows || (int64_t)tiles * ((tile_rows + rs - 1) / rs) < sms)) rs >>= 1;
   const int per_split = rs * (d * esize + 8 + 4);
-  int sb = (100 * 1024) / per_split;
+  const bool alone = single && (int64_t)tiles * ((tile_rows + rs - 1) / rs) <= sms;
+  int sb = (alone ? 200 : 100) * 1024 / per_split;
   if (sb < 1) sb = 1;
   if (sb > splits) sb = splits;
   *slab_rows = rs;
