@@ -79,8 +79,9 @@ int tree_accept_commit_argmax_kv4(const tv_desc* desc, const int32_t* d_argmax, 
                                   int32_t* d_status, void* stream);
 
 /* Scratch bytes and plan of tree_verify_attn_kv4 (win may be NULL).  Plan
- * kernel 0: CUDA cores; 4: tcgen05 with the cache expanded into tensor
- * memory (bf16). */
+ * kernel 0: CUDA cores (fp32, or more than 64 query heads per KV head);
+ * 4: tcgen05 with the cache expanded into tensor memory; 5: up to 8 rows per
+ * KV head (max_nodes * Hq / Hkv), the cache expanded in registers. */
 int tv_kv4_workspace_size(const tv_desc* desc, const tv_window* win, size_t* bytes);
 int tv_kv4_attn_plan(const tv_desc* desc, const tv_window* win, tv_plan* plan);
 

@@ -13,9 +13,11 @@
  * every row's view are not read, so the call costs what the sinks and the
  * window hold, whatever the prefix length.
  *
- * Conventions are those of tree_verify.h.  The cache keeps every position
- * (rows that left the window are not needed again unless they are sinks; a
- * paged cache may map their pages to any valid page).
+ * Conventions are those of tree_verify.h.  The cache keeps its positions:
+ * a key that left the window keeps its place and is not read again unless it
+ * is a sink, so a paged cache may free its page.  The page table's entries of
+ * 16-position pages that no row sees (wholly in [sinks, prefix_len - window
+ * + 1)) are not read and may hold anything.
  */
 #ifndef TREE_WINDOW_H
 #define TREE_WINDOW_H
