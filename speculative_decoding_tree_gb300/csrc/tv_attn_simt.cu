@@ -9,8 +9,8 @@
 //   M = max_s m_s,  L = sum_s l_s 2^(m_s - M),  O = sum_s O_s 2^(m_s - M) / L.
 // Scores are kept in base-2 units (score * scale * log2 e) so exp2 applies.
 //
-// Work split: CTA (row tile, KV head g, split s, sequence b).  Four warps;
-// warp w owns RPW query rows (row m = node * G + group head).  Keys stream
+// Work split: CTA (row tile, KV head g, split s, sequence b).  Four warps (or
+// simt_warps: the windowed and the 4-bit calls); warp w owns RPW query rows (row m = node * G + group head).  Keys stream
 // through shared memory 32 at a time; for QK each lane owns one key, for PV
 // each lane owns d/32 output columns of every row.
 #include <cfloat>
@@ -50,17 +50,17 @@ __device__ __forceinline__ void load8<__nv_bfloat16>(const __nv_bfloat16* src, f
 // staged: K by 8 channels of a key, V by 8 keys of a channel, one 32-bit word
 // each.  WIN: a sliding window with sinks (KeyMap): the chunk walks virtual
 // keys, and a row's view is applied as a mask on the scores.
-template <typename T, int D, bool KV4 = false, bool WIN = false>
-__global__ __launch_bounds__(128) void attn_simt_kernel(AttnParams p) {
+template <typename T, int D, bool KV4 = false, bool WIN = false, int W = 4>
+__global__ __launch_bounds__(32 * W) void attn_simt_kernel(AttnParams p) {
   constexpr int RPW = 1024 / D;          // rows per warp
-  constexpr int ROWS = 4 * RPW;          // rows per CTA
+  constexpr int ROWS = W * RPW;          // rows per CTA
   constexpr int KS = D + 4;              // padded K row (conflict-free float4 reads by key)
   constexpr int CPL = D / 128;           // float4 output chunks per lane
   extern __shared__ float4 smem_f4[];
   float* qs = reinterpret_cast<float*>(smem_f4);          // [ROWS][D]
   float* ks = qs + ROWS * D;                              // [32][KS]
   float* vs = ks + kKeyTile * KS;                         // [32][D]
-  float* ps = vs + kKeyTile * D;                          // [4 warps][RPW][32]
+  float* ps = vs + kKeyTile * D;                          // [W][RPW][32]
   __shared__ uint64_t s_anc[ROWS];
   __shared__ int s_dep[WIN ? ROWS : 1], s_kdep[WIN ? kMaxNodes : 1];   // depths of the CTA's rows and of the tree
   dep_wait();
@@ -130,6 +130,11 @@ __global__ __launch_bounds__(128) void attn_simt_kernel(AttnParams p) {
   const int64_t n_prefix_tiles = (k_end - k_begin + kKeyTile - 1) / kKeyTile;
   const int n_tree_tiles = has_tree ? (n + kKeyTile - 1) / kKeyTile : 0;
 
+  // a warp without rows only loads (an early end of both loops costs nothing
+  // where a jump past them did: a tree of 8 rows 13.4 and 15.5 us)
+  const bool idle = (KV4 || WIN) && m0 + warp * RPW >= nrows;
+  const int c_end = idle ? 0 : D / 4, j_end = idle ? 0 : kKeyTile;
+
   for (int64_t tile = 0; tile < n_prefix_tiles + n_tree_tiles; ++tile) {
     const bool tree_tile = tile >= n_prefix_tiles;
     const int64_t t0 = tree_tile ? (tile - n_prefix_tiles) * kKeyTile : k_begin + tile * kKeyTile;
@@ -150,10 +155,10 @@ __global__ __launch_bounds__(128) void attn_simt_kernel(AttnParams p) {
             const int i = (int)(pos % kPageSize), c = c8 / 4;
             const uint32_t w = *reinterpret_cast<const uint32_t*>(blk + kv4::k_code(c, i) + (c8 % 4) * 4);
             const float sc = kv4::scale_of(blk[kv4::k_scale(D, c, i)]);
-            lo = make_float4((kv4::nibble(w, 0) - 8) * sc, (kv4::nibble(w, 1) - 8) * sc,
-                             (kv4::nibble(w, 2) - 8) * sc, (kv4::nibble(w, 3) - 8) * sc);
-            hi = make_float4((kv4::nibble(w, 4) - 8) * sc, (kv4::nibble(w, 5) - 8) * sc,
-                             (kv4::nibble(w, 6) - 8) * sc, (kv4::nibble(w, 7) - 8) * sc);
+            float x[8];
+            kv4::expand8(w, x);
+            lo = make_float4(x[0] * sc, x[1] * sc, x[2] * sc, x[3] * sc);
+            hi = make_float4(x[4] * sc, x[5] * sc, x[6] * sc, x[7] * sc);
           } else if (c8 == 0) {
             set_status(p.status, TV_DEV_BAD_PAGE);
           }
@@ -176,10 +181,12 @@ __global__ __launch_bounds__(128) void attn_simt_kernel(AttnParams p) {
           w = *reinterpret_cast<const uint32_t*>(blk + kv4::v_code(ch) + i / 8 * 4);
           sc8 = *reinterpret_cast<const uint2*>(blk + kv4::v_scale(D, i));
         }
+        float x[8];
+        kv4::expand8(w, x);
 #pragma unroll
         for (int t = 0; t < 8; ++t) {
           const uint32_t code = ((t < 4 ? sc8.x : sc8.y) >> (8 * (t & 3))) & 255u;
-          vs[(j0 + t) * D + ch] = (kv4::nibble(w, t) - 8) * kv4::scale_of(code);
+          vs[(j0 + t) * D + ch] = x[t] * kv4::scale_of(code);
         }
       }
     } else
@@ -226,14 +233,13 @@ __global__ __launch_bounds__(128) void attn_simt_kernel(AttnParams p) {
       vd[1] = make_float4(tv[4], tv[5], tv[6], tv[7]);
     }
     __syncthreads();
-
     // scores: lane = key
     float sc[RPW];
 #pragma unroll
     for (int r = 0; r < RPW; ++r) sc[r] = 0.f;
     const float4* krow = reinterpret_cast<const float4*>(ks + lane * KS);
 #pragma unroll 4
-    for (int c = 0; c < D / 4; ++c) {
+    for (int c = 0; c < c_end; ++c) {
       const float4 kv = krow[c];
 #pragma unroll
       for (int r = 0; r < RPW; ++r) {
@@ -279,7 +285,7 @@ __global__ __launch_bounds__(128) void attn_simt_kernel(AttnParams p) {
     __syncwarp();
     // PV: lane owns columns lane*4 + 128*c
 #pragma unroll 4
-    for (int j = 0; j < kKeyTile; ++j) {
+    for (int j = 0; j < j_end; ++j) {
       float4 vv[CPL];
 #pragma unroll
       for (int c = 0; c < CPL; ++c) vv[c] = reinterpret_cast<const float4*>(vs + j * D)[lane + 32 * c];
@@ -337,15 +343,21 @@ __global__ __launch_bounds__(128) void attn_simt_kernel(AttnParams p) {
   }
 }
 
-template <typename T, int D, bool KV4 = false, bool WIN = false>
+// Warps of a CTA that takes more rows than four warps hold
+constexpr int wide_warps(int d) { return d == 512 ? 16 : 8; }
+
+template <typename T, int D, bool KV4 = false, bool WIN = false, int W = 4>
 cudaError_t launch_simt_t(const AttnParams& p, cudaStream_t s) {
+  if constexpr ((KV4 || WIN) && W == 4) {
+    if (p.rows_per_tile > 4 * (1024 / D)) return launch_simt_t<T, D, KV4, WIN, wide_warps(D)>(p, s);
+  }
   constexpr int RPW = 1024 / D;
-  constexpr int ROWS = 4 * RPW;
-  const size_t smem = sizeof(float) * (ROWS * D + kKeyTile * (D + 4) + kKeyTile * D + 4 * RPW * kKeyTile);
-  cudaError_t e = ensure_max_dynamic_smem<attn_simt_kernel<T, D, KV4, WIN>>((int)smem);
+  constexpr int ROWS = W * RPW;
+  const size_t smem = sizeof(float) * (ROWS * D + kKeyTile * (D + 4) + kKeyTile * D + W * RPW * kKeyTile);
+  cudaError_t e = ensure_max_dynamic_smem<attn_simt_kernel<T, D, KV4, WIN, W>>((int)smem);
   if (e != cudaSuccess) return e;
   dim3 grid(p.row_tiles * p.Hkv, p.splits, p.B);
-  return launch_dep(attn_simt_kernel<T, D, KV4, WIN>, grid, dim3(128), smem, s, p);
+  return launch_dep(attn_simt_kernel<T, D, KV4, WIN, W>, grid, dim3(32 * W), smem, s, p);
 }
 
 template <bool KV4, bool WIN>
@@ -365,6 +377,17 @@ cudaError_t launch_simt_any(const AttnParams& p, int dtype, cudaStream_t s) {
 cudaError_t launch_attn_simt(const AttnParams& p, int dtype, cudaStream_t s) {
   return launch_simt_any<false, false>(p, dtype, s);
 }
+
+// Four warps share a tile of keys, and at head_dim 256 and 512 shared memory
+// holds two tiles or one an SM.  Where a sequence has more rows than four warps
+// take, 8 warps (16 at head_dim 512) share the tile: half or a quarter of the
+// loads, and two to four times the warps an SM.
+// 40 rows x 8 heads over 8000 fp32 keys in 4 bits: head_dim 512 6604 us with 4
+// warps and 1367 with 16; with 4 and 8, 256 2411 and 455, 128 578 and 246.
+int simt_warps(const tv_desc* d, int G) { return d->max_nodes * G > 4 * (1024 / d->head_dim) ? wide_warps(d->head_dim) : 4; }
+
+// CTAs an SM holds (shared memory, and at head_dim 128 registers)
+int simt_ctas_per_sm(int d, int warps) { return d == 512 ? 1 : (d == 256 || warps > 4 ? 2 : 4); }
 
 cudaError_t launch_attn_simt_window(const AttnParams& p, int dtype, cudaStream_t s) {
   return launch_simt_any<false, true>(p, dtype, s);

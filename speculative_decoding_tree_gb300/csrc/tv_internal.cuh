@@ -254,6 +254,8 @@ cudaError_t ensure_max_dynamic_smem(int bytes) {
 // Launchers (return cudaError_t of the launch).
 cudaError_t launch_attn_simt(const AttnParams& p, int dtype, cudaStream_t s);
 cudaError_t launch_attn_simt_window(const AttnParams& p, int dtype, cudaStream_t s);
+int simt_warps(const tv_desc* d, int G);          // warps of a windowed or 4-bit CUDA-core CTA
+int simt_ctas_per_sm(int d, int warps);
 cudaError_t launch_attn_simt_kv4(const AttnParams& p, int dtype, cudaStream_t s);
 cudaError_t launch_attn_tc(const AttnParams& p, cudaStream_t s);
 cudaError_t launch_attn_tc_window(const AttnParams& p, cudaStream_t s);

@@ -22,8 +22,16 @@ __device__ __forceinline__ int v_scale(int d, int i) { return 8 * d + i; }
 // scale byte e * 8 + m as a float: 2^(e - 15) (1 + m / 8), from its bits
 __device__ __forceinline__ float scale_of(uint32_t code) { return __uint_as_float((code << 20) + (112u << 23)); }
 
-// value e of a word: bits 4 j for e = 2 j, 16 + 4 j for e = 2 j + 1
-__device__ __forceinline__ int nibble(uint32_t w, int e) { return (int)((w >> ((e >> 1) * 4 + (e & 1) * 16)) & 15u); }
+// the eight values u - 8 of a word (value 2 j at bits 4 j, 2 j + 1 at bits 16 +
+// 4 j): a masked pair is two bf16 numbers 128 + u (no conversion instruction)
+__device__ __forceinline__ void expand8(uint32_t w, float (&x)[8]) {
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const uint32_t pair = ((w >> (4 * j)) & 0x000F000Fu) | 0x43004300u;
+    x[2 * j] = __uint_as_float(pair << 16) - 136.f;
+    x[2 * j + 1] = __uint_as_float(pair & 0xffff0000u) - 136.f;
+  }
+}
 
 // block `blk` of sequence b and KV head g (paged: through the page table;
 // nullptr for a page id out of range)

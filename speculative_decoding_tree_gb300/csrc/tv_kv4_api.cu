@@ -22,12 +22,15 @@ int make_window_plan(const tv_desc* d, const tv_window* w, bool kv4, Plan* p) {
   const int G = d->num_q_heads / d->num_kv_heads;
   // kernel: CUDA cores (0), one tensor-core CTA per row tile (1), and for the
   // 4-bit cache tcgen05 (4) or, for few rows, registers only (5)
-  int kernel = 0, key_tile = 32, rows_per_tile = 4 * (1024 / d->head_dim), ctas_per_sm = 1;
+  const int warps = simt_warps(d, G);
+  int kernel = 0, key_tile = 32, rows_per_tile = warps * (1024 / d->head_dim);
+  int ctas_per_sm = simt_ctas_per_sm(d->head_dim, warps);
   int step = 32;                                     // keys a chunk grows by
   if (!kv4 && tc_supported(d, G)) {
     kernel = 1;
     step = key_tile = tc_key_tile(d->head_dim);
     rows_per_tile = (128 / G) * G;
+    ctas_per_sm = 1;
   } else if (kv4 && kv4_rows_supported(d, G)) {
     kernel = 5;
     key_tile = kv4_rows_key_tile();
@@ -62,12 +65,17 @@ int make_window_plan(const tv_desc* d, const tv_window* w, bool kv4, Plan* p) {
     while (c <= tiles && num_chunks(L, (int)(c * step), tree_tile) > want) ++c;
     chunk = c * step;
   } else {
-    // ragged batch: about four waves of CTAs when the sequences are half the
-    // longest on average, but no chunk below 1920 keys (make_plan's): 64
-    // sequences x 4 rows 163 us with 1920, 156 with 2816 and 163 with 4096
-    // keys; x 32 rows 315 / 297 / 289; 16 trees of 64 .. 256 rows 177 / 184 / 182
-    const double even = (double)units * L / (8.0 * slots);
-    chunk = align_up(even < 1920 ? 1920 : (even > 8192 ? 8192 : (int64_t)even), step);
+    // Ragged batch.  Many units: about four waves of CTAs when the sequences
+    // are half the longest on average, but no chunk below 1920 keys
+    // (make_plan's): 64 sequences x 4 rows 163 us with 1920, 156 with 2816 and
+    // 163 with 4096 keys; x 32 rows 315 / 297 / 289; 16 trees of 64 .. 256 rows
+    // 177 / 184 / 182.  Few units: chunks that give every CTA slot one, down to
+    // 512 keys (4 sequences x 4 rows over 8192 keys 22.0 us, 28.8 with 1920).
+    // The CUDA cores' chunks start at 512 keys: their tiles are short
+    // (8 trees of 40 .. 120 rows over up to 2500 keys 645 us, 980 with 1920).
+    const double wave = (double)units * L / slots, even = wave / 8;
+    const double least = kernel == 0 ? 512 : (wave < 512 ? 512 : (wave < 1920 ? wave : 1920));
+    chunk = align_up((int64_t)(even < least ? least : (even > 8192 ? 8192 : even)), step);
   }
   if (chunk > (int64_t)1 << 30) return TV_ERR_OVERFLOW;
   const int splits = num_chunks(L, (int)chunk, tree_tile);
