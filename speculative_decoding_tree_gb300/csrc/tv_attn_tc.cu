@@ -95,7 +95,10 @@ __device__ __forceinline__ uint64_t low_bits(int n) { return n >= 64 ? ~0ull : (
 // WIN: a sliding window with sinks (KeyMap).  The chunk walks virtual keys; a
 // row's view is applied as a mask on the scores of the tiles that reach below
 // the last row's window, and V rows that no row sees are zeroed like the ones
-// past the prefix end (their contents are not defined: 0 x NaN).
+// past the prefix end (their contents are not defined: 0 x NaN).  Three of a
+// short window's tiles are masked, so the mask is one 64-bit word a row: with a
+// comparison a key, unrolled, 16 trees over windows of 1023 positions took 64
+// us instead of 50 and one decoded token over 4096 18.3 instead of 12.5.
 template <int D, bool WIN = false>
 __global__ void __launch_bounds__(kThreads, 1)
 tv_attn_tc_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUtensorMap tm_q,
@@ -437,7 +440,8 @@ tv_attn_tc_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ 
   } else if (warp == 3) {
     // ============================================================ rows to zero
     // The V chunks with such rows complete here, so that the producer never
-    // waits for a copy to land.
+    // waits for a copy to land (16 trees over windows of 1023 positions 49.6 ->
+    // 47.3 us, a tree of 60 nodes over 4096 17.2 -> 16.4).
     uint32_t parity = 0;                          // one bit per slot
     bool ok = true;
     for (int u = 0; u < npt && ok; ++u) {
