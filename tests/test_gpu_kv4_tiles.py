@@ -110,3 +110,34 @@ def test_the_longest_rows_of_a_batch_merge_alike():
     a.attn()
     torch.cuda.synchronize()
     check_attn(w, a, True)
+
+
+@pytest.mark.parametrize("G,nodes", [(2, 4), (4, 9), (65, 2)])
+def test_blocks_beyond_32_bit_offsets(G, nodes):
+    # the sequences' pages sit at the end of a pool of more than 2^32 bytes of K and of V
+    w = workload(wl.small_variant(5, batch=2, hq=8 * G, hkv=8, prefix=(100, 300), tree=f"random:{nodes},{nodes},4",
+                                  vocab=64, seed=G))
+    a = run(w)
+    b = DeviceKv4Step(w)
+    kb, vb = 8 * 1088, 8 * 1040                          # bytes of a page
+    old, new = b.desc.num_pages, (1 << 32) // vb + 1000
+    k4, v4 = (torch.empty(new * size, dtype=torch.uint8, device="cuda") for size in (kb, vb))
+    k4.view(new, kb)[new - old:] = b.k4.view(old, kb)
+    v4.view(new, vb)[new - old:] = b.v4.view(old, vb)
+    b.k4, b.v4 = k4, v4
+    b.page_table = torch.where(b.page_table >= 0, b.page_table + (new - old), b.page_table)
+    b.desc.num_pages = new
+    b.mask()
+    b.attn()
+    argmax = torch.zeros(w.total_rows, dtype=torch.int32, device="cuda")
+    lens = w.prefix_len.tolist()
+    zero = torch.zeros_like(b.prefix_len)
+    for st in (a, b):
+        st.accept_commit_argmax(argmax)
+    rows = [st.read(lens, zero) for st in (a, b)]
+    torch.cuda.synchronize()
+    assert int(b.status[0]) == 0 and torch.equal(bits(a.out), bits(b.out))
+    for x, y in zip(*rows):
+        assert torch.equal(bits(x), bits(y))
+    assert torch.equal(a.k4.view(old, kb), k4.view(new, kb)[new - old:])
+    assert torch.equal(a.v4.view(old, vb), v4.view(new, vb)[new - old:])
