@@ -9,10 +9,11 @@
 //   M = max_s m_s,  L = sum_s l_s 2^(m_s - M),  O = sum_s O_s 2^(m_s - M) / L.
 // Scores are kept in base-2 units (score * scale * log2 e) so exp2 applies.
 //
-// Work split: CTA (row tile, KV head g, split s, sequence b).  Four warps (or
-// simt_warps: the windowed and the 4-bit calls); warp w owns RPW query rows (row m = node * G + group head).  Keys stream
-// through shared memory 32 at a time; for QK each lane owns one key, for PV
-// each lane owns d/32 output columns of every row.
+// Work split: CTA (row tile, KV head g, split s, sequence b).  Four warps
+// (simt_warps in the windowed and the 4-bit calls); warp w owns RPW query rows
+// (row m = node * G + group head).  Keys stream through shared memory 32 at a
+// time; for QK each lane owns one key, for PV each lane owns d/32 output
+// columns of every row.
 #include <cfloat>
 
 #include "tv_internal.cuh"
