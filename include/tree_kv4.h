@@ -53,7 +53,9 @@ int tv_kv4_cache_bytes(const tv_desc* desc, int64_t* k_bytes, int64_t* v_bytes);
  * rows (sizes the grid).  A sequence whose offsets are invalid
  * (TV_DEV_BAD_OFFSETS), whose start is negative (TV_DEV_BAD_PREFIX) or whose
  * rows do not fit (TV_DEV_CAPACITY) is skipped; rows on an invalid page are
- * skipped (TV_DEV_BAD_PAGE).  No two sequences may write the same block.
+ * skipped (TV_DEV_BAD_PAGE).  A sequence may have no rows (equal offsets): it
+ * reads and writes nothing, and its page-table entries may hold anything.  No
+ * two sequences may write the same block.
  * Errors: TV_ERR_SHAPE (rows < 0, max_rows < 0, or too many blocks),
  * TV_ERR_NULL, TV_ERR_ALIGN, TV_ERR_PAGED, TV_ERR_OVERFLOW, TV_ERR_CUDA.
  * rows = 0 or max_rows = 0 enqueues nothing (d_k and d_v may then be NULL). */

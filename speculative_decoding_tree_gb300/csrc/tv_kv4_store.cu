@@ -164,8 +164,9 @@ __host__ __device__ constexpr uint32_t pack_excess() {
   return c;
 }
 
-// Writes the positions i of one block whose s_row[i] >= 0: row s_row[i] of
-// the head's k_rows / v_rows [rows, D].  xs: [16][D] of shared memory.
+// Writes the positions i of one block whose s_row[i] >= 0 (one at least: row 0
+// is read in place of the others): row s_row[i] of the head's k_rows / v_rows
+// [rows, D].  xs: [16][D] of shared memory.
 // Called by all kThreads threads; ends with a barrier.
 template <typename T, int D>
 __device__ __forceinline__ void store_block(const T* k_rows, const T* v_rows, uint8_t* kb, uint8_t* vb, const int* s_row,
@@ -267,8 +268,10 @@ __device__ __forceinline__ void store_block(const T* k_rows, const T* v_rows, ui
 }
 
 // A sequence's rows for append and read: true (and its first row, count and
-// first position) when they are valid and fit.  Every thread gets the same
-// answer; `lead` reports.
+// first position) when there are any, they are valid and fit.  A sequence
+// without rows touches nothing: it has no row 0 that store_block could load,
+// and its start may name a block that another sequence writes, or no page.
+// Every thread gets the same answer; `lead` reports.
 __device__ bool seq_range(const Kv4RowsParams& p, int b, bool lead, int64_t* r0, int* n, int64_t* start) {
   const int64_t a = p.row_offsets[b], c = p.row_offsets[b + 1];
   const int64_t s = p.start[b];
@@ -287,7 +290,7 @@ __device__ bool seq_range(const Kv4RowsParams& p, int b, bool lead, int64_t* r0,
   *r0 = a;
   *n = (int)(c - a);
   *start = s;
-  return true;
+  return c > a;
 }
 
 // grid (blocks of the longest sequence, KV head, sequence)
