@@ -402,16 +402,15 @@ tv_attn_kv4_kernel(const __grid_constant__ AttnParams p, const __grid_constant__
     // lane's operands at a time) than the copies of all lanes together.
     const int blk_of_lane = lane >> 2;
     // ids(t): page id of the lane's block of tile t (or, contiguous, the block
-    // number), kNone where nothing is loaded (past the end, or seen by no
+    // number), kNoPage where nothing is loaded (past the end, or seen by no
     // row), read two tiles before its use
-    constexpr int kNone = INT_MIN;
     auto ids = [&](int t) -> int {
       const int off = blk_of_lane * kPageSize;
-      if (t >= npt || (t == npt - 1 && off >= tail)) return kNone;
+      if (t >= npt || (t == npt - 1 && off >= tail)) return kNoPage;
       const int64_t pos = tile_pos(t) + off;
-      if (WIN && pos >= p.sinks && pos + kPageSize <= first_pos) return kNone;
+      if (WIN && pos >= p.sinks && pos + kPageSize <= first_pos) return kNoPage;
       const int64_t blk = pos / kPageSize;
-      return p.paged ? p.page_table[(int64_t)b * p.max_pages + blk] : (int)blk;
+      return p.paged ? listed_page(p.page_table[(int64_t)b * p.max_pages + blk]) : (int)blk;
     };
     const uint32_t k_dst = smem_u32(sK) + blk_of_lane * C::KB + (lane & 3) * 16;
     const uint32_t v_dst = smem_u32(sV) + blk_of_lane * C::VB + (lane & 3) * 16;
@@ -429,7 +428,7 @@ tv_attn_kv4_kernel(const __grid_constant__ AttnParams p, const __grid_constant__
       id0 = id1;
       id1 = ids(t + 2);
       int64_t blk = -1;
-      if (raw != kNone) {
+      if (raw != kNoPage) {
         if (!p.paged)
           blk = ((int64_t)b * p.Hkv + g) * p.max_pages + raw;
         else

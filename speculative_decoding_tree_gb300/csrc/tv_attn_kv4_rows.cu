@@ -35,8 +35,6 @@
 // score further above moves it.  A warp keeps its own references, sums and O;
 // its CTA's four warps take alternate spans and join at the end.  Each load
 // buffer is refilled as soon as it has been multiplied, a span ahead.
-#include <climits>
-
 #include "tv_kv4.cuh"
 
 namespace tv {
@@ -172,16 +170,16 @@ __global__ void __launch_bounds__(32 * kWarps, Cfg<D>::CTAS) tv_attn_kv4_rows_ke
     int64_t k, v;
     bool bad_k, bad_v;
   };
-  auto page_of = [&](int sp, int j) -> int {       // page id, or block number; -1 none
+  auto page_of = [&](int sp, int j) -> int {       // page id, or block number; kNoPage: none
     const int64_t v = k_begin + (int64_t)sp * kSpan + j * kPageSize;
-    if (sp >= nsp || v >= k_end) return INT_MIN;
+    if (sp >= nsp || v >= k_end) return kNoPage;
     const int64_t pos = WIN ? km.pos(v) : v;
-    if (WIN && pos >= p.sinks && pos + kPageSize <= first_pos) return INT_MIN;
-    return p.paged ? p.page_table[(int64_t)b * p.max_pages + pos / kPageSize] : (int)(pos / kPageSize);
+    if (WIN && pos >= p.sinks && pos + kPageSize <= first_pos) return kNoPage;
+    return p.paged ? listed_page(p.page_table[(int64_t)b * p.max_pages + pos / kPageSize]) : (int)(pos / kPageSize);
   };
   auto block_of = [&](int id, bool* bad) -> int64_t {
     *bad = false;
-    if (id == INT_MIN) return 0;
+    if (id == kNoPage) return 0;
     if (!p.paged) return ((int64_t)b * p.Hkv + g_head) * p.max_pages + id;
     if (id >= 0 && id < p.num_pages) return (int64_t)id * p.Hkv + g_head;
     *bad = true;

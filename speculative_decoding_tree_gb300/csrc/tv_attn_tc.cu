@@ -290,15 +290,15 @@ tv_attn_tc_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ 
     // paged cache: lane i < 8 owns page i of a key tile; page ids are read
     // well ahead of the copies that use them
     const int oob_row = p.paged ? (int)(p.num_pages * p.Hkv * kPageSize) : 0;
-    auto page_id = [&](int tile) -> int {           // raw page id of this lane's page, or INT_MIN (none)
-      if (!p.paged || tile >= npt || lane >= BN / kPageSize) return INT_MIN;
-      if (k_begin + (int64_t)tile * BN + lane * kPageSize >= k_end) return INT_MIN;
+    auto page_id = [&](int tile) -> int {           // raw page id of this lane's page, or kNoPage (none)
+      if (!p.paged || tile >= npt || lane >= BN / kPageSize) return kNoPage;
+      if (k_begin + (int64_t)tile * BN + lane * kPageSize >= k_end) return kNoPage;
       const int64_t pos = tile_pos(tile) + lane * kPageSize;
-      if (WIN && pos >= p.sinks && pos + kPageSize <= first_pos) return INT_MIN;   // no row sees the page
-      return p.page_table[(int64_t)b * p.max_pages + pos / kPageSize];
+      if (WIN && pos >= p.sinks && pos + kPageSize <= first_pos) return kNoPage;   // no row sees the page
+      return listed_page(p.page_table[(int64_t)b * p.max_pages + pos / kPageSize]);
     };
     auto page_row = [&](int pid) -> int {           // TMA row of a page id, checked where it is used
-      if (pid == INT_MIN) return -1;
+      if (pid == kNoPage) return -1;
       if (pid >= 0 && pid < p.num_pages) return (int)(((int64_t)pid * p.Hkv + g) * kPageSize);
       set_status(p.status, TV_DEV_BAD_PAGE);
       return oob_row;                               // out of range: the copy reads zeros

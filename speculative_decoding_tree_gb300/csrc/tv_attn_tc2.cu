@@ -280,14 +280,14 @@ tv_attn_tc2_kernel(const __grid_constant__ AttnParams p, const __grid_constant__
     int j = junk0 ? 1 : 0, tail_uses = 0;
     bool ok = true;
     const int oob_row = p.paged ? (int)(p.num_pages * p.Hkv * kPageSize) : 0;
-    auto page_id = [&](int tile) -> int {           // raw page id of this lane's page (lanes 0-7), or INT_MIN
-      if (!p.paged || tile >= npt || lane >= BN / kPageSize) return INT_MIN;
+    auto page_id = [&](int tile) -> int {           // raw page id of this lane's page (lanes 0-7), or kNoPage
+      if (!p.paged || tile >= npt || lane >= BN / kPageSize) return kNoPage;
       const int64_t pos = k_begin + (int64_t)tile * BN + lane * kPageSize;
-      if (pos >= k_end) return INT_MIN;
-      return p.page_table[(int64_t)b * p.max_pages + pos / kPageSize];
+      if (pos >= k_end) return kNoPage;
+      return listed_page(p.page_table[(int64_t)b * p.max_pages + pos / kPageSize]);
     };
     auto page_row = [&](int pid) -> int {
-      if (pid == INT_MIN) return -1;
+      if (pid == kNoPage) return -1;
       if (pid >= 0 && pid < p.num_pages) return (int)(((int64_t)pid * p.Hkv + g) * kPageSize);
       set_status(p.status, TV_DEV_BAD_PAGE);
       return oob_row;

@@ -63,7 +63,6 @@
 // numbers with atomic adds.
 #include <cuda.h>
 
-#include <climits>
 #include <mutex>
 
 #include "tc_ptx.cuh"
@@ -355,14 +354,14 @@ tv_attn_tcp_kernel(const __grid_constant__ AttnParams p, const __grid_constant__
         q_loaded = true;
         return true;
       };
-      auto page_id = [&](int tile) -> int {         // raw page id of this lane's page, or INT_MIN (none)
-        if (!p.paged || tile >= npt || lane >= BN / kPageSize) return INT_MIN;
+      auto page_id = [&](int tile) -> int {         // raw page id of this lane's page, or kNoPage (none)
+        if (!p.paged || tile >= npt || lane >= BN / kPageSize) return kNoPage;
         const int64_t pos = k_begin + (int64_t)tile * BN + lane * kPageSize;
-        if (pos >= k_end) return INT_MIN;
-        return p.page_table[(int64_t)b * p.max_pages + pos / kPageSize];
+        if (pos >= k_end) return kNoPage;
+        return listed_page(p.page_table[(int64_t)b * p.max_pages + pos / kPageSize]);
       };
       auto page_row = [&](int pid) -> int {         // TMA row of a page id, checked where it is used
-        if (pid == INT_MIN) return -1;
+        if (pid == kNoPage) return -1;
         if (pid >= 0 && pid < p.num_pages) return (int)(((int64_t)pid * p.Hkv + g) * kPageSize);
         set_status(p.status, TV_DEV_BAD_PAGE);
         return oob_row;                             // out of range: the copy reads zeros
