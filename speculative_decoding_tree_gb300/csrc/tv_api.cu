@@ -78,11 +78,10 @@ int make_plan(const tv_desc* d, Plan* p) {
   // two or more 128-row tiles per KV head: CTA pairs (cta_group::2) share
   // each K/V tile -- for one sequence
   const bool pairs = tc && row_tiles >= 2 && d->batch == 1;
-  // a batch on head_dim 128 with a bf16 output: persistent CTA pairs, one CTA
-  // per SM, take (sequence, KV head, pair of row tiles, chunk) units from a
-  // work counter and share each K/V tile through multicast loads
+  // a batch on head_dim 128 with a bf16 output: persistent CTAs, one per SM,
+  // take (sequence, KV head, row tile, chunk) units from a work counter
   const bool persist = tc && d->batch > 1 && d->head_dim == 128 && !d->out_f32;
-  const int launched_tiles = (pairs || persist) ? 2 * ((row_tiles + 1) / 2) : row_tiles;
+  const int launched_tiles = pairs ? 2 * ((row_tiles + 1) / 2) : row_tiles;
   int64_t units = (int64_t)d->batch * d->num_kv_heads * launched_tiles;
   int64_t sms = num_sms();
   int64_t L = d->max_prefix;
@@ -128,7 +127,9 @@ int make_plan(const tv_desc* d, Plan* p) {
   p->pub.chunk = (int)chunk;
   p->pub.row_tiles = row_tiles;
   p->pub.rows_per_tile = rows_per_tile;
-  p->pub.grid_ctas = (int)(persist ? (grid < 2 * (sms / 2) ? grid : 2 * (sms / 2)) : grid);
+  // (the persistent kernel's count is even; a CTA that finds no unit ends at once)
+  const int64_t most = 2 * (sms / 2), even = 2 * ((grid + 1) / 2);
+  p->pub.grid_ctas = (int)(persist ? (even < most ? even : most) : grid);
   p->counter_bytes = persist ? 256 : 0;
   // partials are tile-major: every (split, sequence, KV head, row tile) owns
   // tile_stride rows (128 for the tensor-core kernel, whose epilogue stores
@@ -230,6 +231,7 @@ AttnParams attn_params(const tv_desc* d, const Plan& pl, const void* q, const vo
   float scale = d->scale > 0.f ? d->scale : 1.0f / std::sqrt((float)d->head_dim);
   a.scale_log2 = scale * 1.4426950408889634f;
   a.chunk = pl.pub.chunk; a.tree_tile = pl.tree_tile; a.splits = pl.pub.num_splits;
+  a.grid_ctas = pl.pub.grid_ctas;
   a.rows_per_tile = pl.pub.rows_per_tile; a.row_tiles = pl.pub.row_tiles;
   a.tile_stride = pl.tile_stride;
   a.part_bf16 = part_bf16(d, pl);

@@ -46,6 +46,7 @@ struct AttnParams {
   int chunk;                 // keys per split (multiple of the kernel's key tile)
   int tree_tile;             // 0, or the key tile when the tree may take a split of its own (num_chunks)
   int splits;                // splits in the grid (covers max_prefix)
+  int grid_ctas;             // CTAs of the persistent kernel
   int rows_per_tile;         // query rows per row tile (node x group head)
   int row_tiles;
   int tile_stride;           // partial rows reserved per tile (>= rows_per_tile)
@@ -271,7 +272,6 @@ cudaError_t launch_attn_tc2(const AttnParams& p, cudaStream_t s);
 cudaError_t launch_attn_tcp(const AttnParams& p, cudaStream_t s);
 cudaError_t launch_attn_kv4(const AttnParams& p, int columns, cudaStream_t s);
 cudaError_t launch_attn_kv4_rows(const AttnParams& p, cudaStream_t s);
-int64_t tcp_units(const AttnParams& p);
 cudaError_t launch_merge(const MergeParams& p, cudaStream_t s);
 cudaError_t launch_tree_mask(const int32_t* parents, const int32_t* offs, uint64_t* anc, int32_t* depth,
                              int32_t* status, int B, int R, int max_nodes, cudaStream_t s);
