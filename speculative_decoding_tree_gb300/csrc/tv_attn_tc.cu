@@ -353,10 +353,12 @@ tv_attn_tc_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ 
         }
       }
     }
-    // drain: every copy this warp started has landed before the CTA exits
+    // drain: every copy this warp started has landed before the CTA exits, after
+    // a timeout too (abort_flag is up then, and these waits have their own)
     if (lane == 0) {
-      mbar_wait(Q_FULL, 0, abort_flag, kWaitNs);
-      for (int jj = (j > NS ? j - NS : 0); jj < j; ++jj) mbar_wait(FULL(jj % NS), (jj / NS) & 1, abort_flag, kWaitNs);
+      int spare = 0;
+      mbar_wait(Q_FULL, 0, &spare, kWaitNs);
+      for (int jj = (j > NS ? j - NS : 0); jj < j; ++jj) mbar_wait(FULL(jj % NS), (jj / NS) & 1, &spare, kWaitNs);
     }
   } else if (warp == 1) {
     // ============================================================ MMA issuer
@@ -411,7 +413,8 @@ tv_attn_tc_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ 
       }
       // every MMA this thread issued has finished before tensor memory is freed
       mma_commit(FIN);
-      mbar_wait(FIN, 0, abort_flag, kWaitNs);
+      int spare = 0;                              // (not abort_flag: this wait also follows a timeout)
+      mbar_wait(FIN, 0, &spare, kWaitNs);
     }
   } else if (warp == 2) {
     // ============================================================ partials store

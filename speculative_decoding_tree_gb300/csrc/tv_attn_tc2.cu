@@ -382,6 +382,14 @@ tv_attn_tc2_kernel(const __grid_constant__ AttnParams p, const __grid_constant__
         }
       }
     }
+    // drain: the copies of both CTAs (the leader's barriers count them) have
+    // landed before the pair's last barrier, after a timeout too (abort_flag is
+    // up then, and these waits have their own)
+    if (lane == 0 && leader) {
+      int spare = 0;
+      mbar_wait(Q_FULL, 0, &spare, kWaitNs);
+      for (int jj = (j > NS ? j - NS : 0); jj < j; ++jj) mbar_wait(FULL(jj % NS), (jj / NS) & 1, &spare, kWaitNs);
+    }
   } else if (warp == 1) {
     // ============================================================ MMA issuer (leader)
     if (lane == 0 && rank == 0) {
@@ -434,7 +442,8 @@ tv_attn_tc2_kernel(const __grid_constant__ AttnParams p, const __grid_constant__
         }
       }
       mma_commit_pair(FIN);
-      mbar_wait(FIN, 0, abort_flag, kWaitNs);
+      int spare = 0;                              // (not abort_flag: this wait also follows a timeout)
+      mbar_wait(FIN, 0, &spare, kWaitNs);
     }
   } else if (warp == 2) {
     // ============================================================ partials store
@@ -647,7 +656,10 @@ tv_attn_tc2_kernel(const __grid_constant__ AttnParams p, const __grid_constant__
   // commit: once the peer has seen it, no arrive from the pair's MMAs is in
   // flight towards its shared memory, and an execution-only cluster barrier
   // keeps either CTA from leaving before the other is done.
-  if (active && warp == 1 && lane == 0 && rank != 0) mbar_wait(FIN, 0, abort_flag, kWaitNs);
+  if (active && warp == 1 && lane == 0 && rank != 0) {
+    int spare = 0;                                  // (not abort_flag: this wait also follows a timeout)
+    mbar_wait(FIN, 0, &spare, kWaitNs);
+  }
   tc_fence_before();
   __syncthreads();
   if (tid == 0 && *abort_flag) set_status(p.status, TV_DEV_TIMEOUT);

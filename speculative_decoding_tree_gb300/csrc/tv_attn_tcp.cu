@@ -298,7 +298,7 @@ tv_attn_tcp_kernel(const __grid_constant__ AttnParams p, const __grid_constant__
     }
   } else if (warp == 0) {
     // ============================================================ producer
-    int j = 0, tail_uses = 0, uq = 0, k = 0;
+    int j = 0, tail_uses = 0, uq = 0, k = 0, q_loads = 0;
     bool ok = true;
     const int oob_row = p.paged ? (int)(p.num_pages * p.Hkv * kPageSize) : 0;
     while (ok) {
@@ -321,6 +321,7 @@ tv_attn_tcp_kernel(const __grid_constant__ AttnParams p, const __grid_constant__
             tma_load_3d(smem_u32(sQ + kb * (BM * 128)), &tm_q, Q_FULL, kb * 64, g * G, q_node);
         }
         q_loaded = true;
+        ++q_loads;
         return true;
       };
       auto page_id = [&](int tile) -> int {         // raw page id of this lane's page, or kNoPage (none)
@@ -403,10 +404,12 @@ tv_attn_tcp_kernel(const __grid_constant__ AttnParams p, const __grid_constant__
       k ^= 1;
       ++uq;
     }
-    // drain: every copy this warp started has landed before the CTA exits
+    // drain: every copy this warp started has landed before the CTA exits, after
+    // a timeout too (abort_flag is up then, and these waits have their own)
     if (lane == 0) {
-      if (uq > 0) mbar_wait(Q_FULL, (uq - 1) & 1, abort_flag, kWaitNs);
-      for (int jj = (j > NS ? j - NS : 0); jj < j; ++jj) mbar_wait(FULL(jj % NS), (jj / NS) & 1, abort_flag, kWaitNs);
+      int spare = 0;
+      if (q_loads > 0) mbar_wait(Q_FULL, (q_loads - 1) & 1, &spare, kWaitNs);
+      for (int jj = (j > NS ? j - NS : 0); jj < j; ++jj) mbar_wait(FULL(jj % NS), (jj / NS) & 1, &spare, kWaitNs);
     }
   } else if (warp == 1) {
     // ============================================================ MMA issuer
@@ -478,7 +481,8 @@ tv_attn_tcp_kernel(const __grid_constant__ AttnParams p, const __grid_constant__
       }
       // every MMA this thread issued has finished before tensor memory is freed
       mma_commit(FIN);
-      mbar_wait(FIN, 0, abort_flag, kWaitNs);
+      int spare = 0;                              // (not abort_flag: this wait also follows a timeout)
+      mbar_wait(FIN, 0, &spare, kWaitNs);
     }
   } else if (warp >= kFirstSoftmaxWarp) {
     // ============================================================ softmax

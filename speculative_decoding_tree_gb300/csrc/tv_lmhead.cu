@@ -131,9 +131,10 @@ lmhead_argmax_kernel(const __grid_constant__ LmParams p, const __grid_constant__
           tma_load_2d(smem_u32(st + W_BYTES), &tm_h, FULL(slot), kc * LKC, rt * LM);
         }
       }
-      // every copy started has landed before the CTA exits
+      // every copy started has landed before the CTA exits, after a timeout too
+      int spare = 0;
       for (int j = (it > LNS ? it - LNS : 0); j < it; ++j)
-        mbar_wait(FULL(j % LNS), (j / LNS) & 1, abort_flag, kLWaitNs);
+        mbar_wait(FULL(j % LNS), (j / LNS) & 1, &spare, kLWaitNs);
     }
   } else if (warp == 1) {
     // ============================================================ MMA issuer
@@ -172,7 +173,8 @@ lmhead_argmax_kernel(const __grid_constant__ LmParams p, const __grid_constant__
       }
       // every MMA issued has finished before tensor memory is freed
       mma_commit(FIN);
-      mbar_wait(FIN, 0, abort_flag, kLWaitNs);
+      int spare = 0;                              // (not abort_flag: this wait also follows a timeout)
+      mbar_wait(FIN, 0, &spare, kLWaitNs);
     }
   } else if (warp >= 4) {
     // ============================================================ epilogue
