@@ -8,6 +8,8 @@ torch, and calls the library; it computes nothing itself.
 """
 from __future__ import annotations
 
+import contextlib
+
 import torch
 
 from . import (BF16, F32, make_desc, make_expand_desc, tree_accept_commit, tree_accept_commit_sampled,
@@ -18,6 +20,22 @@ from . import (BF16, F32, make_desc, make_expand_desc, tree_accept_commit, tree_
                tree_accept_commit_argmax_kv4, tv_kv4_append, tv_kv4_cache_bytes, tv_kv4_read, tv_kv4_workspace_size)
 
 _DT = {torch.float32: F32, torch.bfloat16: BF16}
+
+
+def _torch_stream(stream):
+    return torch.cuda.ExternalStream(stream) if isinstance(stream, int) else stream
+
+
+def _on(stream):
+    """A context in which torch allocates and copies on `stream` (None: the current one)."""
+    return contextlib.nullcontext() if stream is None else torch.cuda.stream(_torch_stream(stream))
+
+
+def _keep(stream, *tensors):
+    """The tensors' memory is not given on before `stream` has passed this point."""
+    if stream is not None:
+        for t in tensors:
+            t.record_stream(_torch_stream(stream))
 
 
 class DeviceStep:
@@ -159,17 +177,25 @@ class DeviceKv4Step(DeviceStep):
         return torch.tensor([0] + torch.tensor(counts).cumsum(0).tolist(), dtype=torch.int32, device=self.device)
 
     def append(self, k, v, counts, start, stream=None):
-        """Write k, v [Hkv, sum counts, d] at positions start[b] + i."""
-        tv_kv4_append(self.desc, k.shape[1], max(counts), k, v, self._offsets(counts), start, self.k4, self.v4,
-                      self.page_table, self.status, stream)
+        """Write k, v [Hkv, sum counts, d] at positions start[b] + i.  With a
+        stream, the inputs are kept from reuse until it has read them; that it
+        runs after what made them is the caller's."""
+        with _on(stream):                                # the offsets live and die on the call's stream
+            tv_kv4_append(self.desc, k.shape[1], max(counts), k, v, self._offsets(counts), start, self.k4, self.v4,
+                          self.page_table, self.status, stream)
+        _keep(stream, k, v, start)
 
     def read(self, counts, start, stream=None):
-        """The values at positions start[b] + i, [Hkv, sum counts, d] each."""
-        k = torch.empty(self.desc.num_kv_heads, sum(counts), self.desc.head_dim, dtype=self.q.dtype,
-                        device=self.device)
-        v = torch.empty_like(k)
-        tv_kv4_read(self.desc, k.shape[1], max(counts), self.k4, self.v4, self.page_table, self._offsets(counts),
-                    start, k, v, self.status, stream)
+        """The values at positions start[b] + i, [Hkv, sum counts, d] each;
+        with a stream, tensors of that stream, as torch's are under
+        torch.cuda.stream(stream)."""
+        with _on(stream):
+            k = torch.empty(self.desc.num_kv_heads, sum(counts), self.desc.head_dim, dtype=self.q.dtype,
+                            device=self.device)
+            v = torch.empty_like(k)
+            tv_kv4_read(self.desc, k.shape[1], max(counts), self.k4, self.v4, self.page_table, self._offsets(counts),
+                        start, k, v, self.status, stream)
+        _keep(stream, start)
         return k, v
 
     def attn(self, stream=None):
