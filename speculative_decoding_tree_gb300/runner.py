@@ -17,7 +17,8 @@ from . import (BF16, F32, make_desc, make_expand_desc, tree_accept_commit, tree_
                tv_expand_workspace_size, tv_tree_expand_step, tv_workspace_size, make_lmhead_desc,
                tv_lm_head_argmax, tv_lm_head_workspace_size, tree_accept_commit_argmax,
                make_window, tree_verify_attn_window, tv_window_workspace_size, tree_verify_attn_kv4,
-               tree_accept_commit_argmax_kv4, tv_kv4_append, tv_kv4_cache_bytes, tv_kv4_read, tv_kv4_workspace_size)
+               tree_accept_commit_argmax_kv4, tv_kv4_append, tv_kv4_cache_bytes, tv_kv4_read, tv_kv4_workspace_size,
+               tv_attn_plan, tv_kv4_attn_plan, tv_window_attn_plan)
 
 _DT = {torch.float32: F32, torch.bfloat16: BF16}
 
@@ -56,7 +57,6 @@ class DeviceStep:
             out_f32=int(out_f32))
         to = lambda t: None if t is None else t.to(dev).contiguous()
         self.q, self.k_tree, self.v_tree = to(w.q), to(w.k_tree), to(w.v_tree)
-        self.k_cache, self.v_cache = to(w.k_cache), to(w.v_cache)
         self.page_table = to(w.page_table)
         self.prefix_len = to(w.prefix_len)
         self.node_offsets = to(w.node_offsets)
@@ -73,8 +73,15 @@ class DeviceStep:
         self.accept_len = torch.zeros(B, dtype=torch.int32, device=dev)
         self.path = torch.zeros(B, mn, dtype=torch.int32, device=dev)
         self.tokens = torch.zeros(B, mn, dtype=torch.int32, device=dev)
-        self.ws_bytes = tv_workspace_size(self.desc, self.vocab)
-        self.workspace = torch.empty(max(self.ws_bytes, 256), dtype=torch.uint8, device=dev)
+        self._buffers(to)
+
+    def _buffers(self, to):
+        """The cache and the calls' workspace."""
+        self.k_cache, self.v_cache = to(self.w.k_cache), to(self.w.v_cache)
+        self.ws_bytes, self.workspace = self._workspace(tv_workspace_size(self.desc, self.vocab))
+
+    def _workspace(self, size):
+        return size, torch.empty(max(size, 256), dtype=torch.uint8, device=self.device)
 
     # one call each ------------------------------------------------------
     def mask(self, stream=None):
@@ -121,55 +128,70 @@ class DeviceStep:
         self.attn(stream)
         self.accept_commit(stream)
 
+    def plan(self):
+        """The plan of this step's attention."""
+        return tv_attn_plan(self.desc)
+
     def kernels_per_step(self):
         """Our kernel launches in one step: mask, split, merge (skipped when
         the plan has one key chunk), argmax, walk + commit."""
-        from . import tv_attn_plan
-        return 4 + (1 if tv_attn_plan(self.desc)["num_splits"] > 1 else 0)
+        return 4 + (1 if self.plan()["num_splits"] > 1 else 0)
 
 
 class DeviceWindowStep(DeviceStep):
     """A verify step whose rows see a sliding window and the first positions
-    (sinks) of the prefix; acceptance and commit are DeviceStep's."""
+    (sinks) of the prefix; acceptance and commit are DeviceStep's.  The
+    windowed attention is one call: it has no halves."""
 
     def __init__(self, w, window, sinks=0, **kw):
-        super().__init__(w, **kw)
         self.win = make_window(window, sinks)
-        self.attn_ws_bytes = tv_window_workspace_size(self.desc, self.win)
-        self.attn_workspace = torch.empty(max(self.attn_ws_bytes, 256), dtype=torch.uint8, device=self.device)
+        super().__init__(w, **kw)
+
+    def _buffers(self, to):
+        super()._buffers(to)
+        self.attn_ws_bytes, self.attn_workspace = self._workspace(tv_window_workspace_size(self.desc, self.win))
 
     def attn(self, stream=None):
         tree_verify_attn_window(self.desc, self.win, self.q, self.k_cache, self.v_cache, self.page_table,
                                 self.prefix_len, self.node_offsets, self.k_tree, self.v_tree, self.anc, self.depth,
                                 self.out, self.attn_workspace, self.attn_ws_bytes, self.status, stream)
 
+    def plan(self):
+        return tv_window_attn_plan(self.desc, self.win)
+
+    def partials(self, stream=None):
+        raise NotImplementedError("the windowed attention has no call of its own for its partials: use attn")
+
+    def merge(self, stream=None):
+        raise NotImplementedError("the windowed attention has no call of its own for its merge: use attn")
+
 
 class DeviceKv4Step(DeviceStep):
     """A verify step on a cache held in 4 bits (win: (window, sinks) or None).
-    The workload's prefix rows are written by tv_kv4_append; accept_commit
-    walks on a given argmax and quantises the accepted rows."""
+    The workload's prefix rows are written by tv_kv4_append; acceptance walks
+    on a given target argmax and quantises the accepted rows."""
 
     def __init__(self, w, win=None, **kw):
-        super().__init__(w, **kw)
         self.win = None if win is None else make_window(*win)
+        super().__init__(w, **kw)
+
+    def _buffers(self, to):
         kb, vb = tv_kv4_cache_bytes(self.desc)
         self.k4 = torch.zeros(kb, dtype=torch.uint8, device=self.device)
         self.v4 = torch.zeros(vb, dtype=torch.uint8, device=self.device)
-        self.attn_ws_bytes = tv_kv4_workspace_size(self.desc, self.win)
-        self.attn_workspace = torch.empty(max(self.attn_ws_bytes, 256), dtype=torch.uint8, device=self.device)
+        self.attn_ws_bytes, self.attn_workspace = self._workspace(tv_kv4_workspace_size(self.desc, self.win))
         k, v, lens = self._prefix_rows()
-        self.k_cache = self.v_cache = None
-        self.append(k, v, lens, torch.zeros_like(self.prefix_len))
+        self.append(to(k), to(v), lens, torch.zeros_like(self.prefix_len))
 
     def _prefix_rows(self):
         """The prefix of every sequence as [Hkv, sum P, d] rows, and their counts."""
-        lens = self.w.prefix_len.tolist()
+        w, lens = self.w, self.w.prefix_len.tolist()
         rows = []
-        for x in (self.k_cache, self.v_cache):
-            if self.page_table is None:
+        for x in (w.k_cache, w.v_cache):
+            if w.page_table is None:
                 rows.append([x[b, :, :n] for b, n in enumerate(lens)])
             else:
-                flat = [x[self.page_table[b].long()].transpose(0, 1).flatten(1, 2) for b in range(len(lens))]
+                flat = [x[w.page_table[b].long()].transpose(0, 1).flatten(1, 2) for b in range(len(lens))]
                 rows.append([f[:, :n] for f, n in zip(flat, lens)])
         return torch.cat(rows[0], 1).contiguous(), torch.cat(rows[1], 1).contiguous(), lens
 
@@ -207,6 +229,32 @@ class DeviceKv4Step(DeviceStep):
         tree_accept_commit_argmax_kv4(self.desc, argmax, self.draft, self.parents, self.node_offsets, self.k_tree,
                                       self.v_tree, self.k4, self.v4, self.page_table, self.prefix_len,
                                       self.accept_len, self.path, self.tokens, self.status, stream)
+
+    def step(self, argmax, stream=None):
+        """One verify step on the target's argmax [rows] int32 (device): mask,
+        attention, walk + commit."""
+        self.mask(stream)
+        self.attn(stream)
+        self.accept_commit_argmax(argmax, stream)
+
+    def plan(self):
+        return tv_kv4_attn_plan(self.desc, self.win)
+
+    def kernels_per_step(self):
+        """Mask, split, merge (skipped when the plan has one key chunk), walk + commit."""
+        return 3 + (1 if self.plan()["num_splits"] > 1 else 0)
+
+    def partials(self, stream=None):
+        raise NotImplementedError("the 4-bit cache's attention has no call of its own for its partials: use attn")
+
+    def merge(self, stream=None):
+        raise NotImplementedError("the 4-bit cache's attention has no call of its own for its merge: use attn")
+
+    def accept_commit(self, stream=None):
+        raise NotImplementedError("the 4-bit cache is committed on a given argmax: use accept_commit_argmax")
+
+    def accept_commit_sampled(self, temperature, seed, offset, stream=None):
+        raise NotImplementedError("the 4-bit cache is committed on a given argmax: use accept_commit_argmax")
 
 
 class DeviceExpand:
@@ -290,12 +338,15 @@ def main(argv=None):
     ap.add_argument("--attn-only", action="store_true", help="mask and attention only")
     ap.add_argument("--sampled", type=float, default=0.0,
                     help="temperature > 0: sampled verification (tree_accept_commit_sampled)")
-    ap.add_argument("--window", default="", help="W,S: rows see the last W and the first S positions (attention only)")
-    ap.add_argument("--kv4", action="store_true", help="the prefix in a 4-bit cache (attention only; with --window too)")
+    ap.add_argument("--window", default="", help="W,S: rows see the last W and the first S positions")
+    ap.add_argument("--kv4", action="store_true",
+                    help="the prefix in a 4-bit cache (with --window too); acceptance on the logits' argmax")
     ap.add_argument("--expand", default="", help="run a dynamic-expansion workload instead (eagle2, batched)")
     ap.add_argument("--lm-head", default="", help="run a fused lm_head + argmax workload instead (qwen, batched)")
     ap.add_argument("--vocab", type=int, default=0, help="with --lm-head: a smaller vocabulary (e.g. for a profiler)")
     a = ap.parse_args(argv)
+    if a.kv4 and a.sampled > 0:
+        ap.error("--sampled: the 4-bit cache is committed on a given argmax only")
     _build.build()
     if a.lm_head:
         spec = wl.LMHEAD_CONFIGS[a.lm_head]
@@ -319,7 +370,7 @@ def main(argv=None):
                          argmax_fn=lambda x: torch.argmax(x.float(), dim=1))   # plants the draft tokens
     win = tuple(int(x) for x in a.window.split(",")) if a.window else None
     st = DeviceKv4Step(w, win) if a.kv4 else (DeviceWindowStep(w, *win) if win else DeviceStep(w))
-    a.attn_only = a.attn_only or a.kv4 or win is not None
+    target = st.logits.float().argmax(1).to(torch.int32) if a.kv4 else None
     p0 = st.prefix_len.clone()
     for _ in range(a.steps):
         st.prefix_len.copy_(p0)
@@ -330,6 +381,8 @@ def main(argv=None):
             st.mask()
             st.attn()
             st.accept_commit_sampled(a.sampled, 1234, _)
+        elif a.kv4:
+            st.step(target)
         else:
             st.step()
     torch.cuda.synchronize()
