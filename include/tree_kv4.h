@@ -27,7 +27,9 @@
  * The capacity is a multiple of 16 in both cases.
  *
  * desc->dtype is the type of queries, of the tree's K/V and of the rows
- * written and read.  Everything else follows tree_verify.h: buffers are the
+ * written and read.  The calls on the cache alone (tv_kv4_cache_bytes,
+ * tv_kv4_append, tv_kv4_read) have no tree: the descriptor's max_nodes and
+ * total_rows are not looked at.  Everything else follows tree_verify.h: buffers are the
  * caller's, device pointers 16-byte aligned, host errors before anything is
  * enqueued, device faults OR-ed into *d_status.
  */

@@ -112,6 +112,16 @@ int validate_kv4(const tv_desc* d) {
   return d->capacity % kPageSize ? TV_ERR_SHAPE : TV_OK;
 }
 
+// The descriptor of calls on the cache alone: it has no tree, so max_nodes and
+// total_rows may hold anything.
+int validate_cache(const tv_desc* d) {
+  if (!d) return TV_ERR_NULL;
+  tv_desc c = *d;
+  c.max_nodes = 1;
+  c.total_rows = c.batch;
+  return validate_kv4(&c);
+}
+
 int plan_of(const tv_desc* d, const tv_window* w, bool kv4, Plan* p) {
   int rc = kv4 ? validate_kv4(d) : validate(d);
   if (rc) return rc;
@@ -170,7 +180,7 @@ int attention(const tv_desc* d, const tv_window* w, bool kv4, const void* q, con
 int rows_params(const tv_desc* d, int64_t rows, int64_t max_rows, const void* k, const void* v,
                 const int32_t* offs, const int32_t* start, const void* k4, const void* v4, const int32_t* pt,
                 int32_t* st, Kv4RowsParams* p) {
-  const int rc = validate_kv4(d);
+  const int rc = validate_cache(d);
   if (rc) return rc;
   if (rows < 0 || max_rows < 0 || rows > ((int64_t)1 << 31) - 1) return TV_ERR_SHAPE;
   const bool some = rows > 0 && max_rows > 0;
@@ -224,7 +234,7 @@ int tree_verify_attn_window(const tv_desc* desc, const tv_window* win, const voi
 }
 
 int tv_kv4_cache_bytes(const tv_desc* desc, int64_t* k_bytes, int64_t* v_bytes) {
-  const int rc = validate_kv4(desc);
+  const int rc = validate_cache(desc);
   if (rc) return rc;
   if (!k_bytes || !v_bytes) return TV_ERR_NULL;
   // below the fp32/bf16 cache's size, which validate() checked against int64
