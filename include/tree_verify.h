@@ -191,6 +191,9 @@ int tv_build_tree_mask(const tv_desc* desc, const int32_t* d_parents, const int3
  * computed in fp32 (no TF32); bf16 inputs are multiplied in bf16 with fp32
  * accumulation and an fp32 softmax.  d_page_table is NULL for a contiguous
  * cache.  The cache is only read.  Runs tv_attn_partials then tv_attn_merge.
+ * A row's answer does not depend on other sequences' rows, on cache rows past
+ * its prefix, or on K that it does not see.  V of a node it does not see must
+ * be finite within its own sequence (its weight of 0 multiplies it).
  * ADR-037 phase rows E1.1-E1.5 and E4b.6 (tree attention as flash-decode
  * with a reduce kernel merging the split-KV partials). */
 int tree_verify_attn(const tv_desc* desc, const void* d_q, const void* d_k_cache, const void* d_v_cache,

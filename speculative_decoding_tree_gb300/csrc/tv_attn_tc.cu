@@ -19,8 +19,9 @@
 //   warp 1      owns tensor memory; lane 0 issues tcgen05.mma:
 //               S(t) = Q K(t)^T into one of two 128-column TMEM buffers, then
 //               O += P(t-1) V(t-1) with P read from TMEM.
-//   warp 3      completes the V chunks whose rows past the prefix end, or seen
-//               by no row of the query tile, have to be zeros.
+//   warp 3      completes the V chunks with rows that have to be zeros: past
+//               the prefix end or the tree's nodes, or seen by no row of the
+//               query tile.
 //   warps 4-11  softmax, two threads per query row (its TMEM lane), each
 //               taking half of the tile's keys: load the S half-row, mask,
 //               exchange the half-row maxima, P = 2^(s*c - m) written back
@@ -263,11 +264,17 @@ tv_attn_tc_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ 
   const int T = npt + (has_tree ? 1 : 0);
   const int tail_valid = npt > 0 ? (int)(k_end - (k_begin + (int64_t)(npt - 1) * BN)) : BN;
 
-  // V rows of a prefix tile that have to be zeros: [z0, z1) (seen by no row)
-  // and [ze, BN) (past the end); false: none
-  auto zero_rows = [&](int tile, int* z0, int* z1, int* ze) -> bool {
+  // V rows of a tile that have to be zeros: [z0, z1) (seen by no row) and
+  // [ze, zt) (past the end); false: none
+  auto zero_rows = [&](int tile, int* z0, int* z1, int* ze, int* zt) -> bool {
     *z0 = *z1 = 0;
+    if (tile == npt) {                               // the tree
+      *ze = n;
+      *zt = tree_keys(n);
+      return *ze < *zt;
+    }
     *ze = tile == npt - 1 ? tail_valid : BN;
+    *zt = BN;
     if (WIN) {
       const int64_t p0 = tile_pos(tile);
       *z0 = (int)min((int64_t)*ze, max((int64_t)0, p.sinks - p0));
@@ -318,8 +325,8 @@ tv_attn_tc_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ 
         const int tile = kind == 0 ? t : t - 1;
         if ((kind == 0 && t >= T) || (kind == 1 && t < 1)) continue;
         const bool tree = (tile == npt);
-        int z0, z1, ze;
-        const bool fix = kind == 1 && !tree && zero_rows(tile, &z0, &z1, &ze);   // warp 3 completes the chunk
+        int z0, z1, ze, zt;
+        const bool fix = kind == 1 && zero_rows(tile, &z0, &z1, &ze, &zt);   // warp 3 completes the chunk
         for (int c = 0; c < CPT && ok; ++c, ++j) {
           const int slot = j % NS, use = j / NS;
           if (use > 0 && !__all_sync(kAll, mbar_wait(EMPTY(slot), (use - 1) & 1, abort_flag, kWaitNs))) {
@@ -395,6 +402,7 @@ tv_attn_tc_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ 
           const uint32_t pbuf = tmem + (uint32_t)((u & 1) * 128);
           if (!mbar_wait(P_FULL(u & 1), (u >> 1) & 1, abort_flag, kWaitNs)) { ok = false; break; }
           tc_fence_after();
+          const int steps = u == npt ? tree_keys(n) / 16 : BN / 16;
           for (int c = 0; c < CPT && ok; ++c, ++j) {
             const int slot = j % NS;
             if (!mbar_wait(FULL(slot), (j / NS) & 1, abort_flag, kWaitNs)) { ok = false; break; }
@@ -402,6 +410,7 @@ tv_attn_tc_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ 
             const uint32_t vaddr = ring_addr + slot * CHUNK_BYTES;
 #pragma unroll
             for (int kk = 0; kk < BN / 16; ++kk) {       // 16 keys per step
+              if (kk >= steps) break;
               const uint64_t bd = smem_desc(vaddr + kk * (16 * 128), BOX_BYTES, 1024, 2);
               mma_ts(tmem + 256 + c * CH, pbuf + kk * 8, bd, ID_PV, (u > 0 || kk > 0) ? 1u : 0u);
             }
@@ -447,16 +456,16 @@ tv_attn_tc_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ 
     // 47.3 us, a tree of 60 nodes over 4096 17.2 -> 16.4).
     uint32_t parity = 0;                          // one bit per slot
     bool ok = true;
-    for (int u = 0; u < npt && ok; ++u) {
-      int z0, z1, ze;
-      if (!zero_rows(u, &z0, &z1, &ze)) continue;
+    for (int u = 0; u < T && ok; ++u) {
+      int z0, z1, ze, zt;
+      if (!zero_rows(u, &z0, &z1, &ze, &zt)) continue;
       for (int c = 0; c < CPT && ok; ++c) {
         // the step of V(u) in the producer's order: K(0), K(1), V(0), K(2), ...
         const int slot = ((min(u + 2, T) + u) * CPT + c) % NS;
         ok = __all_sync(kAll, mbar_wait(TAIL(slot), (parity >> slot) & 1u, abort_flag, kWaitNs));
         if (!ok) break;
         parity ^= 1u << slot;
-        const int nu = z1 - z0, nz = nu + BN - ze;
+        const int nu = z1 - z0, nz = nu + zt - ze;
         for (int i = lane >> 3; i < nz; i += 4) {            // eight lanes a row, both boxes
           const int r = i < nu ? z0 + i : ze + i - nu;
           uint8_t* at = ring + slot * CHUNK_BYTES + r * 128 + (lane & 7) * 16;

@@ -311,7 +311,9 @@ tv_attn_tc2_kernel(const __grid_constant__ AttnParams p, const __grid_constant__
         if ((kind == 0 && t >= T) || (kind == 1 && t < 1)) { --j; continue; }
         if (spec_k && !junk0 && t == 0 && kind == 0) continue;   // K(0) is in slot 0 already
         const bool tree = (tile == npt);
-        const bool tail_fix = (kind == 1) && !tree && tile == npt - 1 && tail_valid < BN;
+        // V rows that have to be zeros: past the prefix end, or the tree's nodes
+        const int ze = tree ? n : (tile == npt - 1 ? tail_valid : BN), zt = tree ? tree_keys(n) : BN;
+        const bool tail_fix = kind == 1 && ze < zt;
         const int slot = j % NS, use = j / NS;
         if (use > 0 && !__all_sync(kAll, mbar_wait(EMPTY(slot), (use - 1) & 1, abort_flag, kWaitNs))) {
           ok = false;
@@ -363,15 +365,15 @@ tv_attn_tc2_kernel(const __grid_constant__ AttnParams p, const __grid_constant__
         }
         __syncwarp();
         if (tail_fix) {
-          // this CTA's rows past the prefix end become zeros before any MMA reads them
+          // this CTA's rows past the end become zeros before any MMA reads them
           if (!__all_sync(kAll, mbar_wait(TAIL, tail_uses & 1, abort_flag, kWaitNs))) {
             ok = false;
             break;
           }
           ++tail_uses;
-          const int nz = BN - tail_valid;
+          const int nz = zt - ze;
           for (int e = lane; e < (D / 128) * nz * 8; e += 32) {
-            const int bx = e / (nz * 8), r = tail_valid + (e / 8) % nz, q16 = e % 8;
+            const int bx = e / (nz * 8), r = ze + (e / 8) % nz, q16 = e % 8;
             *reinterpret_cast<uint4*>(dst + bx * (BN * 128) + r * 128 + q16 * 16) = make_uint4(0, 0, 0, 0);
           }
           fence_proxy_async_smem();
@@ -431,8 +433,10 @@ tv_attn_tc2_kernel(const __grid_constant__ AttnParams p, const __grid_constant__
           if (!mbar_wait(FULL(slot), (j / NS) & 1, abort_flag, kWaitNs)) { ok = false; break; }
           tc_fence_after();
           const uint32_t vaddr = ring_addr + slot * SLOT;
+          const int steps = u == npt ? tree_keys(n) / 16 : BN / 16;
 #pragma unroll
           for (int kk = 0; kk < BN / 16; ++kk) {     // 16 keys per step
+            if (kk >= steps) break;
             const uint64_t bd = smem_desc(vaddr + kk * (16 * 128), BN * 128, 1024, 2);
             mma_pair_ts(tmem + 256, pbuf + kk * 8, bd, ID_PV, (u > 0 || kk > 0) ? 1u : 0u);
           }

@@ -305,7 +305,8 @@ tv_attn_tcp_kernel(const __grid_constant__ AttnParams p, const __grid_constant__
       if (!__all_sync(kAll, mbar_wait(UFULL(k), (uq / kUnitSlots) & 1, abort_flag, kWaitNs))) break;
       const volatile UnitInfo* qe = reinterpret_cast<const volatile UnitInfo*>(uqueue + k);
       if (!qe->valid) break;                     // the last entry: nobody waits for its release
-      const int b = qe->b, g = qe->g, npt = qe->npt, T = qe->T, tail_valid = qe->tail_valid, o0 = qe->o0;
+      const int b = qe->b, g = qe->g, npt = qe->npt, T = qe->T, tail_valid = qe->tail_valid, o0 = qe->o0,
+                n = qe->n;
       const int q_node = o0 + qe->rt * p.rows_per_tile / G;   // the Q tile's first node
       const int64_t k_begin = qe->k_begin, k_end = qe->k_end;
       // The unit's Q tile replaces the previous unit's once that unit's QK
@@ -353,7 +354,9 @@ tv_attn_tcp_kernel(const __grid_constant__ AttnParams p, const __grid_constant__
             break;
           }
           const bool tree = (tile == npt);
-          const bool tail_fix = (kind == 1) && !tree && tile == npt - 1 && tail_valid < BN;
+          // V rows that have to be zeros: past the prefix end, or the tree's nodes
+          const int ze = tree ? n : (tile == npt - 1 ? tail_valid : BN), zt = tree ? tree_keys(n) : BN;
+          const bool tail_fix = kind == 1 && ze < zt;
           const int slot = j % NS, use = j / NS;
           if (use > 0 && !__all_sync(kAll, mbar_wait(EMPTY(slot), (use - 1) & 1, abort_flag, kWaitNs))) {
             ok = false;
@@ -381,15 +384,15 @@ tv_attn_tcp_kernel(const __grid_constant__ AttnParams p, const __grid_constant__
           }
           __syncwarp();
           if (tail_fix) {
-            // the chunk's rows past the prefix end become zeros before the MMA reads them
+            // the chunk's rows past the end become zeros before the MMA reads them
             if (!__all_sync(kAll, mbar_wait(TAIL, tail_uses & 1, abort_flag, kWaitNs))) {
               ok = false;
               break;
             }
             ++tail_uses;
-            const int nz = BN - tail_valid;
+            const int nz = zt - ze;
             for (int e = lane; e < 2 * nz * 8; e += 32) {
-              const int bx = e / (nz * 8), r = tail_valid + (e / 8) % nz, q16 = e % 8;
+              const int bx = e / (nz * 8), r = ze + (e / 8) % nz, q16 = e % 8;
               *reinterpret_cast<uint4*>(dst + bx * BOX_BYTES + r * 128 + q16 * 16) = make_uint4(0, 0, 0, 0);
             }
             fence_proxy_async_smem();
@@ -422,11 +425,10 @@ tv_attn_tcp_kernel(const __grid_constant__ AttnParams p, const __grid_constant__
       bool ok = true;
       while (ok) {
         if (!mbar_wait(UFULL(k), (uq / kUnitSlots) & 1, abort_flag, kWaitNs)) break;
-        const int T = reinterpret_cast<const volatile UnitInfo*>(uqueue + k)->valid
-                          ? reinterpret_cast<const volatile UnitInfo*>(uqueue + k)->T
-                          : 0;
-        if (T == 0) break;                          // the last entry: nobody waits for its release
-        mbar_arrive(UEMPTY(k));                     // only T is needed, and it is read
+        const volatile UnitInfo* qe = reinterpret_cast<const volatile UnitInfo*>(uqueue + k);
+        if (!qe->valid) break;                      // the last entry: nobody waits for its release
+        const int T = qe->T, npt = qe->npt, tree_steps = tree_keys(qe->n) / 16;
+        mbar_arrive(UEMPTY(k));                     // what is needed of the entry has been read
         k ^= 1;
         if (!mbar_wait(Q_FULL, uq & 1, abort_flag, kWaitNs)) break;
         tc_fence_after();
@@ -462,9 +464,15 @@ tv_attn_tcp_kernel(const __grid_constant__ AttnParams p, const __grid_constant__
             for (int h = 0; h < 2 && ok; ++h) {
               if (!mbar_wait(P_FULL(h, ug & 1), (ug >> 1) & 1, abort_flag, kWaitNs)) { ok = false; break; }
               tc_fence_after();
+              // the tree's nodes are all in half 0; half 1's weights are zeros
+              // there, and only start its accumulator, with V rows of half 0,
+              // where the tree is the unit's first tile
+              const int steps = u < npt ? BN / 32 : (h == 0 ? tree_steps : (u == 0 ? 1 : 0));
+              const int k0 = u < npt ? h * (BN / 32) : 0;
 #pragma unroll
               for (int kq = 0; kq < BN / 32; ++kq) {  // 16 keys per step, 4 steps per half
-                const int kk = h * (BN / 32) + kq;
+                if (kq >= steps) break;
+                const int kk = k0 + kq;
                 const uint64_t bd = smem_desc(vaddr + kk * (16 * 128), BOX_BYTES, 1024, 2);
                 mma_ts(tmem + 256 + (uint32_t)(h * D), pbuf + h * (BN / 2) + kq * 8, bd, ID_PV,
                        (u > 0 || kq > 0) ? 1u : 0u);

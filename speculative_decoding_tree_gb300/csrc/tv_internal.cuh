@@ -140,6 +140,13 @@ __host__ __device__ inline int num_chunks(int64_t P, int chunk, int tree_tile) {
   return (int)n;
 }
 
+// Keys of the tree tile that the tensor-core kernels multiply with V: the
+// sequence's n nodes in whole MMA steps of 16.  The V rows from n up to there,
+// and all behind, belong to other sequences or KV heads: the former are made
+// zeros, the latter take no part, so that a neighbour's NaN or infinity meets
+// no weight of 0.
+__host__ __device__ constexpr int tree_keys(int n) { return (n + 15) / 16 * 16; }
+
 __host__ __device__ inline int64_t clamp_prefix(int64_t P, int64_t max_prefix, int64_t capacity) {
   int64_t hi = max_prefix < capacity ? max_prefix : capacity;
   return P < 0 ? 0 : (P > hi ? hi : P);
