@@ -26,6 +26,12 @@
  * so a K value takes 4.25 bits and a V value 4 + 8 / d.
  * The capacity is a multiple of 16 in both cases.
  *
+ * Rounding.  Cached values are exact in both types.  fp32 calls are computed in
+ * fp32.  bf16 calls accumulate, and take the softmax and the partial results,
+ * in fp32; each softmax weight, times its position's V scale, is rounded to
+ * bf16 (2^-8 of it at most) before it multiplies the steps u - 8 of V,
+ * while the sum that divides keeps the unrounded weights.
+ *
  * desc->dtype is the type of queries, of the tree's K/V and of the rows
  * written and read.  The calls on the cache alone (tv_kv4_cache_bytes,
  * tv_kv4_append, tv_kv4_read) have no tree: the descriptor's max_nodes and

@@ -17,7 +17,13 @@
  * a key that left the window keeps its place and is not read again unless it
  * is a sink, so a paged cache may free its page.  The page table's entries of
  * 16-position pages that no row sees (wholly in [sinks, prefix_len - window
- * + 1)) are not read and may hold anything.
+ * + 1)) are not read and may hold anything, and so may every cache row that no
+ * row sees.  V that some rows of a sequence see must be finite for the others.
+ *
+ * Rounding.  fp32 calls are computed in fp32.  bf16 calls accumulate, and take
+ * the softmax and the partial results, in fp32; each softmax weight is rounded
+ * to bf16 (2^-8 of it at most) before it multiplies V, while the sum
+ * that divides keeps the unrounded ones.
  */
 #ifndef TREE_WINDOW_H
 #define TREE_WINDOW_H
