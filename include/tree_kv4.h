@@ -30,7 +30,9 @@
  * fp32.  bf16 calls accumulate, and take the softmax and the partial results,
  * in fp32; each softmax weight, times its position's V scale, is rounded to
  * bf16 (2^-8 of it at most) before it multiplies the steps u - 8 of V,
- * while the sum that divides keeps the unrounded weights.
+ * while the sum that divides keeps the unrounded weights.  These weights are
+ * relative to one of the row's scores, not always its largest, and reach 2^60:
+ * V of the tree should stay below 2^60 in magnitude there.
  *
  * desc->dtype is the type of queries, of the tree's K/V and of the rows
  * written and read.  The calls on the cache alone (tv_kv4_cache_bytes,
