@@ -401,16 +401,18 @@ tv_attn_kv4_kernel(const __grid_constant__ AttnParams p, const __grid_constant__
     // constant offsets: a bulk copy per block cost more instructions (one
     // lane's operands at a time) than the copies of all lanes together.
     const int blk_of_lane = lane >> 2;
-    // ids(t): page id of the lane's block of tile t (or, contiguous, the block
-    // number), kNoPage where nothing is loaded (past the end, or seen by no
-    // row), read two tiles before its use
-    auto ids = [&](int t) -> int {
+    // at(t): number of the lane's block of tile t in its sequence, -1 where
+    // nothing is loaded (past the end, or seen by no row); ids(t): what the page
+    // table holds for it (any number), read two tiles before its use
+    auto at = [&](int t) -> int64_t {
       const int off = blk_of_lane * kPageSize;
-      if (t >= npt || (t == npt - 1 && off >= tail)) return kNoPage;
+      if (t >= npt || (t == npt - 1 && off >= tail)) return -1;
       const int64_t pos = tile_pos(t) + off;
-      if (WIN && pos >= p.sinks && pos + kPageSize <= first_pos) return kNoPage;
-      const int64_t blk = pos / kPageSize;
-      return p.paged ? listed_page(p.page_table[(int64_t)b * p.max_pages + blk]) : (int)blk;
+      return WIN && pos >= p.sinks && pos + kPageSize <= first_pos ? -1 : pos / kPageSize;
+    };
+    auto ids = [&](int t) -> int {
+      const int64_t i = p.paged ? at(t) : -1;
+      return i < 0 ? 0 : p.page_table[(int64_t)b * p.max_pages + i];
     };
     const uint32_t k_dst = smem_u32(sK) + blk_of_lane * C::KB + (lane & 3) * 16;
     const uint32_t v_dst = smem_u32(sV) + blk_of_lane * C::VB + (lane & 3) * 16;
@@ -427,10 +429,10 @@ tv_attn_kv4_kernel(const __grid_constant__ AttnParams p, const __grid_constant__
       const int raw = id0;
       id0 = id1;
       id1 = ids(t + 2);
-      int64_t blk = -1;
-      if (raw != kNoPage) {
+      int64_t blk = at(t);
+      if (blk >= 0) {
         if (!p.paged)
-          blk = ((int64_t)b * p.Hkv + g) * p.max_pages + raw;
+          blk += ((int64_t)b * p.Hkv + g) * p.max_pages;
         else
           blk = raw >= 0 && raw < p.num_pages ? (int64_t)raw * p.Hkv + g : -2;
       }

@@ -35,6 +35,8 @@
 // score further above moves it.  A warp keeps its own references, sums and O;
 // its CTA's four warps take alternate spans and join at the end.  Each load
 // buffer is refilled as soon as it has been multiplied, a span ahead.
+#include <climits>
+
 #include "tv_kv4.cuh"
 
 namespace tv {
@@ -44,6 +46,7 @@ constexpr int kSpan = 64;                        // keys per span
 constexpr int kRows = 8;                         // query rows of a KV head: an mma.sync column each
 constexpr int kWarps = 4;
 constexpr float kHeadroom = 60.0f;               // log2: a weight above 2^60 moves the reference
+constexpr int kNoPage = INT_MIN;                 // nothing to load (past the end, or seen by no row): not a page id
 
 __device__ __forceinline__ float ex2(float x) {
   float y;
@@ -175,7 +178,8 @@ __global__ void __launch_bounds__(32 * kWarps, Cfg<D>::CTAS) tv_attn_kv4_rows_ke
     if (sp >= nsp || v >= k_end) return kNoPage;
     const int64_t pos = WIN ? km.pos(v) : v;
     if (WIN && pos >= p.sinks && pos + kPageSize <= first_pos) return kNoPage;
-    return p.paged ? listed_page(p.page_table[(int64_t)b * p.max_pages + pos / kPageSize]) : (int)(pos / kPageSize);
+    // (the table may hold any number: every negative one is out of range, and -1 stands for them all)
+    return p.paged ? max(p.page_table[(int64_t)b * p.max_pages + pos / kPageSize], -1) : (int)(pos / kPageSize);
   };
   auto block_of = [&](int id, bool* bad) -> int64_t {
     *bad = false;

@@ -297,15 +297,18 @@ tv_attn_tc_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ 
     // paged cache: lane i < 8 owns page i of a key tile; page ids are read
     // well ahead of the copies that use them
     const int oob_row = p.paged ? (int)(p.num_pages * p.Hkv * kPageSize) : 0;
-    auto page_id = [&](int tile) -> int {           // raw page id of this lane's page, or kNoPage (none)
-      if (!p.paged || tile >= npt || lane >= BN / kPageSize) return kNoPage;
-      if (k_begin + (int64_t)tile * BN + lane * kPageSize >= k_end) return kNoPage;
+    auto page_pos = [&](int tile) -> int64_t {      // first position of this lane's page, or -1 (nothing to load)
+      if (!p.paged || tile >= npt || lane >= BN / kPageSize) return -1;
+      if (k_begin + (int64_t)tile * BN + lane * kPageSize >= k_end) return -1;
       const int64_t pos = tile_pos(tile) + lane * kPageSize;
-      if (WIN && pos >= p.sinks && pos + kPageSize <= first_pos) return kNoPage;   // no row sees the page
-      return listed_page(p.page_table[(int64_t)b * p.max_pages + pos / kPageSize]);
+      return WIN && pos >= p.sinks && pos + kPageSize <= first_pos ? -1 : pos;   // (no row sees the page)
     };
-    auto page_row = [&](int pid) -> int {           // TMA row of a page id, checked where it is used
-      if (pid == kNoPage) return -1;
+    auto page_id = [&](int tile) -> int {           // what the table holds (any number)
+      const int64_t pos = page_pos(tile);
+      return pos < 0 ? 0 : p.page_table[(int64_t)b * p.max_pages + pos / kPageSize];
+    };
+    auto page_row = [&](int tile, int pid) -> int { // TMA row of a page id, checked where it is used
+      if (page_pos(tile) < 0) return -1;
       if (pid >= 0 && pid < p.num_pages) return (int)(((int64_t)pid * p.Hkv + g) * kPageSize);
       set_status(p.status, TV_DEV_BAD_PAGE);
       return oob_row;                               // out of range: the copy reads zeros
@@ -316,7 +319,7 @@ tv_attn_tc_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ 
     int row_k = -1, row_v = -1;
     for (int t = 0; t <= T && ok; ++t) {
       row_v = row_k;                                // tile t-1 (for V)
-      row_k = page_row(pid_a);                      // tile t   (for K)
+      row_k = page_row(t, pid_a);                   // tile t   (for K)
       pid_a = pid_b;
       pid_b = pid_c;
       pid_c = pid_d;
@@ -402,17 +405,21 @@ tv_attn_tc_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ 
           const uint32_t pbuf = tmem + (uint32_t)((u & 1) * 128);
           if (!mbar_wait(P_FULL(u & 1), (u >> 1) & 1, abort_flag, kWaitNs)) { ok = false; break; }
           tc_fence_after();
-          const int steps = u == npt ? tree_keys(n) / 16 : BN / 16;
           for (int c = 0; c < CPT && ok; ++c, ++j) {
             const int slot = j % NS;
             if (!mbar_wait(FULL(slot), (j / NS) & 1, abort_flag, kWaitNs)) { ok = false; break; }
             tc_fence_after();
             const uint32_t vaddr = ring_addr + slot * CHUNK_BYTES;
-#pragma unroll
-            for (int kk = 0; kk < BN / 16; ++kk) {       // 16 keys per step
-              if (kk >= steps) break;
+            auto step = [&](int kk) {                    // 16 keys
               const uint64_t bd = smem_desc(vaddr + kk * (16 * 128), BOX_BYTES, 1024, 2);
               mma_ts(tmem + 256 + c * CH, pbuf + kk * 8, bd, ID_PV, (u > 0 || kk > 0) ? 1u : 0u);
+            };
+            if (u < npt) {
+#pragma unroll
+              for (int kk = 0; kk < BN / 16; ++kk) step(kk);
+            } else {
+#pragma unroll 1
+              for (int kk = 0; kk < tree_keys(n) / 16; ++kk) step(kk);
             }
             mma_commit(EMPTY(slot));
           }

@@ -280,14 +280,17 @@ tv_attn_tc2_kernel(const __grid_constant__ AttnParams p, const __grid_constant__
     int j = junk0 ? 1 : 0, tail_uses = 0;
     bool ok = true;
     const int oob_row = p.paged ? (int)(p.num_pages * p.Hkv * kPageSize) : 0;
-    auto page_id = [&](int tile) -> int {           // raw page id of this lane's page (lanes 0-7), or kNoPage
-      if (!p.paged || tile >= npt || lane >= BN / kPageSize) return kNoPage;
+    auto page_pos = [&](int tile) -> int64_t {      // first position of this lane's page (lanes 0-7), or -1 (none)
+      if (!p.paged || tile >= npt || lane >= BN / kPageSize) return -1;
       const int64_t pos = k_begin + (int64_t)tile * BN + lane * kPageSize;
-      if (pos >= k_end) return kNoPage;
-      return listed_page(p.page_table[(int64_t)b * p.max_pages + pos / kPageSize]);
+      return pos < k_end ? pos : -1;
     };
-    auto page_row = [&](int pid) -> int {
-      if (pid == kNoPage) return -1;
+    auto page_id = [&](int tile) -> int {           // what the table holds (any number)
+      const int64_t pos = page_pos(tile);
+      return pos < 0 ? 0 : p.page_table[(int64_t)b * p.max_pages + pos / kPageSize];
+    };
+    auto page_row = [&](int tile, int pid) -> int { // TMA row of a page id, checked where it is used
+      if (page_pos(tile) < 0) return -1;
       if (pid >= 0 && pid < p.num_pages) return (int)(((int64_t)pid * p.Hkv + g) * kPageSize);
       set_status(p.status, TV_DEV_BAD_PAGE);
       return oob_row;
@@ -301,7 +304,7 @@ tv_attn_tc2_kernel(const __grid_constant__ AttnParams p, const __grid_constant__
     int row_k = -1, row_v = -1;
     for (int t = 0; t <= T && ok; ++t) {
       row_v = row_k;
-      row_k = page_row(pid_a);
+      row_k = page_row(t, pid_a);
       pid_a = pid_b;
       pid_b = pid_c;
       pid_c = pid_d;
@@ -433,12 +436,16 @@ tv_attn_tc2_kernel(const __grid_constant__ AttnParams p, const __grid_constant__
           if (!mbar_wait(FULL(slot), (j / NS) & 1, abort_flag, kWaitNs)) { ok = false; break; }
           tc_fence_after();
           const uint32_t vaddr = ring_addr + slot * SLOT;
-          const int steps = u == npt ? tree_keys(n) / 16 : BN / 16;
-#pragma unroll
-          for (int kk = 0; kk < BN / 16; ++kk) {     // 16 keys per step
-            if (kk >= steps) break;
+          auto step = [&](int kk) {                  // 16 keys
             const uint64_t bd = smem_desc(vaddr + kk * (16 * 128), BN * 128, 1024, 2);
             mma_pair_ts(tmem + 256, pbuf + kk * 8, bd, ID_PV, (u > 0 || kk > 0) ? 1u : 0u);
+          };
+          if (u < npt) {
+#pragma unroll
+            for (int kk = 0; kk < BN / 16; ++kk) step(kk);
+          } else {
+#pragma unroll 1
+            for (int kk = 0; kk < tree_keys(n) / 16; ++kk) step(kk);
           }
           mma_commit_pair(EMPTY(slot));
           mma_commit_pair(O_DONE(u & 1));

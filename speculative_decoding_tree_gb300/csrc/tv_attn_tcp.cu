@@ -325,14 +325,17 @@ tv_attn_tcp_kernel(const __grid_constant__ AttnParams p, const __grid_constant__
         ++q_loads;
         return true;
       };
-      auto page_id = [&](int tile) -> int {         // raw page id of this lane's page, or kNoPage (none)
-        if (!p.paged || tile >= npt || lane >= BN / kPageSize) return kNoPage;
+      auto page_pos = [&](int tile) -> int64_t {    // first position of this lane's page, or -1 (none)
+        if (!p.paged || tile >= npt || lane >= BN / kPageSize) return -1;
         const int64_t pos = k_begin + (int64_t)tile * BN + lane * kPageSize;
-        if (pos >= k_end) return kNoPage;
-        return listed_page(p.page_table[(int64_t)b * p.max_pages + pos / kPageSize]);
+        return pos < k_end ? pos : -1;
       };
-      auto page_row = [&](int pid) -> int {         // TMA row of a page id, checked where it is used
-        if (pid == kNoPage) return -1;
+      auto page_id = [&](int tile) -> int {         // what the table holds (any number)
+        const int64_t pos = page_pos(tile);
+        return pos < 0 ? 0 : p.page_table[(int64_t)b * p.max_pages + pos / kPageSize];
+      };
+      auto page_row = [&](int tile, int pid) -> int {   // TMA row of a page id, checked where it is used
+        if (page_pos(tile) < 0) return -1;
         if (pid >= 0 && pid < p.num_pages) return (int)(((int64_t)pid * p.Hkv + g) * kPageSize);
         set_status(p.status, TV_DEV_BAD_PAGE);
         return oob_row;                             // out of range: the copy reads zeros
@@ -341,7 +344,7 @@ tv_attn_tcp_kernel(const __grid_constant__ AttnParams p, const __grid_constant__
       int row_k = -1, row_v = -1;
       for (int t = 0; t <= T && ok; ++t) {
         row_v = row_k;                              // tile t - 1
-        row_k = page_row(pid_a);
+        row_k = page_row(t, pid_a);
         pid_a = pid_b;
         pid_b = pid_c;
         pid_c = pid_d;

@@ -4,7 +4,6 @@
 
 #include <cuda_runtime.h>
 #include <cuda_bf16.h>
-#include <limits.h>
 #include <stdint.h>
 
 #include <atomic>
@@ -171,13 +170,6 @@ __device__ inline bool seq_rows(const int32_t* offs, int b, int R, int max_nodes
   *n = cnt;
   return true;
 }
-
-// Kernels that read page ids ahead keep kNoPage where nothing is loaded (past
-// the end, or seen by no row).  The table may hold any number: listed_page
-// gives what it holds, every negative id as -1 (out of range too), never
-// kNoPage.
-constexpr int kNoPage = INT_MIN;
-__device__ __forceinline__ int listed_page(int id) { return id < 0 ? -1 : id; }
 
 // Programmatic dependent launch.  Every kernel of the library is launched
 // with programmatic stream serialization, so its CTAs may start while the
