@@ -53,16 +53,21 @@
 #include <cuda.h>
 
 #include <climits>
-#include <mutex>
 #include <type_traits>
 
 #include "tc_ptx.cuh"
 #include "tv_kv4.cuh"
+#include "tv_tensormap.cuh"
 
 namespace tv {
 namespace {
 
 using namespace tc;
+using kv4::fma_bf16x2;
+using kv4::kMinus136;
+using kv4::kMinusZero;
+using kv4::kOne;
+using kv4::PairBits;
 
 constexpr int BK = 128;                          // keys per tile
 constexpr int kBlocks = BK / kPageSize;          // cache blocks per tile
@@ -105,41 +110,6 @@ struct Cfg {
                        kADone = kAFull + NS, kS = kADone + NS, kPV = kS + 2, kQ = kPV + 1, kFin = kQ + 1, kBars = kFin + 1;
   static_assert(kBars * 8 <= 512, "barriers overflow their area");
 };
-
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
-__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
-  __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
-  return *reinterpret_cast<uint32_t*>(&h);
-}
-
-__device__ __forceinline__ uint32_t fma_bf16x2(uint32_t a, uint32_t b, uint32_t c) {
-  uint32_t r;
-  asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(c));
-  return r;
-}
-
-// Pair j of a word as two bf16 numbers 128 + u: (w >> 4 j) & mask | base, one
-// three-input operation with the two constants in registers (as immediates
-// they would take two).
-struct PairBits {
-  uint32_t mask, base;
-  __device__ __forceinline__ PairBits() {
-    asm volatile("mov.b32 %0, 0x000F000F;" : "=r"(mask));
-    asm volatile("mov.b32 %0, 0x43004300;" : "=r"(base));
-  }
-  __device__ __forceinline__ uint32_t operator()(uint32_t w, int j) const {
-    uint32_t r;
-    asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(r) : "r"(w >> (4 * j)), "r"(mask), "r"(base));
-    return r;
-  }
-};
-
-constexpr uint32_t kMinus136 = 0xC308C308u, kOne = 0x3F803F80u, kZero = 0x80008000u;   // bf16 pairs (kZero: -0)
 
 __device__ __forceinline__ void tmem_st16(uint32_t a, const uint32_t (&r)[16]) {
   asm volatile(
@@ -609,7 +579,7 @@ tv_attn_kv4_kernel(const __grid_constant__ AttnParams p, const __grid_constant__
           for (int h = 0; h < H; ++h) {
             const uint4 w4 = *reinterpret_cast<const uint4*>(code + h * 256);
             const uint32_t s2 = (((uint32_t)scale[h * 16] << 4) + 0x3800u) * 0x00010001u;   // the scale as a bf16 pair
-            const uint32_t o2 = fma_bf16x2(s2, kMinus136, kZero);
+            const uint32_t o2 = fma_bf16x2(s2, kMinus136, kMinusZero);
             const uint32_t w[4] = {w4.x, w4.y, w4.z, w4.w};
             uint32_t r[16];
 #pragma unroll
@@ -930,29 +900,10 @@ tv_attn_kv4_kernel(const __grid_constant__ AttnParams p, const __grid_constant__
 
 // ---------------------------------------------------------------- host
 
-typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
-                                  const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
-                                  CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-EncodeTiledFn encode_fn() {
-  static EncodeTiledFn fn = nullptr;
-  static std::once_flag once;
-  std::call_once(once, [] {
-    void* f = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) == cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-      fn = reinterpret_cast<EncodeTiledFn>(f);
-    else
-      cudaGetLastError();
-  });
-  return fn;
-}
-
 template <int D, int N, bool WIN>
 cudaError_t launch_t(const AttnParams& p, cudaStream_t st) {
   using C = Cfg<D, N>;
-  EncodeTiledFn fn = encode_fn();
+  EncodeTiledFn fn = encode_tiled_fn();
   if (!fn) return cudaErrorInvalidValue;
   CUtensorMap mq;
   const cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)p.Hq, (cuuint64_t)p.R};

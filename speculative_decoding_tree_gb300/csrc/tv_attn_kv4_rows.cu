@@ -42,40 +42,17 @@
 namespace tv {
 namespace {
 
+using kv4::fma_bf16x2;
+using kv4::kMinus136;
+using kv4::kMinusZero;
+using kv4::kOne;
+using kv4::PairBits;
+
 constexpr int kSpan = 64;                        // keys per span
 constexpr int kRows = 8;                         // query rows of a KV head: an mma.sync column each
 constexpr int kWarps = 4;
 constexpr float kHeadroom = 60.0f;               // log2: a weight above 2^60 moves the reference
 constexpr int kNoPage = INT_MIN;                 // nothing to load (past the end, or seen by no row): not a page id
-
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
-  __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
-  return *reinterpret_cast<uint32_t*>(&h);
-}
-__device__ __forceinline__ uint32_t fma_bf16x2(uint32_t a, uint32_t b, uint32_t c) {
-  uint32_t r;
-  asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(c));
-  return r;
-}
-// pair j of a word as bf16 numbers 128 + u (the constants in registers)
-struct PairBits {
-  uint32_t mask, base;
-  __device__ __forceinline__ PairBits() {
-    asm volatile("mov.b32 %0, 0x000F000F;" : "=r"(mask));
-    asm volatile("mov.b32 %0, 0x43004300;" : "=r"(base));
-  }
-  __device__ __forceinline__ uint32_t operator()(uint32_t w, int j) const {
-    uint32_t r;
-    asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(r) : "r"(w >> (4 * j)), "r"(mask), "r"(base));
-    return r;
-  }
-};
-constexpr uint32_t kMinus136 = 0xC308C308u, kOne = 0x3F803F80u, kMinusZero = 0x80008000u;   // bf16 pairs
 
 __device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                     uint32_t b1) {
@@ -98,7 +75,6 @@ __device__ __forceinline__ uint4 ldg16(const uint8_t* p) {
                : "l"(p));
   return v;
 }
-__device__ __forceinline__ void prefetch_l2(const uint8_t* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
 __device__ __forceinline__ uint32_t word(const uint4& v, int i) { return i == 0 ? v.x : (i == 1 ? v.y : (i == 2 ? v.z : v.w)); }
 
 template <int D>

@@ -51,10 +51,10 @@
 // numbers with atomic adds.
 #include <cuda.h>
 
-#include <mutex>
 
 #include "tc_ptx.cuh"
 #include "tv_internal.cuh"
+#include "tv_tensormap.cuh"
 
 namespace tv {
 namespace {
@@ -97,17 +97,6 @@ static_assert(sizeof(UnitInfo) == 64, "unit queue entry");
 constexpr uint32_t kXchOfs = 384;               // [2 parity][2 half][128 rows] floats
 constexpr uint32_t kQueueOfs = kXchOfs + 2048;
 static_assert(kQueueOfs + kUnitSlots * sizeof(UnitInfo) <= kHeader, "unit queue overflows the header");
-
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
-__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
-  __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
-  return *reinterpret_cast<uint32_t*>(&h);
-}
 
 // Packed fp32 pairs (f32x2 arithmetic: one instruction for two lanes of
 // work on the FMA pipes).
@@ -706,29 +695,9 @@ tv_attn_tcp_kernel(const __grid_constant__ AttnParams p, const __grid_constant__
 
 // ---------------------------------------------------------------- host
 
-typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
-                                  const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
-                                  CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-EncodeTiledFn encode_fn_p() {
-  static EncodeTiledFn fn = nullptr;
-  static std::once_flag once;
-  std::call_once(once, [] {
-    void* f = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) ==
-            cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-      fn = reinterpret_cast<EncodeTiledFn>(f);
-    else
-      cudaGetLastError();
-  });
-  return fn;
-}
-
 bool encode_p(CUtensorMap* m, const void* ptr, int rank, const cuuint64_t* dims, const cuuint64_t* strides,
               const cuuint32_t* box) {
-  EncodeTiledFn fn = encode_fn_p();
+  EncodeTiledFn fn = encode_tiled_fn();
   if (!fn) return false;
   cuuint32_t es[3] = {1, 1, 1};
   return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank, const_cast<void*>(ptr), dims, strides, box, es,

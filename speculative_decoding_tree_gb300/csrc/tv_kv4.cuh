@@ -33,6 +33,34 @@ __device__ __forceinline__ void expand8(uint32_t w, float (&x)[8]) {
   }
 }
 
+// Expansion in bf16 pairs: a masked pair is 128 + u, and
+// (128 + u) s - 136 s = (u - 8) s is one fused multiply-add, exact because s has
+// 4 significant bits.  (That a 4-bit code under the exponent of 128 is a number
+// is the known way to widen 4-bit weights without a conversion.)
+constexpr uint32_t kMinus136 = 0xC308C308u, kOne = 0x3F803F80u, kMinusZero = 0x80008000u;   // bf16 pairs
+
+__device__ __forceinline__ uint32_t fma_bf16x2(uint32_t a, uint32_t b, uint32_t c) {
+  uint32_t r;
+  asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(c));
+  return r;
+}
+
+// Pair j of a word as two bf16 numbers 128 + u: (w >> 4 j) & mask | base, one
+// three-input operation with the two constants in registers (as immediates
+// they would take two).
+struct PairBits {
+  uint32_t mask, base;
+  __device__ __forceinline__ PairBits() {
+    asm volatile("mov.b32 %0, 0x000F000F;" : "=r"(mask));
+    asm volatile("mov.b32 %0, 0x43004300;" : "=r"(base));
+  }
+  __device__ __forceinline__ uint32_t operator()(uint32_t w, int j) const {
+    uint32_t r;
+    asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(r) : "r"(w >> (4 * j)), "r"(mask), "r"(base));
+    return r;
+  }
+};
+
 // block `blk` of sequence b and KV head g (paged: through the page table;
 // nullptr for a page id out of range)
 __device__ __forceinline__ const uint8_t* block_at(const uint8_t* base, int bytes, int b, int g, int64_t blk, int Hkv,

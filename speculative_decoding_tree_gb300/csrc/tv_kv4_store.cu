@@ -325,15 +325,9 @@ __global__ __launch_bounds__(kThreads) void kv4_append_kernel(const Kv4RowsParam
   store_block<T, D>(k, v, kb, vb, s_row, xs, s_step);
 }
 
-__device__ __forceinline__ uint32_t fma_bf16x2(uint32_t a, uint32_t b, uint32_t c) {
-  uint32_t r;
-  asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(c));
-  return r;
-}
-
 // pair j of a word times the bf16 pair of scales s2, exact
 __device__ __forceinline__ uint32_t pair_value(uint32_t w, int j, uint32_t s2) {
-  return fma_bf16x2(((w >> (4 * j)) & 0x000F000Fu) | 0x43004300u, s2, fma_bf16x2(s2, 0xC308C308u, 0x80008000u));
+  return fma_bf16x2(((w >> (4 * j)) & 0x000F000Fu) | 0x43004300u, s2, fma_bf16x2(s2, kMinus136, kMinusZero));
 }
 __device__ __forceinline__ uint32_t scale_bits(uint32_t code) { return (code << 4) + 0x3800u; }   // as bf16
 

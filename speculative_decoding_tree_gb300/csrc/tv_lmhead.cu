@@ -24,12 +24,12 @@
 
 #include <cmath>
 #include <cstdint>
-#include <mutex>
 
 #include "tc_ptx.cuh"
 #include "tree_lm_head.h"
 #include "tv_internal.cuh"
 #include "tv_select.cuh"
+#include "tv_tensormap.cuh"
 
 namespace tv {
 namespace {
@@ -252,30 +252,10 @@ __global__ void __launch_bounds__(256) lmhead_finish_kernel(const float* __restr
 
 // ---------------------------------------------------------------- host
 
-typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
-                                  const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
-                                  CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-EncodeTiledFn encode_fn_lm() {
-  static EncodeTiledFn fn = nullptr;
-  static std::once_flag once;
-  std::call_once(once, [] {
-    void* f = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) ==
-            cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-      fn = reinterpret_cast<EncodeTiledFn>(f);
-    else
-      cudaGetLastError();
-  });
-  return fn;
-}
-
 // 2D bf16 map over [rows, cols] row-major, box [box_rows, 64], 128-byte
 // swizzle; reads past the last row fill zeros
 bool encode_rows(CUtensorMap* m, const void* ptr, int64_t rows, int64_t cols, uint32_t box_rows) {
-  EncodeTiledFn fn = encode_fn_lm();
+  EncodeTiledFn fn = encode_tiled_fn();
   if (!fn) return false;
   cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
   cuuint64_t strides[1] = {(cuuint64_t)cols * 2};
