@@ -101,13 +101,13 @@ int make_plan(const tv_desc* d, Plan* p) {
     while (c <= tiles && num_chunks(L, (int)(c * key_tile), tree_tile) > want) ++c;
     chunk = c * key_tile;
   } else {
-    // ragged batch: fixed 1920-key chunks (15 key tiles of 128), so that the
-    // units balance sequences of different lengths.  On the batched
-    // workload's persistent kernel, summed over three seeds of its prefixes
-    // and trees, the call took 348.8 / 343.1 / 341.0 / 345.0 us with 1664 /
-    // 1792 / 1920 / 2048-key chunks; on one seed 1024 and 4096 keys gave
-    // 128.9 and 132.2 us against 120.3 at 2048)
-    chunk = align_up(1920, key_tile);
+    // ragged batch: fixed chunks, so that the units balance sequences of
+    // different lengths: 1792 keys on the persistent kernel, 1920 elsewhere.
+    // Persistent, the call summed over three seeds of the batched workload's
+    // prefixes and trees: 384.6 / 387.9 / 399.4 / 410.3 us with 1664 / 1792 /
+    // 1920 / 2048 keys, 398.6 and 404.3 with 1152 and 1024; 4 such sequences
+    // 43.0 / 39.3 / 40.7 / 42.1, 48 of them 341 / 336 / 334 / 339.
+    chunk = align_up(persist ? 1792 : 1920, key_tile);
   }
   if (chunk > (int64_t)1 << 30) return TV_ERR_OVERFLOW;
   int splits = num_chunks(L, (int)chunk, tree_tile);
