@@ -38,11 +38,11 @@
 // and by instruction fetch over five kinds of loops (64 sequences x 1 row over
 // up to 16384 keys: 422 us against 264 us).
 //
-// Measured: a tree of 60 nodes x 4 heads over 32768 keys (head_dim 256) 50 us,
-// 640 TFLOP/s; 16 ragged trees over up to 8192 keys (128, paged) 164 us, 310
+// Measured: a tree of 60 nodes x 4 heads over 32768 keys (head_dim 256) 51 us,
+// 630 TFLOP/s; 16 ragged trees over up to 8192 keys (128, paged) 164 us, 310
 // TFLOP/s.  What bounds it is the compute warps' work and the chain of its
 // steps: expansion (2.75 instructions a pair of values, for each tile of query
-// rows again), exponents, two barriers a tile; 46% of the issue slots at one
+// rows again), exponents, two barriers a tile; 47% of the issue slots at one
 // CTA of 128 columns an SM.  Narrower tiles expand more often: 64 columns took
 // 78 and 229 us where 128 took 56 and 190 (the same two calls, an earlier
 // build).

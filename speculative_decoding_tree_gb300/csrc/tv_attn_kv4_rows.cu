@@ -10,7 +10,7 @@
 // multiply-add: see tv_attn_kv4.cu) and multiplies with mma.sync.m16n8k16,
 // whose row granularity (8 query rows) fits where a tcgen05 operand would have
 // to go through tensor memory.  64 sequences x 4 rows over up to 16384 keys:
-// 156 us (the floor of its bytes is 90), 209 with tcgen05's 16-column tile.  From
+// 152 us (the floor of its bytes is 90), 209 with tcgen05's 16-column tile.  From
 // 9 rows on that tile is the faster one: 64 x 16 rows 214 us, 242 with two
 // mma.sync columns here.
 //
