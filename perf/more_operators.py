@@ -310,7 +310,8 @@ def _plan(st):
     c = st["case"]
     if c["op"] == "steer":
         st["desc"] = tv.make_logits_desc(batch=c["batch"], vocab=c["vocab"], max_nodes=st["mn"], total_rows=st["R"],
-                                         logits_dtype=tv.BF16 if c["dtype"] == "bf16" else tv.F32)
+                                         logits_dtype=tv.BF16 if c["dtype"] == "bf16" else tv.F32,
+                                         biases=c["batch"] * c["bias"])
     else:
         st["desc"] = tv.make_desc(
             batch=c["batch"], num_q_heads=c["hq"], num_kv_heads=c["hkv"], head_dim=c["d"],
