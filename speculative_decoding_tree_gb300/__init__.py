@@ -4,8 +4,10 @@ A thin ctypes binding over libtreeverify.so, whose C ABI is declared in
 include/tree_verify.h (the verify step), include/tree_expand.h (dynamic
 draft-tree expansion), include/tree_lm_head.h (fused lm_head + argmax),
 include/tree_rope.h (tree-position RoPE and the K/V scatter),
-include/tree_window.h (attention over a sliding window with sinks) and
-include/tree_kv4.h (a KV cache held in 4 bits).  Every function here only marshals arguments (torch
+include/tree_window.h (attention over a sliding window with sinks),
+include/tree_kv4.h (a KV cache held in 4 bits), include/tree_prompt.h (prompts:
+RoPE, the cache's writes and causal attention) and include/tree_logits.h
+(penalties, biases and grammar masks on tree logits).  Every function here only marshals arguments (torch
 tensors or raw device addresses, a stream) and raises on a non-zero status;
 all work happens in the library's CUDA kernels.  There is no CPU fallback:
 calling into a library that was not built raises ``LibraryNotBuilt``.
@@ -25,11 +27,13 @@ __all__ = [
     "TvWindow", "make_window", "tv_window_workspace_size", "tv_window_attn_plan", "tree_verify_attn_window",
     "tv_kv4_cache_bytes", "tv_kv4_append", "tv_kv4_read", "tree_accept_commit_argmax_kv4", "tv_kv4_workspace_size",
     "tv_kv4_attn_plan", "tree_verify_attn_kv4",
+    "tv_prompt_rope_store", "tv_prompt_workspace_size", "tv_prompt_attn_plan", "tv_prompt_attn",
+    "TvLogitsDesc", "make_logits_desc", "tv_token_counts_add", "tv_tree_logits_process",
 ]
 
 F32, BF16 = 0, 1
 DEV_BITS = {1: "BAD_TREE", 2: "BAD_OFFSETS", 4: "BAD_PREFIX", 8: "BAD_PAGE", 16: "CAPACITY", 32: "TIMEOUT",
-            64: "BAD_LOGITS", 128: "BAD_STEP"}
+            64: "BAD_LOGITS", 128: "BAD_STEP", 256: "BAD_TOKEN"}
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libtreeverify.so")
 
 
@@ -65,6 +69,11 @@ class TvExpandDesc(ctypes.Structure):
 
 class TvLmHeadDesc(ctypes.Structure):
     _fields_ = [(n, ctypes.c_int32) for n in ("rows", "hidden", "vocab")]
+
+
+class TvLogitsDesc(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in
+                ("batch", "vocab", "max_nodes", "total_rows", "logits_dtype", "biases")]
 
 
 class TvWindow(ctypes.Structure):
@@ -105,6 +114,14 @@ _SIG = {
     "tv_kv4_attn_plan": [ctypes.POINTER(TvDesc), ctypes.POINTER(TvWindow), ctypes.POINTER(TvPlan)],
     "tree_verify_attn_kv4": [ctypes.POINTER(TvDesc), ctypes.POINTER(TvWindow)] + [_P] * 12
                             + [ctypes.c_size_t, _P, _P],
+    "tv_prompt_rope_store": [ctypes.POINTER(TvDesc), ctypes.c_int64, ctypes.c_int64, ctypes.c_double] + [_P] * 14,
+    "tv_prompt_workspace_size": [ctypes.POINTER(TvDesc), ctypes.c_int64, ctypes.c_int64,
+                                 ctypes.POINTER(ctypes.c_size_t)],
+    "tv_prompt_attn_plan": [ctypes.POINTER(TvDesc), ctypes.c_int64, ctypes.c_int64, ctypes.POINTER(TvPlan)],
+    "tv_prompt_attn": [ctypes.POINTER(TvDesc), ctypes.c_int64, ctypes.c_int64] + [_P] * 10
+                      + [ctypes.c_size_t, _P, _P],
+    "tv_token_counts_add": [ctypes.POINTER(TvLogitsDesc), _P, _P, ctypes.c_int64, _I, _P, _P, _P],
+    "tv_tree_logits_process": [ctypes.POINTER(TvLogitsDesc)] + [_P] * 13,
 }
 
 
@@ -369,3 +386,52 @@ def tree_verify_attn_kv4(desc, win, q, k4, v4, page_table, prefix_len, node_offs
                                       _ptr(depth), _ptr(out), _ptr(workspace), int(workspace_bytes), _ptr(status),
                                       _stream(stream)),
            "tree_verify_attn_kv4")
+
+
+def tv_prompt_rope_store(desc, rows, max_rows, theta, q_in, k_in, v_in, prefix_len, row_offsets, q_out, k_rows, v_rows,
+                         k_cache, v_cache, page_table, new_prefix_len, status, stream=None):
+    _check(lib().tv_prompt_rope_store(ctypes.byref(desc), int(rows), int(max_rows), float(theta), _ptr(q_in),
+                                      _ptr(k_in), _ptr(v_in), _ptr(prefix_len), _ptr(row_offsets), _ptr(q_out),
+                                      _ptr(k_rows), _ptr(v_rows), _ptr(k_cache), _ptr(v_cache), _ptr(page_table),
+                                      _ptr(new_prefix_len), _ptr(status), _stream(stream)), "tv_prompt_rope_store")
+
+
+def tv_prompt_workspace_size(desc: TvDesc, rows: int, max_rows: int) -> int:
+    n = ctypes.c_size_t(0)
+    _check(lib().tv_prompt_workspace_size(ctypes.byref(desc), int(rows), int(max_rows), ctypes.byref(n)),
+           "tv_prompt_workspace_size")
+    return n.value
+
+
+def tv_prompt_attn_plan(desc: TvDesc, rows: int, max_rows: int) -> dict:
+    p = TvPlan()
+    _check(lib().tv_prompt_attn_plan(ctypes.byref(desc), int(rows), int(max_rows), ctypes.byref(p)),
+           "tv_prompt_attn_plan")
+    return _plan_dict(p)
+
+
+def tv_prompt_attn(desc, rows, max_rows, q, k_cache, v_cache, page_table, prefix_len, row_offsets, k_rows, v_rows, out,
+                   workspace, workspace_bytes, status, stream=None):
+    _check(lib().tv_prompt_attn(ctypes.byref(desc), int(rows), int(max_rows), _ptr(q), _ptr(k_cache), _ptr(v_cache),
+                                _ptr(page_table), _ptr(prefix_len), _ptr(row_offsets), _ptr(k_rows), _ptr(v_rows),
+                                _ptr(out), _ptr(workspace), int(workspace_bytes), _ptr(status), _stream(stream)),
+           "tv_prompt_attn")
+
+
+def make_logits_desc(*, batch, vocab, max_nodes, total_rows, logits_dtype, biases=0) -> TvLogitsDesc:
+    return TvLogitsDesc(batch, vocab, max_nodes, total_rows, logits_dtype, biases)
+
+
+def tv_token_counts_add(desc, tokens_buf, offsets, tokens, prompt, counts, status, stream=None):
+    """`tokens` tokens in all with `offsets`, or that many of every sequence where offsets is None."""
+    _check(lib().tv_token_counts_add(ctypes.byref(desc), _ptr(tokens_buf), _ptr(offsets), int(tokens),
+                                     1 if prompt else 0, _ptr(counts), _ptr(status), _stream(stream)),
+           "tv_token_counts_add")
+
+
+def tv_tree_logits_process(desc, logits, counts, penalties, bias_offsets, bias_tokens, bias_values, mask, draft_tokens,
+                           node_offsets, anc, out, status, stream=None):
+    _check(lib().tv_tree_logits_process(ctypes.byref(desc), _ptr(logits), _ptr(counts), _ptr(penalties),
+                                        _ptr(bias_offsets), _ptr(bias_tokens), _ptr(bias_values), _ptr(mask),
+                                        _ptr(draft_tokens), _ptr(node_offsets), _ptr(anc), _ptr(out), _ptr(status),
+                                        _stream(stream)), "tv_tree_logits_process")

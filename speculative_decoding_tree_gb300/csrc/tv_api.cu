@@ -6,6 +6,7 @@
 #include <cstring>
 
 #include "tree_expand.h"
+#include "tree_logits.h"
 #include "tv_internal.cuh"
 #include "tv_accept.cuh"
 #include "tv_host.cuh"
@@ -369,6 +370,7 @@ const char* tv_status_string(int code) {
     case TV_DEV_TIMEOUT: return "device: bounded wait ran out";
     case TV_DEV_BAD_LOGITS: return "device: +inf draft logit (node not expanded)";
     case TV_DEV_BAD_STEP: return "device: expansion step out of order";
+    case TV_DEV_BAD_TOKEN: return "device: token outside the vocabulary";
     default: return "unknown";
   }
 }
