@@ -37,9 +37,9 @@ int make_prompt_plan(const tv_desc* d, int64_t rows, int64_t max_rows, PromptPla
   const int G = d->num_q_heads / d->num_kv_heads;
   if (max_rows > rows) max_rows = rows;
   p->pub = tv_plan{};
-  p->pub.kernel = 0;
-  p->rows_per_unit = prompt_simt_rows(d->head_dim);
-  p->pub.rows_per_tile = p->rows_per_unit;
+  p->pub.kernel = prompt_tc_supported(d, rows) ? 6 : 0;
+  p->pub.rows_per_tile = p->pub.kernel ? 128 / G * G : prompt_simt_rows(d->head_dim);
+  p->rows_per_unit = p->pub.kernel ? 2 * p->pub.rows_per_tile : p->pub.rows_per_tile;
   p->units = prompt_units(rows, max_rows, d->batch, G, p->rows_per_unit);
   const int64_t tiles = (d->max_prefix + kPromptTile - 1) / kPromptTile + (max_rows + kPromptTile - 1) / kPromptTile;
   // Few units of many keys are split over the keys, so that about every SM
@@ -142,7 +142,7 @@ int tv_prompt_attn(const tv_desc* desc, int64_t rows, int64_t max_rows, const vo
   const float scale = desc->scale > 0.f ? desc->scale : 1.0f / std::sqrt((float)desc->head_dim);
   p.scale_log2 = scale * 1.4426950408889634f;
   const cudaStream_t s = as_stream(stream);
-  cudaError_t e = launch_prompt_simt(p, desc->dtype, pl.units, s);
+  cudaError_t e = pl.pub.kernel == 6 ? launch_prompt_tc(p, pl.units, s) : launch_prompt_simt(p, desc->dtype, pl.units, s);
   if (e == cudaSuccess && split) e = launch_prompt_merge(p, s);
   return e == cudaSuccess ? TV_OK : TV_ERR_CUDA;
 }
