@@ -37,14 +37,14 @@ int make_prompt_plan(const tv_desc* d, int64_t rows, int64_t max_rows, PromptPla
   const int G = d->num_q_heads / d->num_kv_heads;
   if (max_rows > rows) max_rows = rows;
   p->pub = tv_plan{};
-  p->pub.kernel = prompt_tc_supported(d, rows) ? 6 : 0;
+  p->pub.kernel = prompt_tc_supported(d, rows) ? (d->head_dim == 128 ? 6 : 7) : 0;
   p->pub.rows_per_tile = p->pub.kernel ? 128 / G * G : prompt_simt_rows(d->head_dim);
   p->rows_per_unit = p->pub.kernel ? 2 * p->pub.rows_per_tile : p->pub.rows_per_tile;
   p->units = prompt_units(rows, max_rows, d->batch, G, p->rows_per_unit);
   const int64_t tiles = (d->max_prefix + kPromptTile - 1) / kPromptTile + (max_rows + kPromptTile - 1) / kPromptTile;
   // Few units of many keys are split over the keys, so that about every SM
   // has one, in chunks of four tiles or more.
-  const int64_t ctas = p->units * d->num_kv_heads, sms = num_sms();
+  const int64_t ctas = p->units * d->num_kv_heads * (p->pub.kernel == 7 ? d->head_dim / 128 : 1), sms = num_sms();
   int64_t want = ctas > 0 ? sms / ctas : 1;
   if (want > tiles / 4) want = tiles / 4;
   if (want < 1) want = 1;
@@ -142,7 +142,9 @@ int tv_prompt_attn(const tv_desc* desc, int64_t rows, int64_t max_rows, const vo
   const float scale = desc->scale > 0.f ? desc->scale : 1.0f / std::sqrt((float)desc->head_dim);
   p.scale_log2 = scale * 1.4426950408889634f;
   const cudaStream_t s = as_stream(stream);
-  cudaError_t e = pl.pub.kernel == 6 ? launch_prompt_tc(p, pl.units, s) : launch_prompt_simt(p, desc->dtype, pl.units, s);
+  cudaError_t e = pl.pub.kernel == 7   ? launch_prompt_tc2(p, pl.units, s)
+                  : pl.pub.kernel == 6 ? launch_prompt_tc(p, pl.units, s)
+                                       : launch_prompt_simt(p, desc->dtype, pl.units, s);
   if (e == cudaSuccess && split) e = launch_prompt_merge(p, s);
   return e == cudaSuccess ? TV_OK : TV_ERR_CUDA;
 }

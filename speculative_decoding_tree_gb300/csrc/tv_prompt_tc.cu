@@ -447,7 +447,7 @@ bool prompt_tc_supported(const tv_desc* d, int64_t rows) {
   int64_t cache = d->page_size ? d->num_pages * d->num_kv_heads * kPageSize
                                : (int64_t)d->batch * d->num_kv_heads * d->capacity;
   if (d->max_prefix == 0) cache = 0;
-  return d->dtype == TV_BF16 && d->head_dim == D && G <= BM && cache <= most && rows * d->num_kv_heads <= most;
+  return d->dtype == TV_BF16 && G <= BM && cache <= most && rows * d->num_kv_heads <= most;
 }
 
 cudaError_t launch_prompt_tc(const PromptParams& p, int64_t units, cudaStream_t st) {
