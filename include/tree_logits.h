@@ -15,7 +15,7 @@
  * in fp32, in this order, rounded once to the logits' type.  So every tree row
  * is steered as plain decoding would steer it after that row's path.  A row
  * whose mask allows nothing is -inf everywhere (its argmax is token 0).  NaN
- * stays NaN where it is allowed.
+ * stays NaN where it is allowed, and -inf stays -inf.
  *
  * Counts.  One 16-bit word per sequence and token, in rows of
  * (vocab + 7) / 8 * 8 words: bit 15 is set when the token stands in the

@@ -154,10 +154,24 @@ def _ptr(x):
     return x.data_ptr()
 
 
+_CURRENT_STREAM = None
+
+
+def _current_stream():
+    """The current stream of the current device, as an address.  torch's stream object takes 3 us to make, as long as
+    the launch itself; the address alone is what is needed."""
+    global _CURRENT_STREAM
+    if _CURRENT_STREAM is None:
+        import torch
+        torch.cuda.current_stream()                   # initialises torch's CUDA state
+        raw, dev = (getattr(torch._C, n, None) for n in ("_cuda_getCurrentRawStream", "_cuda_getDevice"))
+        _CURRENT_STREAM = (lambda: raw(dev())) if raw and dev else (lambda: torch.cuda.current_stream().cuda_stream)
+    return _CURRENT_STREAM()
+
+
 def _stream(s):
     if s is None:
-        import torch
-        return torch.cuda.current_stream().cuda_stream
+        return _current_stream()
     if isinstance(s, int):
         return s
     return s.cuda_stream

@@ -9,6 +9,7 @@
 // head, whose halves are d / 2 apart.  Bound by the bytes: q read and written,
 // k and v read once and written to the rows and to the cache.
 #include <cmath>
+#include <cstring>
 
 #include "tv_host.cuh"
 #include "tv_prompt.cuh"
@@ -212,8 +213,19 @@ int tv_prompt_rope_store(const tv_desc* desc, int64_t rows, int64_t max_rows, do
   p.rows = rows;
   p.max_rows = max_rows < rows ? max_rows : rows;
   p.capacity = desc->capacity; p.num_pages = desc->num_pages; p.max_prefix = desc->max_prefix;
-  for (int j = 0; j < p.d / 2; ++j)
-    p.turns[j] = (uint64_t)(std::pow(theta, -2.0 * j / p.d) * 0.15915494309189535 * 18446744073709551616.0);
+  // the host's last table: its powers take longer than the launch of a short call
+  static thread_local struct {
+    double theta;
+    int d;
+    uint64_t turns[256];
+  } last = {0.0, 0, {}};
+  if (last.theta != theta || last.d != p.d) {
+    for (int j = 0; j < p.d / 2; ++j)
+      last.turns[j] = (uint64_t)(std::pow(theta, -2.0 * j / p.d) * 0.15915494309189535 * 18446744073709551616.0);
+    last.theta = theta;
+    last.d = p.d;
+  }
+  std::memcpy(p.turns, last.turns, sizeof(uint64_t) * (p.d / 2));
   // one row a CTA while that leaves SMs idle, then four
   p.rows_per_cta = rows >= (int64_t)8 * num_sms() ? kMaxRows : 1;
   const unsigned grid = (unsigned)((rows + p.rows_per_cta - 1) / p.rows_per_cta + 1);
