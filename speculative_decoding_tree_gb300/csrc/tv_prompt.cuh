@@ -115,7 +115,8 @@ __host__ __device__ inline int64_t prompt_slot(int64_t row, int h, int s, int Hq
 int validate_prompt(const tv_desc* d, int64_t rows, int64_t max_rows);
 cudaError_t launch_prompt_simt(const PromptParams& p, int dtype, int64_t units, cudaStream_t s);
 cudaError_t launch_prompt_merge(const PromptParams& p, cudaStream_t s);
-int prompt_simt_rows(int d);                        // rows_per_unit of the CUDA-core kernel
+int prompt_simt_rows();                             // rows_per_unit of the CUDA-core kernel
+int prompt_simt_ctas_per_sm(int d);
 bool prompt_tc_supported(const tv_desc* d, int64_t rows);   // the tensor-core kernels' tiles fit the call
 cudaError_t launch_prompt_tc(const PromptParams& p, int64_t units, cudaStream_t s);
 cudaError_t launch_prompt_tc2(const PromptParams& p, int64_t units, cudaStream_t s);

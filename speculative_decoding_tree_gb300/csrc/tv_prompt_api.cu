@@ -38,15 +38,19 @@ int make_prompt_plan(const tv_desc* d, int64_t rows, int64_t max_rows, PromptPla
   if (max_rows > rows) max_rows = rows;
   p->pub = tv_plan{};
   p->pub.kernel = prompt_tc_supported(d, rows) ? (d->head_dim == 128 ? 6 : 7) : 0;
-  p->pub.rows_per_tile = p->pub.kernel ? 128 / G * G : prompt_simt_rows(d->head_dim);
+  p->pub.rows_per_tile = p->pub.kernel ? 128 / G * G : prompt_simt_rows();
   p->rows_per_unit = p->pub.kernel ? 2 * p->pub.rows_per_tile : p->pub.rows_per_tile;
   p->units = prompt_units(rows, max_rows, d->batch, G, p->rows_per_unit);
   const int64_t tiles = (d->max_prefix + kPromptTile - 1) / kPromptTile + (max_rows + kPromptTile - 1) / kPromptTile;
-  // Few units of many keys are split over the keys, so that about every SM
-  // has one, in chunks of four tiles or more.
+  // Few units of many keys are split over the keys: on the tensor cores so
+  // that about every SM has one, in chunks of four tiles or more; on the CUDA
+  // cores into about three waves (rows further down see more keys, and short
+  // chunks even that out), in chunks of two tiles or more.
   const int64_t ctas = p->units * d->num_kv_heads * (p->pub.kernel == 7 ? d->head_dim / 128 : 1), sms = num_sms();
-  int64_t want = ctas > 0 ? sms / ctas : 1;
-  if (want > tiles / 4) want = tiles / 4;
+  const int64_t slots = p->pub.kernel ? sms : 3 * sms * prompt_simt_ctas_per_sm(d->head_dim);
+  const int64_t least = p->pub.kernel ? 4 : 2;
+  int64_t want = ctas > 0 ? slots / ctas : 1;
+  if (want > tiles / least) want = tiles / least;
   if (want < 1) want = 1;
   const int64_t chunk = tiles > 0 ? (tiles + want - 1) / want : 1;
   const int64_t splits = tiles > 0 ? (tiles + chunk - 1) / chunk : 1;

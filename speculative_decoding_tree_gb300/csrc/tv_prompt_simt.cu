@@ -1,27 +1,30 @@
 // Causal prompt attention on the CUDA cores (fp32, and head groups the tensor
 // cores' tiles do not take), and the merge of split rows.
 //
-// One CTA of 256 threads takes a unit of BM query rows (128, at head_dim 512
-// 64) and walks its keys 64 at a time with the running maximum and sum of the
-// softmax: S = Q K^T in 8 x 4 (4 x 4) blocks per thread, weights through
-// shared memory, O += P V in registers (rows x d / 16 values per thread).  K
-// and V come in pieces of 16 KB through two shared buffers, the next piece
-// held in registers while the present one is multiplied.  Bound by the fp32
-// units and the shared-memory reads that feed them.
+// One CTA of 256 threads takes a unit of 64 query rows and walks its keys 64
+// at a time with the running maximum and sum of the softmax: S = Q K^T in 4 x
+// 4 blocks per thread, weights through shared memory, O += P V in registers
+// (4 rows x d / 16 values per thread), all products in packed pairs.  K and V
+// come in pieces of 8 KB through two shared buffers, the next piece held in
+// registers while the present one is multiplied; the 64 keys' places are found
+// once a step.  64 rows and 8 KB leave room for two CTAs an SM up to head_dim
+// 256, whose barriers then overlap.  Bound by the fp32 units and the shared
+// memory reads that feed them.
+#include "tv_f32x2.cuh"
 #include "tv_prompt.cuh"
 
 namespace tv {
 namespace {
 
 constexpr int kThreads = 256;
+constexpr int RPT = 4;                              // rows per thread
+constexpr int BM = 16 * RPT;
 constexpr int BN = 64;                              // keys a step
-constexpr int KD = 64;                              // channels of a K piece
+constexpr int KD = 32;                              // channels of a K piece
 constexpr int kPiece = BN * KD;                     // floats of a piece of K or V
 
 template <int D>
 struct SCfg {
-  static constexpr int RPT = D == 512 ? 4 : 8;      // rows per thread
-  static constexpr int BM = 16 * RPT;
   static constexpr int QS = D + 4;                  // row strides, padded against bank conflicts
   static constexpr int PS = BN + 4;
   static constexpr int KS = KD + 4;
@@ -42,20 +45,22 @@ __device__ __forceinline__ float4 load4(const void* base, int64_t elem) {
 }
 
 template <bool BF16, int D>
-__global__ void __launch_bounds__(kThreads, 1) prompt_simt_kernel(const __grid_constant__ PromptParams p) {
+__global__ void __launch_bounds__(kThreads, D == 512 ? 1 : 2)
+prompt_simt_kernel(const __grid_constant__ PromptParams p) {
   using C = SCfg<D>;
-  constexpr int RPT = C::RPT, BM = C::BM, OC = C::OC;
+  constexpr int OC = C::OC;
   extern __shared__ __align__(16) float smem[];
   float* sQ = smem;
   float* sP = sQ + BM * C::QS;
   float* sB = sP + BM * C::PS;
+  __shared__ int64_t s_at[2][BN];                   // first element of a step's keys, -1: none (zeros)
   __shared__ int s_b, s_i, s_bad;
   const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
   dep_wait();
   dep_launch();
   const int s = blockIdx.x % p.splits;
-  const int64_t rest = blockIdx.x / p.splits;
-  const int g = (int)(rest % p.Hkv);
+  const int rest = blockIdx.x / p.splits;
+  const int g = rest % p.Hkv;
   if (tid < 32) {
     int b = -1, i = 0;
     if (!find_unit(p, rest / p.Hkv, &b, &i)) b = -1;
@@ -74,11 +79,34 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_simt_kernel(const __grid_c
   if (P != Praw && tid == 0) set_status(p.status, TV_DEV_BAD_PREFIX);
   const int64_t m0 = (int64_t)s_i * BM, nrows = n * p.G;
   const int64_t mlast = min(nrows, m0 + BM) - 1;
-  const int64_t Pt = (P + kPromptTile - 1) / kPromptTile;
-  const int64_t t_begin = (int64_t)s * p.chunk_tiles;
-  const int64_t t_end = min(Pt + mlast / p.G / kPromptTile + 1, t_begin + p.chunk_tiles);
+  const int Pt = (int)((P + kPromptTile - 1) / kPromptTile);
+  const int t_begin = s * p.chunk_tiles;
+  const int t_end = min(Pt + (int)(mlast / p.G / kPromptTile) + 1, t_begin + p.chunk_tiles);
   if (t_begin >= t_end) return;
+  // steps of 64 keys; the last may lie past every row's keys
+  const int step0 = t_begin * 2, psteps = Pt * 2;
+  int step1 = t_end * 2;
+  if (t_end > Pt && mlast / p.G - (int64_t)(t_end - 1 - Pt) * kPromptTile < BN) --step1;
 
+  // places of step st's keys
+  auto find_keys = [&](int st) {
+    if (tid >= BN) return;
+    const int64_t key = (int64_t)(st < psteps ? st : st - psteps) * BN + tid;
+    int64_t at = -1;
+    if (st >= psteps) {
+      if (key < n) at = ((int64_t)g * p.rows + o0 + key) * D;
+    } else if (key < P) {
+      if (!p.paged) {
+        at = (((int64_t)b * p.Hkv + g) * p.capacity + key) * D;
+      } else {
+        const int pid = p.page_table[(int64_t)b * p.max_pages + key / kPageSize];
+        if (pid >= 0 && pid < p.num_pages) at = (((int64_t)pid * p.Hkv + g) * kPageSize + key % kPageSize) * D;
+        else s_bad = 1;
+      }
+    }
+    s_at[st & 1][tid] = at;
+  };
+  find_keys(step0);
   for (int e = tid; e < BM * (D / 4); e += kThreads) {
     const int r = e / (D / 4), c = (e % (D / 4)) * 4;
     float4 v = make_float4(0, 0, 0, 0);
@@ -86,157 +114,139 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_simt_kernel(const __grid_c
       v = load4<BF16>(p.q, ((o0 + (m0 + r) / p.G) * p.Hq + g * p.G + (m0 + r) % p.G) * D + c);
     *reinterpret_cast<float4*>(sQ + r * C::QS + c) = v;
   }
-  int64_t seen[RPT];                                // own rows this row sees: 0 .. seen
+  int seen[RPT];                                    // own rows this row sees: 0 .. seen
 #pragma unroll
-  for (int i = 0; i < RPT; ++i) seen[i] = (m0 + ty * RPT + i) / p.G;
+  for (int i = 0; i < RPT; ++i) seen[i] = (int)(min(m0 + ty * RPT + i, nrows - 1) / p.G);
+  __syncthreads();
 
-  // first element of key j of step st (64 keys), or -1: past the prefix or the rows, or on a bad page
-  const int64_t steps = (t_end - t_begin) * 2, step0 = t_begin * 2, psteps = Pt * 2;
-  auto key_elem = [&](int64_t st, int j, bool* own) -> int64_t {
-    const int64_t at = st * BN + j;
-    *own = st >= psteps;
-    if (*own) {
-      const int64_t i = at - psteps * BN;
-      return i < n ? ((int64_t)g * p.rows + o0 + i) * D : -1;
-    }
-    if (at >= P) return -1;
-    if (!p.paged) return (((int64_t)b * p.Hkv + g) * p.capacity + at) * D;
-    const int pid = p.page_table[(int64_t)b * p.max_pages + at / kPageSize];
-    if (pid < 0 || pid >= p.num_pages) {
-      s_bad = 1;
-      return -1;
-    }
-    return (((int64_t)pid * p.Hkv + g) * kPageSize + at % kPageSize) * D;
-  };
-  // piece c of step st: K pieces 0 .. D / 64 - 1 (64 keys x 64 channels), then V pieces (VK keys x D)
+  // piece c of step st: K pieces 0 .. D / 32 - 1 (64 keys x 32 channels), then V pieces (VK keys x D)
   constexpr int KP = D / KD, NP = KP + BN / C::VK;
-  float4 hold[4];
-  auto fetch = [&](int64_t st, int c) {
+  float4 hold[2];
+  auto fetch = [&](int st, int c) {
+    const bool own = st >= psteps, isk = c < KP;
+    const void* src = isk ? (own ? p.k_rows : p.k_cache) : (own ? p.v_rows : p.v_cache);
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const int f = (tid + e * kThreads) * 4;       // of the piece's 4096 floats
-      const bool isk = c < KP;
+    for (int e = 0; e < 2; ++e) {
+      const int f = (tid + e * kThreads) * 4;       // of the piece's 2048 floats
       const int j = isk ? f / KD : (c - KP) * C::VK + f / D;
       const int ch = isk ? c * KD + f % KD : f % D;
-      bool own;
-      const int64_t at = key_elem(st, j, &own);
-      const void* src = isk ? (own ? p.k_rows : p.k_cache) : (own ? p.v_rows : p.v_cache);
+      const int64_t at = s_at[st & 1][j];
       hold[e] = at < 0 ? make_float4(0, 0, 0, 0) : load4<BF16>(src, at + ch);
     }
   };
   auto put = [&](int c, float* buf) {
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
+    for (int e = 0; e < 2; ++e) {
       const int f = (tid + e * kThreads) * 4;
-      const int at = c < KP ? f / KD * C::KS + f % KD : f;
-      *reinterpret_cast<float4*>(buf + at) = hold[e];
+      *reinterpret_cast<float4*>(buf + (c < KP ? f / KD * C::KS + f % KD : f)) = hold[e];
     }
   };
 
-  float4 o[RPT][OC];
+  uint64_t o[RPT][OC][2];                           // pairs of columns
   float m_run[RPT], l_run[RPT];
 #pragma unroll
   for (int i = 0; i < RPT; ++i) {
     m_run[i] = -INFINITY;
     l_run[i] = 0.f;
 #pragma unroll
-    for (int c = 0; c < OC; ++c) o[i][c] = make_float4(0, 0, 0, 0);
+    for (int c = 0; c < OC; ++c) o[i][c][0] = o[i][c][1] = 0ull;
   }
   int par = 0;
   fetch(step0, 0);
-  for (int64_t st = step0; st < step0 + steps; ++st) {
-    float sc[RPT][4];
+  for (int st = step0; st < step1; ++st) {
+    if (st + 1 < step1) find_keys(st + 1);          // seen by the others after the next barrier
+    uint64_t sc[RPT][4];                            // sums of the even and of the odd channels
 #pragma unroll
     for (int i = 0; i < RPT; ++i)
 #pragma unroll
-      for (int j = 0; j < 4; ++j) sc[i][j] = 0.f;
+      for (int j = 0; j < 4; ++j) sc[i][j] = 0ull;
 #pragma unroll 1
-    for (int c = 0; c < NP; ++c) {
+    for (int c = 0; c < KP; ++c) {
+      float* buf = sB + par * C::BUF;
+      par ^= 1;
+      put(c, buf);
+      __syncthreads();
+      fetch(st, c + 1);
+#pragma unroll
+      for (int k = 0; k < KD; k += 4) {
+        ulonglong2 kv[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) kv[j] = *reinterpret_cast<const ulonglong2*>(buf + (tx + 16 * j) * C::KS + k);
+#pragma unroll
+        for (int i = 0; i < RPT; ++i) {
+          const ulonglong2 qv = *reinterpret_cast<const ulonglong2*>(sQ + (ty * RPT + i) * C::QS + c * KD + k);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) sc[i][j] = ffma2(qv.y, kv[j].y, ffma2(qv.x, kv[j].x, sc[i][j]));
+        }
+      }
+    }
+    // mask, running maximum and sum; a row's 64 scores lie with the 16 threads of its half warp
+    const bool own = st >= psteps;
+    const int64_t j0 = (int64_t)(own ? st - psteps : st) * BN;
+#pragma unroll
+    for (int i = 0; i < RPT; ++i) {
+      const int64_t lim = (own ? (int64_t)seen[i] : P - 1) - j0 - tx;   // keys 16 j up to here are seen
+      float x[4], mx = -INFINITY;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float2 v = up2(sc[i][j]);
+        x[j] = 16 * j <= lim ? (v.x + v.y) * p.scale_log2 : -INFINITY;
+        mx = fmaxf(mx, x[j]);
+      }
+#pragma unroll
+      for (int a = 8; a > 0; a >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, a));
+      const float m_new = fmaxf(m_run[i], mx);
+      const float ref = m_new == -INFINITY ? 0.f : m_new;
+      const float alpha = exp2f(m_run[i] - ref);
+      float sum = 0.f;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float w = exp2f(x[j] - ref);
+        sum += w;
+        sP[(ty * RPT + i) * C::PS + tx + 16 * j] = w;
+      }
+#pragma unroll
+      for (int a = 8; a > 0; a >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, a);
+      l_run[i] = l_run[i] * alpha + sum;
+      m_run[i] = m_new;
+      const uint64_t a2 = pk2(alpha, alpha);
+#pragma unroll
+      for (int c = 0; c < OC; ++c) {
+        o[i][c][0] = ffma2(o[i][c][0], a2, 0ull);
+        o[i][c][1] = ffma2(o[i][c][1], a2, 0ull);
+      }
+    }
+    __syncwarp();
+#pragma unroll 1
+    for (int c = KP; c < NP; ++c) {
       float* buf = sB + par * C::BUF;
       par ^= 1;
       put(c, buf);
       __syncthreads();
       if (c + 1 < NP) fetch(st, c + 1);
-      else if (st + 1 < step0 + steps) fetch(st + 1, 0);
-      if (c < KP) {
-#pragma unroll 4
-        for (int k = 0; k < KD; k += 4) {
-          float4 kv[4];
+      else if (st + 1 < step1) fetch(st + 1, 0);
+      const int k0 = (c - KP) * C::VK;
+#pragma unroll(C::VK > 8 ? 2 : 1)
+      for (int k = 0; k < C::VK; k += 4) {
+        float4 w[RPT];
 #pragma unroll
-          for (int j = 0; j < 4; ++j) kv[j] = *reinterpret_cast<const float4*>(buf + (tx + 16 * j) * C::KS + k);
+        for (int i = 0; i < RPT; ++i)
+          w[i] = *reinterpret_cast<const float4*>(sP + (ty * RPT + i) * C::PS + k0 + k);
 #pragma unroll
-          for (int i = 0; i < RPT; ++i) {
-            const float4 qv = *reinterpret_cast<const float4*>(sQ + (ty * RPT + i) * C::QS + c * KD + k);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              float a = fmaf(qv.x, kv[j].x, sc[i][j]);
-              a = fmaf(qv.y, kv[j].y, a);
-              a = fmaf(qv.z, kv[j].z, a);
-              sc[i][j] = fmaf(qv.w, kv[j].w, a);
-            }
-          }
-        }
-        if (c == KP - 1) {
-          // mask, running maximum and sum; a row's 64 scores lie with the 16 threads of its half warp
-          const bool own = st >= psteps;
-          const int64_t j0 = own ? (st - psteps) * BN : st * BN;
+        for (int kk = 0; kk < 4; ++kk) {
+          uint64_t w2[RPT];
 #pragma unroll
           for (int i = 0; i < RPT; ++i) {
-            float mx = -INFINITY;
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              const int64_t key = j0 + tx + 16 * j;
-              const bool vis = own ? key <= seen[i] && key < n : key < P;
-              sc[i][j] = vis ? sc[i][j] * p.scale_log2 : -INFINITY;
-              mx = fmaxf(mx, sc[i][j]);
-            }
-#pragma unroll
-            for (int x = 8; x > 0; x >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, x));
-            const float m_new = fmaxf(m_run[i], mx);
-            const float ref = m_new == -INFINITY ? 0.f : m_new;
-            const float alpha = exp2f(m_run[i] - ref);
-            float sum = 0.f;
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              const float w = exp2f(sc[i][j] - ref);
-              sum += w;
-              sP[(ty * RPT + i) * C::PS + tx + 16 * j] = w;
-            }
-#pragma unroll
-            for (int x = 8; x > 0; x >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, x);
-            l_run[i] = l_run[i] * alpha + sum;
-            m_run[i] = m_new;
-#pragma unroll
-            for (int c4 = 0; c4 < OC; ++c4) {
-              o[i][c4].x *= alpha;
-              o[i][c4].y *= alpha;
-              o[i][c4].z *= alpha;
-              o[i][c4].w *= alpha;
-            }
+            const float x = kk == 0 ? w[i].x : kk == 1 ? w[i].y : kk == 2 ? w[i].z : w[i].w;
+            w2[i] = pk2(x, x);
           }
-          __syncwarp();
-        }
-      } else {
-        const int k0 = (c - KP) * C::VK;
-#pragma unroll 1
-        for (int k = 0; k < C::VK; k += 4) {
-          float4 w[RPT];
 #pragma unroll
-          for (int i = 0; i < RPT; ++i)
-            w[i] = *reinterpret_cast<const float4*>(sP + (ty * RPT + i) * C::PS + k0 + k);
+          for (int c4 = 0; c4 < OC; ++c4) {
+            const ulonglong2 v = *reinterpret_cast<const ulonglong2*>(buf + (k + kk) * D + tx * 4 + 64 * c4);
 #pragma unroll
-          for (int kk = 0; kk < 4; ++kk) {
-#pragma unroll
-            for (int c4 = 0; c4 < OC; ++c4) {
-              const float4 v = *reinterpret_cast<const float4*>(buf + (k + kk) * D + tx * 4 + 64 * c4);
-#pragma unroll
-              for (int i = 0; i < RPT; ++i) {
-                const float x = kk == 0 ? w[i].x : kk == 1 ? w[i].y : kk == 2 ? w[i].z : w[i].w;
-                o[i][c4].x = fmaf(x, v.x, o[i][c4].x);
-                o[i][c4].y = fmaf(x, v.y, o[i][c4].y);
-                o[i][c4].z = fmaf(x, v.z, o[i][c4].z);
-                o[i][c4].w = fmaf(x, v.w, o[i][c4].w);
-              }
+            for (int i = 0; i < RPT; ++i) {
+              o[i][c4][0] = ffma2(w2[i], v.x, o[i][c4][0]);
+              o[i][c4][1] = ffma2(w2[i], v.y, o[i][c4][1]);
             }
           }
         }
@@ -250,12 +260,14 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_simt_kernel(const __grid_c
     const int64_t row = o0 + m / p.G;
     const int h = g * p.G + (int)(m % p.G);
     const float inv = l_run[i] > 0.f ? 1.f / l_run[i] : (l_run[i] == 0.f ? 0.f : l_run[i]);
-    const bool split = (Pt + m / p.G / kPromptTile) / p.chunk_tiles > 0;
-    if (split && s > (Pt + m / p.G / kPromptTile) / p.chunk_tiles) continue;
+    const int my_s = (Pt + seen[i] / kPromptTile) / p.chunk_tiles;   // the row's last split
+    if (s > my_s) continue;
+    const bool split = my_s > 0;
     const int64_t slot = split ? prompt_slot(row, h, s, p.Hq, p.splits) : row * p.Hq + h;
 #pragma unroll
     for (int c4 = 0; c4 < OC; ++c4) {
-      const float4 v = make_float4(o[i][c4].x * inv, o[i][c4].y * inv, o[i][c4].z * inv, o[i][c4].w * inv);
+      const float2 lo = up2(o[i][c4][0]), hi = up2(o[i][c4][1]);
+      const float4 v = make_float4(lo.x * inv, lo.y * inv, hi.x * inv, hi.y * inv);
       const int64_t at = slot * D + tx * 4 + 64 * c4;
       if (split) *reinterpret_cast<float4*>(p.o_part + at) = v;
       else if (p.out_bf16)
@@ -343,7 +355,8 @@ cudaError_t launch_d(const PromptParams& p, int64_t units, cudaStream_t s) {
 
 }  // namespace
 
-int prompt_simt_rows(int d) { return d == 512 ? SCfg<512>::BM : d == 256 ? SCfg<256>::BM : SCfg<128>::BM; }
+int prompt_simt_rows() { return BM; }
+int prompt_simt_ctas_per_sm(int d) { return d == 512 ? 1 : 2; }
 
 cudaError_t launch_prompt_simt(const PromptParams& p, int dtype, int64_t units, cudaStream_t s) {
   const bool bf = dtype == TV_BF16;
