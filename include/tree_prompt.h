@@ -38,8 +38,9 @@
  * deterministic results.  rows = 0 or max_rows = 0 enqueues nothing (the
  * pointers are then not looked at).
  *
- * Device faults of both calls: a sequence whose offsets are invalid is skipped
- * (TV_DEV_BAD_OFFSETS); a prefix length out of range is clamped
+ * Device faults of both calls: where a sequence's offsets are invalid
+ * (TV_DEV_BAD_OFFSETS) it is skipped, and what the call leaves in the outputs of
+ * the others is undefined; a prefix length out of range is clamped
  * (TV_DEV_BAD_PREFIX).
  */
 #ifndef TREE_PROMPT_H
@@ -78,14 +79,20 @@ int tv_prompt_rope_store(const tv_desc* desc, int64_t rows, int64_t max_rows, do
                          int32_t* d_status, void* stream);
 
 /* Bytes of scratch tv_prompt_attn needs (256-byte aligned; any contents; one
- * call at a time), and the plan it runs: kernel 0 CUDA cores, 6 tcgen05 with
- * two query tiles a CTA, 7 tcgen05 on CTA pairs; chunk and num_splits count
- * keys in tiles of 128 (prefix and rows each rounded up). */
+ * call at a time), and the plan it runs: kernel 6 tcgen05 with two query tiles a
+ * CTA (bf16, head_dim 128), 7 tcgen05 on CTA pairs (bf16, 256 and 512), 8
+ * tcgen05 on numbers in three bf16 parts (fp32; bf16 with more than 128 query
+ * heads a KV head or a cache of 2^31 rows); chunk and num_splits count keys in
+ * tiles of 128 (prefix and rows each rounded up).  Kernel 8 keeps 12 bytes a
+ * value of K and V of max_prefix and the rows in the scratch. */
 int tv_prompt_workspace_size(const tv_desc* desc, int64_t rows, int64_t max_rows, size_t* bytes);
 int tv_prompt_attn_plan(const tv_desc* desc, int64_t rows, int64_t max_rows, tv_plan* plan);
 
 /* out[r, h, :] = sum_j softmax_j(scale * q[r,h,:] . k_j) v_j over the keys row
- * r sees.  fp32 inputs are computed in fp32 (no TF32); bf16 inputs are
+ * r sees.  fp32 inputs are computed to fp32 accuracy: each
+ * number as the sum of three bf16 ones (exact below 2^127 in magnitude; seen K
+ * and V must be finite), six products of them on the tensor cores, sums in fp32,
+ * the sum over the keys rounded to nearest from tile to tile.  bf16 inputs are
  * multiplied in bf16 with fp32 accumulation, an fp32 softmax and fp32
  * partials; each weight is rounded to bf16 (2^-8 of it at most) before it
  * multiplies V, while the sum that divides keeps the unrounded ones.

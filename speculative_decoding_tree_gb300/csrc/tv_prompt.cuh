@@ -31,6 +31,7 @@ struct PromptParams {
   void* out;
   float* o_part;             // [rows, Hq, splits, d] O_s / l_s of rows with two splits or more
   float2* ml_part;           // [rows, Hq, splits] running maximum (log2 units) and sum
+  void* split;               // fp32: the numbers in three bf16 parts, in blocks
   int32_t* status;
   int B, Hq, Hkv, G, d, paged, out_bf16;
   int rows_per_tile;         // query rows of a 128-row tile in use (tensor cores: a multiple of G)
@@ -113,12 +114,11 @@ __host__ __device__ inline int64_t prompt_slot(int64_t row, int h, int s, int Hq
 }
 
 int validate_prompt(const tv_desc* d, int64_t rows, int64_t max_rows);
-cudaError_t launch_prompt_simt(const PromptParams& p, int dtype, int64_t units, cudaStream_t s);
 cudaError_t launch_prompt_merge(const PromptParams& p, cudaStream_t s);
-int prompt_simt_rows();                             // rows_per_unit of the CUDA-core kernel
-int prompt_simt_ctas_per_sm(int d);
 bool prompt_tc_supported(const tv_desc* d, int64_t rows);   // the tensor-core kernels' tiles fit the call
 cudaError_t launch_prompt_tc(const PromptParams& p, int64_t units, cudaStream_t s);
+int64_t prompt_f32_bytes(const tv_desc* d, int64_t rows);   // of the blocks; -1: more than a call can have
+cudaError_t launch_prompt_f32(const PromptParams& p, int dtype, int64_t units, cudaStream_t s);
 cudaError_t launch_prompt_tc2(const PromptParams& p, int64_t units, cudaStream_t s);
 
 }  // namespace tv

@@ -12,7 +12,7 @@ struct PromptPlan {
   tv_plan pub;
   int64_t units;             // per KV head
   int rows_per_unit;
-  int64_t o_bytes, ml_bytes;
+  int64_t o_bytes, ml_bytes, split_bytes;
 };
 
 }  // namespace
@@ -37,20 +37,20 @@ int make_prompt_plan(const tv_desc* d, int64_t rows, int64_t max_rows, PromptPla
   const int G = d->num_q_heads / d->num_kv_heads;
   if (max_rows > rows) max_rows = rows;
   p->pub = tv_plan{};
-  p->pub.kernel = prompt_tc_supported(d, rows) ? (d->head_dim == 128 ? 6 : 7) : 0;
-  p->pub.rows_per_tile = p->pub.kernel ? 128 / G * G : prompt_simt_rows();
-  p->rows_per_unit = p->pub.kernel ? 2 * p->pub.rows_per_tile : p->pub.rows_per_tile;
+  p->pub.kernel = prompt_tc_supported(d, rows) ? (d->head_dim == 128 ? 6 : 7) : 8;
+  const bool parts = p->pub.kernel == 8;             // numbers in three parts: one query tile a unit, any grouping
+  p->pub.rows_per_tile = parts ? 128 : 128 / G * G;
+  p->rows_per_unit = parts ? 128 : 2 * p->pub.rows_per_tile;
   p->units = prompt_units(rows, max_rows, d->batch, G, p->rows_per_unit);
   const int64_t tiles = (d->max_prefix + kPromptTile - 1) / kPromptTile + (max_rows + kPromptTile - 1) / kPromptTile;
-  // Few units of many keys are split over the keys: on the tensor cores so
-  // that about every SM has one, in chunks of four tiles or more; on the CUDA
-  // cores into about three waves (rows further down see more keys, and short
-  // chunks even that out), in chunks of two tiles or more.
-  const int64_t ctas = p->units * d->num_kv_heads * (p->pub.kernel == 7 ? d->head_dim / 128 : 1), sms = num_sms();
-  const int64_t slots = p->pub.kernel ? sms : 3 * sms * prompt_simt_ctas_per_sm(d->head_dim);
-  const int64_t least = p->pub.kernel ? 4 : 2;
-  int64_t want = ctas > 0 ? slots / ctas : 1;
-  if (want > tiles / least) want = tiles / least;
+  // Few units of many keys are split over the keys: so that about every SM has
+  // one, in chunks of four tiles or more; kernel 8, whose tiles take longer,
+  // into about two waves of chunks of any length (2000 fp32 rows x 4 heads at
+  // head_dim 256: 175, 108, 144 and 129 us with 1, 2, 3 and 4).
+  const int64_t ctas = p->units * d->num_kv_heads * (p->pub.kernel >= 7 ? d->head_dim / 128 : 1), sms = num_sms();
+  int64_t want = ctas > 0 ? (parts ? 2 * sms : sms) / ctas : 1;
+  if (!parts && want > tiles / 4) want = tiles / 4;
+  if (want > tiles) want = tiles;
   if (want < 1) want = 1;
   const int64_t chunk = tiles > 0 ? (tiles + want - 1) / want : 1;
   const int64_t splits = tiles > 0 ? (tiles + chunk - 1) / chunk : 1;
@@ -61,13 +61,18 @@ int make_prompt_plan(const tv_desc* d, int64_t rows, int64_t max_rows, PromptPla
   p->pub.num_splits = (int)splits;
   p->pub.row_tiles = (int)((max_rows * G + p->pub.rows_per_tile - 1) / p->pub.rows_per_tile);
   p->pub.grid_ctas = (int)grid;
-  p->o_bytes = p->ml_bytes = 0;
+  p->o_bytes = p->ml_bytes = p->split_bytes = 0;
+  if (parts) {
+    p->split_bytes = prompt_f32_bytes(d, rows);
+    if (p->split_bytes < 0) return TV_ERR_OVERFLOW;
+  }
   if (splits > 1) {
     int64_t t;
     if (!mul_ok(rows, d->num_q_heads, &t) || !mul_ok(t, splits, &t) || !mul_ok(t, 8, &p->ml_bytes) ||
         !mul_ok(t, (int64_t)d->head_dim * 4, &p->o_bytes))
       return TV_ERR_OVERFLOW;
     if ((rows * d->num_q_heads + 7) / 8 > ((int64_t)1 << 31) - 1) return TV_ERR_OVERFLOW;   // the merge's grid
+    if (p->split_bytes > ((int64_t)1 << 62) - p->o_bytes || p->o_bytes > (int64_t)1 << 61) return TV_ERR_OVERFLOW;
     p->o_bytes = align_up(p->o_bytes, 256);
     p->ml_bytes = align_up(p->ml_bytes, 256);
   }
@@ -88,7 +93,7 @@ int tv_prompt_workspace_size(const tv_desc* desc, int64_t rows, int64_t max_rows
   PromptPlan p;
   rc = make_prompt_plan(desc, rows, max_rows, &p);
   if (rc) return rc;
-  *bytes = (size_t)(p.o_bytes + p.ml_bytes);
+  *bytes = (size_t)(p.o_bytes + p.ml_bytes + p.split_bytes);
   return TV_OK;
 }
 
@@ -115,14 +120,14 @@ int tv_prompt_attn(const tv_desc* desc, int64_t rows, int64_t max_rows, const vo
   if (rows == 0 || max_rows == 0) return TV_OK;
   const bool split = pl.pub.num_splits > 1, cache = desc->max_prefix > 0;
   if (!d_q || !d_prefix_len || !d_row_offsets || !d_k_rows || !d_v_rows || !d_out || !d_status ||
-      (split && !d_workspace) || (cache && (!d_k_cache || !d_v_cache)) ||
+      ((split || pl.split_bytes) && !d_workspace) || (cache && (!d_k_cache || !d_v_cache)) ||
       (cache && desc->page_size == kPageSize && !d_page_table))
     return TV_ERR_NULL;
   const void* all[] = {d_q,      d_k_cache, d_v_cache,   d_page_table, d_prefix_len, d_row_offsets,
                        d_k_rows, d_v_rows,  d_workspace, d_out,        d_status};
   for (const void* x : all)
     if (!aligned16(x)) return TV_ERR_ALIGN;
-  if ((int64_t)workspace_bytes < pl.o_bytes + pl.ml_bytes) return TV_ERR_WORKSPACE;
+  if ((int64_t)workspace_bytes < pl.o_bytes + pl.ml_bytes + pl.split_bytes) return TV_ERR_WORKSPACE;
   PromptParams p = {};
   p.q = d_q; p.k_cache = d_k_cache; p.v_cache = d_v_cache;
   p.page_table = desc->page_size ? d_page_table : nullptr;
@@ -130,6 +135,7 @@ int tv_prompt_attn(const tv_desc* desc, int64_t rows, int64_t max_rows, const vo
   p.out = d_out;
   p.o_part = reinterpret_cast<float*>(d_workspace);
   p.ml_part = reinterpret_cast<float2*>(reinterpret_cast<char*>(d_workspace) + pl.o_bytes);
+  p.split = reinterpret_cast<char*>(d_workspace) + pl.o_bytes + pl.ml_bytes;
   p.status = d_status;
   p.B = desc->batch; p.Hq = desc->num_q_heads; p.Hkv = desc->num_kv_heads; p.G = p.Hq / p.Hkv;
   p.d = desc->head_dim;
@@ -146,9 +152,9 @@ int tv_prompt_attn(const tv_desc* desc, int64_t rows, int64_t max_rows, const vo
   const float scale = desc->scale > 0.f ? desc->scale : 1.0f / std::sqrt((float)desc->head_dim);
   p.scale_log2 = scale * 1.4426950408889634f;
   const cudaStream_t s = as_stream(stream);
-  cudaError_t e = pl.pub.kernel == 7   ? launch_prompt_tc2(p, pl.units, s)
-                  : pl.pub.kernel == 6 ? launch_prompt_tc(p, pl.units, s)
-                                       : launch_prompt_simt(p, desc->dtype, pl.units, s);
+  cudaError_t e = pl.pub.kernel == 8   ? launch_prompt_f32(p, desc->dtype, pl.units, s)
+                  : pl.pub.kernel == 7   ? launch_prompt_tc2(p, pl.units, s)
+                                       : launch_prompt_tc(p, pl.units, s);
   if (e == cudaSuccess && split) e = launch_prompt_merge(p, s);
   return e == cudaSuccess ? TV_OK : TV_ERR_CUDA;
 }
