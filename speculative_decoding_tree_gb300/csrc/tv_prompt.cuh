@@ -36,6 +36,7 @@ struct PromptParams {
   int B, Hq, Hkv, G, d, paged, out_bf16;
   int rows_per_tile;         // query rows of a 128-row tile in use (tensor cores: a multiple of G)
   int rows_per_unit;
+  int unit_tokens;           // rows_per_unit / G where G divides it (tensor-core tiles of bf16), else 0
   int chunk_tiles, splits;   // ct, and the grid's splits
   int64_t rows, max_rows;
   int64_t capacity, num_pages, max_pages, max_prefix;
@@ -63,50 +64,89 @@ inline int64_t prompt_units(int64_t rows, int64_t max_rows, int B, int G, int ro
   return packed < padded ? packed : padded;
 }
 
-// Whole warp: unit u of the numbering above as (sequence, index of the unit in
-// it); false past the last.  f(L) = units at level L or above, over all
-// sequences; u's level is the largest L with f(L) > u.
-__device__ inline bool find_unit(const PromptParams& p, int64_t u, int* b_out, int* i_out) {
+// What a CTA works on: unit i of sequence b (-1: nothing), whose rows are
+// o0 .. o0 + n - 1 behind P cached positions.
+struct PromptUnit {
+  int b, i, o0, n;
+  int64_t P;
+};
+
+// Whole warp: unit u of the numbering above; lane 0 leaves it in *out.  f(L) =
+// units at level L or above, over all sequences; u's level is the largest L
+// with f(L) > u.  The first 128 sequences' sizes stay in registers.
+__device__ inline void find_unit(const PromptParams& p, unsigned u, PromptUnit* out) {
+  constexpr unsigned kAll = 0xffffffffu;
+  constexpr int K = 4;
   const int lane = threadIdx.x & 31;
-  auto tiles = [&](int b) -> int64_t {
-    if (b >= p.B) return 0;
-    int64_t o0, n;
-    prompt_rows(p.row_offsets, b, p.rows, p.max_rows, p.status, &o0, &n);
-    return (n * p.G + p.rows_per_unit - 1) / p.rows_per_unit;
+  auto units = [&](int64_t n) -> unsigned {
+    if (p.unit_tokens > 0) return ((unsigned)n + p.unit_tokens - 1) / (unsigned)p.unit_tokens;
+    return (unsigned)((n * p.G + p.rows_per_unit - 1) / p.rows_per_unit);
   };
-  auto sum = [](int64_t v) {
-    for (int s = 16; s > 0; s >>= 1) v += __shfl_xor_sync(0xffffffffu, v, s);
-    return v;
+  auto load = [&](int b, int64_t* o0, int64_t* n) {
+    *o0 = *n = 0;
+    if (b < p.B) prompt_rows(p.row_offsets, b, p.rows, p.max_rows, p.status, o0, n);
   };
-  const int64_t mine = tiles(lane);                 // of the first 32 sequences, kept in a register
-  auto at_or_above = [&](int64_t L) -> int64_t {
-    int64_t v = mine > L ? mine - L : 0;
-    for (int b = lane + 32; b < p.B; b += 32) {
-      const int64_t t = tiles(b);
-      if (t > L) v += t - L;
+  int64_t o0[K], n[K], P[K];
+  unsigned has[K], top = 0;
+#pragma unroll
+  for (int k = 0; k < K; ++k) {
+    const int b = lane + 32 * k;
+    P[k] = b < p.B ? p.prefix_len[b] : 0;
+    load(b, &o0[k], &n[k]);
+  }
+#pragma unroll
+  for (int k = 0; k < K; ++k) {
+    has[k] = units(n[k]);
+    top = max(top, has[k]);
+  }
+  auto each_later = [&](auto f) {                   // the units of sequences past the registers
+    for (int b = lane + 32 * K; b < p.B; b += 32) {
+      int64_t x, m;
+      load(b, &x, &m);
+      f(units(m));
     }
-    return sum(v);
   };
-  if (at_or_above(0) <= u) return false;
-  int64_t lo = 0, hi = (p.max_rows * p.G + p.rows_per_unit - 1) / p.rows_per_unit;   // f(lo) > u, f(hi) = 0
+  each_later([&](unsigned t) { top = max(top, t); });
+  auto at_or_above = [&](unsigned L) -> unsigned {
+    unsigned v = 0;
+#pragma unroll
+    for (int k = 0; k < K; ++k) v += has[k] > L ? has[k] - L : 0u;
+    each_later([&](unsigned t) { v += t > L ? t - L : 0u; });
+    return __reduce_add_sync(kAll, v);
+  };
+  unsigned lo = 0, hi = __reduce_max_sync(kAll, top);   // f(hi) = 0
+  if (at_or_above(0) <= u) {
+    if (lane == 0) *out = PromptUnit{-1, 0, 0, 0, 0};   // no rows, no tiles
+    return;
+  }
   while (hi - lo > 1) {
-    const int64_t mid = (lo + hi) >> 1;
+    const unsigned mid = (lo + hi) >> 1;
     if (at_or_above(mid) > u) lo = mid;
     else hi = mid;
   }
-  int64_t rank = u - at_or_above(lo + 1);           // among the sequences with a unit at this level
-  for (int b0 = 0; b0 < p.B; b0 += 32) {
-    const bool has = (b0 == 0 ? mine : tiles(b0 + lane)) > lo;
-    const unsigned m = __ballot_sync(0xffffffffu, has);
-    if (rank < __popc(m)) {
-      const bool me = has && __popc(m & ((1u << lane) - 1)) == rank;
-      *b_out = b0 + __ffs(__ballot_sync(0xffffffffu, me)) - 1;
-      *i_out = (int)lo;
-      return true;
+  unsigned rank = u - at_or_above(lo + 1);          // among the sequences with a unit at this level
+  auto take = [&](int b, bool mine, int64_t a, int64_t m, int64_t raw) -> bool {
+    const unsigned w = __ballot_sync(kAll, mine);
+    if (rank >= (unsigned)__popc(w)) {
+      rank -= __popc(w);
+      return false;
     }
-    rank -= __popc(m);
+    if (mine && (unsigned)__popc(w & ((1u << lane) - 1)) == rank) {
+      const int64_t c = clamp_prefix(raw, p.max_prefix, p.capacity);
+      if (c != raw) set_status(p.status, TV_DEV_BAD_PREFIX);
+      *out = PromptUnit{b, (int)lo, (int)a, (int)m, c};
+    }
+    return true;
+  };
+#pragma unroll
+  for (int k = 0; k < K; ++k)
+    if (take(lane + 32 * k, has[k] > lo, o0[k], n[k], P[k])) return;
+  for (int b0 = 32 * K; b0 < p.B; b0 += 32) {
+    const int b = b0 + lane;
+    int64_t a, m;
+    load(b, &a, &m);
+    if (take(b, units(m) > lo, a, m, b < p.B ? p.prefix_len[b] : 0)) return;
   }
-  return false;
 }
 
 __host__ __device__ inline int64_t prompt_slot(int64_t row, int h, int s, int Hq, int splits) {

@@ -143,6 +143,7 @@ int tv_prompt_attn(const tv_desc* desc, int64_t rows, int64_t max_rows, const vo
   p.out_bf16 = desc->dtype == TV_BF16 && !desc->out_f32;
   p.rows_per_tile = pl.pub.rows_per_tile;
   p.rows_per_unit = pl.rows_per_unit;
+  p.unit_tokens = pl.pub.kernel == 8 ? 0 : pl.rows_per_unit / p.G;
   p.chunk_tiles = pl.pub.chunk / kPromptTile;
   p.splits = pl.pub.num_splits;
   p.rows = rows;

@@ -58,7 +58,8 @@ constexpr uint64_t kWaitNs = 1000000000ull;
 constexpr int B_FULL = 0, B_EMPTY = NS, B_S = 2 * NS, B_P = B_S + 1, B_OFULL = B_P + 1, B_OEMPTY = B_OFULL + 1,
               B_XCH = B_OEMPTY + 1, B_FIN = B_XCH + 8, NBARS = B_FIN + 1;
 constexpr uint32_t kXchOfs = 512;               // [2 parity][2 half][128 rows] floats
-static_assert(kXchOfs + 2048 <= kHeader && NBARS * 8 + 16 <= kXchOfs, "header");
+constexpr uint32_t kUnitOfs = kXchOfs + 2048;
+static_assert(kUnitOfs + sizeof(PromptUnit) <= kHeader && NBARS * 8 + 16 <= kXchOfs, "header");
 
 // tensor memory: large products of S (then parts 1 and 2 of P), small products
 // of S (then part 3 of P), P V of a tile
@@ -197,7 +198,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_f32_kernel(const __grid_co
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem_raw);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem_raw + NBARS * 8);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  volatile int* s_unit = reinterpret_cast<volatile int*>(tmem_slot + 2);   // sequence (-1: none), unit
+  PromptUnit& s_unit = *reinterpret_cast<PromptUnit*>(smem_raw + kUnitOfs);
   float* xch = reinterpret_cast<float*>(smem_raw + kXchOfs);
   uint8_t* ring = smem_raw + kHeader;
   auto bar = [&](int i) { return smem_u32(&bars[i]); };
@@ -240,31 +241,17 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_f32_kernel(const __grid_co
   const int vq = rest % (D / DV);                   // which 128 columns of V
   rest /= D / DV;
   const int g = rest % p.Hkv;
-  if (warp == 0) {
-    int ub = -1, ui = 0;
-    if (!find_unit(p, rest / p.Hkv, &ub, &ui)) ub = -1;
-    if (lane == 0) {
-      s_unit[0] = ub;
-      s_unit[1] = ui;
-    }
-  }
+  if (warp == 0) find_unit(p, rest / p.Hkv, &s_unit);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
 
   // the unit's rows and tiles (the same in every thread)
-  const int b = s_unit[0];
-  int64_t o0 = 0, n = 0, P = 0;
-  if (b >= 0) {
-    prompt_rows(p.row_offsets, b, p.rows, p.max_rows, p.status, &o0, &n);
-    const int64_t Praw = p.prefix_len[b];
-    P = clamp_prefix(Praw, p.max_prefix, p.capacity);
-    if (P != Praw && tid == 0) set_status(p.status, TV_DEV_BAD_PREFIX);
-  }
-  const int G = p.G;
+  const int b = s_unit.b, G = p.G;
+  const int64_t o0 = s_unit.o0, n = s_unit.n, P = s_unit.P;
   const int64_t nrows = n * G;
-  const int64_t m0 = (int64_t)s_unit[1] * BM;
+  const int64_t m0 = (int64_t)s_unit.i * BM;
   const int64_t last = min(nrows, m0 + BM) - 1;
   const int Pt = (int)((P + BN - 1) / BN);
   const int t_begin = s * p.chunk_tiles;
@@ -278,7 +265,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_f32_kernel(const __grid_co
     if (lane == 0) {
       const Blocks blocks(p.max_prefix, p.rows, p.B, G);
       const uint8_t* split = reinterpret_cast<const uint8_t*>(p.split);
-      const int64_t unit = blocks.unit(b, o0, G) + s_unit[1];
+      const int64_t unit = blocks.unit(b, o0, G) + s_unit.i;
       constexpr int PER = 2 * KC + DV / CH;         // slots of a tile
       int u = 0;
       bool ok = true;

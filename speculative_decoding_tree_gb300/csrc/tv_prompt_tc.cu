@@ -36,7 +36,7 @@ constexpr int BN = kPromptTile;                 // keys of a tile
 constexpr uint32_t BOX_BYTES = BN * 128;        // 128 rows x 64 bf16
 constexpr uint32_t SLOT_BYTES = 2 * BOX_BYTES;
 constexpr int NS = 5;                           // ring slots
-constexpr uint32_t kHeader = 3072;
+constexpr uint32_t kHeader = 3072, kUnitOfs = 1024;
 constexpr uint32_t Q_BYTES = 2 * BM * D * 2;
 constexpr uint32_t SMEM = kHeader + Q_BYTES + NS * SLOT_BYTES;
 static_assert(SMEM <= 232448, "shared memory over the 227 KB per-block limit");
@@ -56,7 +56,7 @@ prompt_tc_kernel(const __grid_constant__ PromptParams p, const __grid_constant__
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem_raw);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem_raw + NBARS * 8);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  volatile int* s_unit = reinterpret_cast<volatile int*>(tmem_slot + 2);   // sequence (-1: none), unit
+  PromptUnit& s_unit = *reinterpret_cast<PromptUnit*>(smem_raw + kUnitOfs);
   uint8_t* sQ = smem_raw + kHeader;
   uint8_t* ring = sQ + Q_BYTES;
   auto bar = [&](int i) { return smem_u32(&bars[i]); };
@@ -115,39 +115,23 @@ prompt_tc_kernel(const __grid_constant__ PromptParams p, const __grid_constant__
   const int s = blockIdx.x % p.splits;
   const int rest = blockIdx.x / p.splits;
   const int g = rest % p.Hkv;
-  if (warp == 0) {
-    int ub = -1, ui = 0;
-    if (!find_unit(p, rest / p.Hkv, &ub, &ui)) ub = -1;
-    if (lane == 0) {
-      s_unit[0] = ub;
-      s_unit[1] = ui;
-    }
-  }
+  if (warp == 0) find_unit(p, rest / p.Hkv, &s_unit);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
 
   // the unit's rows and tiles (the same in every thread)
-  const int b = s_unit[0];
-  int64_t o0 = 0, n = 0, P = 0;
-  if (b >= 0) {
-    prompt_rows(p.row_offsets, b, p.rows, p.max_rows, p.status, &o0, &n);
-    const int64_t Praw = p.prefix_len[b];
-    P = clamp_prefix(Praw, p.max_prefix, p.capacity);
-    if (P != Praw && tid == 0) set_status(p.status, TV_DEV_BAD_PREFIX);
-  }
-  const int G = p.G;
-  const int64_t nrows = n * G;
-  const int64_t m0 = (int64_t)s_unit[1] * p.rows_per_unit;
+  const int b = s_unit.b, G = p.G, o0 = s_unit.o0, n = s_unit.n;
+  const int64_t P = s_unit.P;
+  const int tile_tokens = p.unit_tokens >> 1, tok0 = s_unit.i * p.unit_tokens;   // first token of the unit
   const int Pt = (int)((P + BN - 1) / BN);
   const int t_begin = s * p.chunk_tiles;
   int Tw[2];
 #pragma unroll
   for (int w = 0; w < 2; ++w) {
-    const int64_t first = m0 + w * p.rows_per_tile;
-    const int64_t last = min(nrows, first + p.rows_per_tile) - 1;
-    const int all = first < nrows ? Pt + (int)(last / G / BN) + 1 : 0;
+    const int first = tok0 + w * tile_tokens;
+    const int all = first < n ? Pt + (min(n, first + tile_tokens) - 1) / BN + 1 : 0;
     Tw[w] = max(0, min(all - t_begin, p.chunk_tiles));
   }
   const int T = max(Tw[0], Tw[1]);
@@ -163,7 +147,7 @@ prompt_tc_kernel(const __grid_constant__ PromptParams p, const __grid_constant__
         if (Tw[w] > 0)
           for (int kb = 0; kb < 2; ++kb)
             tma_load_3d(smem_u32(sQ + (2 * w + kb) * (BM * 128)), &tm_q, Q_FULL, kb * 64, g * G,
-                        (int)(o0 + (m0 + w * p.rows_per_tile) / G));
+                        o0 + tok0 + w * tile_tokens);
     }
     const int oob_row = p.paged ? (int)(p.num_pages * p.Hkv * kPageSize) : 0;
     auto page_pos = [&](int t) -> int64_t {         // first position of this lane's page of tile t, or -1 (none)
@@ -189,7 +173,7 @@ prompt_tc_kernel(const __grid_constant__ PromptParams p, const __grid_constant__
       const int tt = t_begin + t;
       const bool own = tt >= Pt;
       const int64_t first = own ? (int64_t)(tt - Pt) * BN : (int64_t)tt * BN;
-      const int valid = (int)min((int64_t)BN, (own ? n : P) - first);   // keys of the tile that exist
+      const int valid = (int)min((int64_t)BN, (own ? (int64_t)n : P) - first);   // keys of the tile that exist
       const int my_row = page_row(t, pid_a);
       pid_a = pid_b;
       pid_b = page_id(t + 2);
@@ -247,15 +231,17 @@ prompt_tc_kernel(const __grid_constant__ PromptParams p, const __grid_constant__
     if (lane == 0) {
       constexpr uint32_t ID_QK = idesc_bf16_f32(BM, BN, 0, 0);
       constexpr uint32_t ID_PV = idesc_bf16_f32(BM, D, 0, 1);
-      const uint32_t q_addr = smem_u32(sQ), ring_addr = smem_u32(ring);
+      constexpr uint32_t HI = desc_hi(1024, 2);
+      const uint32_t q_lo = desc_lo(smem_u32(sQ), 16), k_lo = desc_lo(smem_u32(ring), 16),
+                     v_lo = desc_lo(smem_u32(ring), BOX_BYTES);
       auto qk = [&](int w, int slot) {
-        const uint32_t kaddr = ring_addr + slot * SLOT_BYTES;
+        const uint32_t a = q_lo + w * (2 * BM * 128 / 16), bd = k_lo + slot * (SLOT_BYTES / 16);
+        const uint32_t to = tmem + (uint32_t)(w * 128);
+        mma_ss_lo<false>(to, a, bd, HI, ID_QK);
 #pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk) {
-          const uint64_t a = smem_desc(q_addr + (2 * w + (kk >> 2)) * (BM * 128) + (kk & 3) * 32, 16, 1024, 2);
-          const uint64_t bd = smem_desc(kaddr + (kk >> 2) * BOX_BYTES + (kk & 3) * 32, 16, 1024, 2);
-          mma_ss(tmem + (uint32_t)(w * 128), a, bd, ID_QK, kk > 0 ? 1u : 0u);
-        }
+        for (int kk = 1; kk < D / 16; ++kk)
+          mma_ss_lo<true>(to, a + (kk >> 2) * (BM * 128 / 16) + (kk & 3) * 2, bd + (kk >> 2) * (BOX_BYTES / 16) + (kk & 3) * 2,
+                          HI, ID_QK);
         mma_commit(S_FULL(w));
       };
       bool ok = mbar_wait(Q_FULL, 0, abort_flag, kWaitNs) && mbar_wait(FULL(0), 0, abort_flag, kWaitNs);
@@ -271,19 +257,20 @@ prompt_tc_kernel(const __grid_constant__ PromptParams p, const __grid_constant__
         if (!mbar_wait(FULL(vs), (jv / NS) & 1, abort_flag, kWaitNs)) break;
         if (t + 1 < T && !mbar_wait(FULL(ks), (jk / NS) & 1, abort_flag, kWaitNs)) break;
         tc_fence_after();
-        const uint32_t vaddr = ring_addr + vs * SLOT_BYTES;
+        const uint32_t bd = v_lo + vs * (SLOT_BYTES / 16);
 #pragma unroll
         for (int w = 0; w < 2; ++w) {
           if (t < Tw[w]) {
-            for (int h = 0; h < 2 && ok; ++h) {
+            const uint32_t to = tmem + 256 + (uint32_t)(w * D), pa = tmem + (uint32_t)(w * 128);
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
               if (!mbar_wait(P_FULL(w, h), t & 1, abort_flag, kWaitNs)) { ok = false; break; }
               tc_fence_after();
 #pragma unroll
               for (int kq = 0; kq < BN / 32; ++kq) {
                 const int kk = h * (BN / 32) + kq;
-                const uint64_t bd = smem_desc(vaddr + kk * (16 * 128), BOX_BYTES, 1024, 2);
-                mma_ts(tmem + 256 + (uint32_t)(w * D), tmem + (uint32_t)(w * 128) + kk * 8, bd, ID_PV,
-                       (t > 0 || kk > 0) ? 1u : 0u);
+                if (kk == 0 && t == 0) mma_ts_lo<false>(to, pa, bd, HI, ID_PV);
+                else mma_ts_lo<true>(to, pa + kk * 8, bd + kk * (16 * 128 / 16), HI, ID_PV);
               }
             }
             if (!ok) break;
@@ -309,9 +296,8 @@ prompt_tc_kernel(const __grid_constant__ PromptParams p, const __grid_constant__
     const uint32_t sbuf = tmem + lane_base + (uint32_t)(w * 128);
     const uint32_t obuf = tmem + lane_base + 256 + (uint32_t)(w * D);
     const float c2 = p.scale_log2;
-    const int64_t m = m0 + w * p.rows_per_tile + r;
-    const bool row_ok = r < p.rows_per_tile && m < nrows;
-    const int token = row_ok ? (int)(m / G) : 0;    // the row's place in its sequence
+    const int token = tok0 + w * tile_tokens + r / G;   // the row's place in its sequence
+    const bool row_ok = r < p.rows_per_tile && token < n;
     const bool warp_live = __any_sync(kAll, row_ok);
     float m_ref = -INFINITY, l = 0.f;
     bool ok = true;
@@ -391,31 +377,65 @@ prompt_tc_kernel(const __grid_constant__ PromptParams p, const __grid_constant__
     if (ok && myT > 0) {
       tc_fence_after();
       const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
+      // Rows go out through the query tile's shared memory, which no product reads any more: a thread stages its row
+      // 16 bytes at a time (piece c at c ^ (row & 7)), then 16 lanes store a row of 256 bytes together.  (Each thread
+      // storing its own row took 3 us of a CTA.)
+      uint8_t* stage = sQ + w * 2 * (BM * 128) + (warp & 3) * (32 * 256);
       const int my_s = (Pt + token / BN) / p.chunk_tiles;     // the row's last split
-      const bool split = my_s > 0, write = row_ok && s <= my_s;
-      const int h = row_ok ? g * G + (int)(m % G) : 0;
-      const int64_t at = split ? prompt_slot(o0 + token, h, s, p.Hq, p.splits) : (o0 + token) * p.Hq + h;
-#pragma unroll 1
-      for (int c = 0; c < D; c += 32) {
-        uint32_t rr[32];
-        tmem_ld_x32(obuf + c, rr);
-        if (!write) continue;
-        float v[32];
+      const bool wide = !p.out_bf16 || my_s > 0;    // fp32: partials, or the output's type
+      const int64_t slot = my_s > 0 ? prompt_slot(o0 + token, g * G + r % G, s, p.Hq, p.splits)
+                                    : (int64_t)(o0 + token) * p.Hq + g * G + r % G;
+      const bool write = row_ok && s <= my_s;
+      // (bf16 rows and fp32 ones may meet in a warp: both forms run where both occur)
+      const unsigned any_wide = __ballot_sync(kAll, write && wide), any_slim = __ballot_sync(kAll, write && !wide);
+      auto flush = [&](unsigned rows, char* base, int64_t row_bytes, int col_bytes) {
+        __syncwarp();
+#pragma unroll 4
+        for (int i = 0; i < 16; ++i) {
+          const int rr = 2 * i + (lane >> 4), c = lane & 15;
+          const int64_t at = __shfl_sync(kAll, slot, rr);
+          const uint4 v = *reinterpret_cast<const uint4*>(stage + rr * 256 + ((c ^ (rr & 7)) << 4));
+          if (rows >> rr & 1u) *reinterpret_cast<uint4*>(base + at * row_bytes + col_bytes + c * 16) = v;
+        }
+        __syncwarp();
+      };
+      if (any_slim) {
 #pragma unroll
-        for (int e = 0; e < 32; ++e) v[e] = __uint_as_float(rr[e]) * inv;
-        if (!split && p.out_bf16) {
-          uint4* dst = reinterpret_cast<uint4*>(reinterpret_cast<__nv_bfloat16*>(p.out) + at * D + c);
+        for (int c = 0; c < D; c += 32) {
+          uint32_t rr[32];
+          tmem_ld_x32(obuf + c, rr);
 #pragma unroll
-          for (int e = 0; e < 4; ++e)
-            dst[e] = make_uint4(pack_bf16(v[8 * e], v[8 * e + 1]), pack_bf16(v[8 * e + 2], v[8 * e + 3]),
-                                pack_bf16(v[8 * e + 4], v[8 * e + 5]), pack_bf16(v[8 * e + 6], v[8 * e + 7]));
-        } else {
-          float4* dst = reinterpret_cast<float4*>((split ? p.o_part : reinterpret_cast<float*>(p.out)) + at * D + c);
+          for (int e = 0; e < 4; ++e) {
+            uint4 v;
+            uint32_t* vw = &v.x;
 #pragma unroll
-          for (int e = 0; e < 8; ++e) dst[e] = make_float4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
+            for (int q = 0; q < 4; ++q)
+              vw[q] = pack_bf16(__uint_as_float(rr[8 * e + 2 * q]) * inv, __uint_as_float(rr[8 * e + 2 * q + 1]) * inv);
+            *reinterpret_cast<uint4*>(stage + lane * 256 + (((c / 8 + e) ^ (lane & 7)) << 4)) = v;
+          }
+        }
+        flush(any_slim, reinterpret_cast<char*>(p.out), D * 2, 0);
+      }
+      if (any_wide) {
+#pragma unroll
+        for (int hf = 0; hf < 2; ++hf) {            // 64 columns at a time
+#pragma unroll
+          for (int c = 0; c < 64; c += 32) {
+            uint32_t rr[32];
+            tmem_ld_x32(obuf + hf * 64 + c, rr);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              const float4 v = make_float4(__uint_as_float(rr[4 * e]) * inv, __uint_as_float(rr[4 * e + 1]) * inv,
+                                           __uint_as_float(rr[4 * e + 2]) * inv, __uint_as_float(rr[4 * e + 3]) * inv);
+              *reinterpret_cast<float4*>(stage + lane * 256 + (((c / 4 + e) ^ (lane & 7)) << 4)) = v;
+            }
+          }
+          const unsigned parts = __ballot_sync(kAll, write && my_s > 0);
+          if (parts) flush(parts, reinterpret_cast<char*>(p.o_part), D * 4, hf * 256);
+          if (any_wide & ~parts) flush(any_wide & ~parts, reinterpret_cast<char*>(p.out), D * 4, hf * 256);
         }
       }
-      if (write && split) p.ml_part[at] = make_float2(m_ref, l);
+      if (write && my_s > 0) p.ml_part[slot] = make_float2(m_ref, l);
     }
   }
 

@@ -35,7 +35,7 @@ constexpr int BN = kPromptTile;                 // keys of a tile
 constexpr int KH = BN / 2;                      // keys of a K tile per CTA
 constexpr int DV = 256;                         // value columns per unit
 constexpr uint32_t SLOT = 32768;                // 64 keys x 256 channels of K, or 128 keys x 128 columns of V
-constexpr uint32_t kHeader = 3072;
+constexpr uint32_t kHeader = 3072, kUnitOfs = 1024;
 constexpr int kThreads = 192;
 constexpr uint64_t kWaitNs = 1000000000ull;
 constexpr float kRescaleThreshold = 8.0f;       // rescale O when the maximum grows by more than 2^8
@@ -63,7 +63,7 @@ prompt_tc2_kernel(const __grid_constant__ PromptParams p, const __grid_constant_
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem_raw);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem_raw + C::NBARS * 8);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  volatile int* s_unit = reinterpret_cast<volatile int*>(tmem_slot + 2);   // sequence (-1: none), unit
+  PromptUnit& s_unit = *reinterpret_cast<PromptUnit*>(smem_raw + kUnitOfs);
   uint8_t* sQ = smem_raw + kHeader;
   uint8_t* ring = sQ + C::Q_BYTES;
   auto bar = [&](int i) { return smem_u32(&bars[i]); };
@@ -126,14 +126,7 @@ prompt_tc2_kernel(const __grid_constant__ PromptParams p, const __grid_constant_
   const int vh = rest % (D / DV);                   // which 256 columns of V
   rest /= D / DV;
   const int g = rest % p.Hkv;
-  if (warp == 0) {
-    int ub = -1, ui = 0;
-    if (!find_unit(p, rest / p.Hkv, &ub, &ui)) ub = -1;
-    if (lane == 0) {
-      s_unit[0] = ub;
-      s_unit[1] = ui;
-    }
-  }
+  if (warp == 0) find_unit(p, rest / p.Hkv, &s_unit);
   tc_fence_before();
   __syncthreads();
   cluster_sync_all();                               // both CTAs' barriers exist before any remote use
@@ -141,36 +134,27 @@ prompt_tc2_kernel(const __grid_constant__ PromptParams p, const __grid_constant_
   const uint32_t tmem = *tmem_slot;
 
   // the pair's rows and tiles (the same in every thread of both CTAs)
-  const int b = s_unit[0];
-  int64_t o0 = 0, n = 0, P = 0;
-  if (b >= 0) {
-    prompt_rows(p.row_offsets, b, p.rows, p.max_rows, p.status, &o0, &n);
-    const int64_t Praw = p.prefix_len[b];
-    P = clamp_prefix(Praw, p.max_prefix, p.capacity);
-    if (P != Praw && tid == 0) set_status(p.status, TV_DEV_BAD_PREFIX);
-  }
-  const int G = p.G;
-  const int64_t nrows = n * G;
-  const int64_t pair0 = (int64_t)s_unit[1] * p.rows_per_unit;
-  const int64_t m0 = pair0 + rank * p.rows_per_tile;
+  const int b = s_unit.b, G = p.G, o0 = s_unit.o0, n = s_unit.n;
+  const int64_t P = s_unit.P;
+  const int tile_tokens = p.unit_tokens >> 1;
+  const int pair0 = s_unit.i * p.unit_tokens, tok0 = pair0 + (int)rank * tile_tokens;   // first token of the pair, of the CTA
   const int Pt = (int)((P + BN - 1) / BN);
   const int t_begin = s * p.chunk_tiles;
-  const int64_t last = min(nrows, pair0 + p.rows_per_unit) - 1;
-  const int all = pair0 < nrows ? Pt + (int)(last / G / BN) + 1 : 0;
+  const int all = pair0 < n ? Pt + (min(n, pair0 + p.unit_tokens) - 1) / BN + 1 : 0;
   const int T = max(0, min(all - t_begin, p.chunk_tiles));
 
   if (T == 0) {
     // nothing for this pair
   } else if (warp == 4) {
     // ============================================================ producer
-    const bool leader = rank == 0, rows_here = m0 < nrows;
+    const bool leader = rank == 0, rows_here = tok0 < n;
     if (lane == 0) {
       const uint32_t qf = map_to_cta(Q_FULL, 0);
       const uint32_t bytes = (uint32_t)p.rows_per_tile * 128u * (D / 64);
-      if (leader) mbar_expect_tx(Q_FULL, bytes * (1 + (pair0 + p.rows_per_tile < nrows)));
+      if (leader) mbar_expect_tx(Q_FULL, bytes * (1 + (pair0 + tile_tokens < n)));
       if (rows_here)
         for (int kb = 0; kb < D / 64; ++kb)
-          tma2_load_3d(smem_u32(sQ + kb * (BM * 128)), &tm_q, qf, kb * 64, g * G, (int)(o0 + m0 / G));
+          tma2_load_3d(smem_u32(sQ + kb * (BM * 128)), &tm_q, qf, kb * 64, g * G, o0 + tok0);
       if (!leader) mbar_arrive_cluster_relaxed(qf);
     }
     const int oob_row = p.paged ? (int)(p.num_pages * p.Hkv * kPageSize) : 0;
@@ -209,7 +193,7 @@ prompt_tc2_kernel(const __grid_constant__ PromptParams p, const __grid_constant_
         const int tt = t_begin + tile;
         const bool own = tt >= Pt;
         const int64_t first = own ? (int64_t)(tt - Pt) * BN : (int64_t)tt * BN;
-        const int valid = (int)min((int64_t)BN, (own ? n : P) - first);   // keys of the tile that exist
+        const int valid = (int)min((int64_t)BN, (own ? (int64_t)n : P) - first);   // keys of the tile that exist
         const bool fix = isv && valid < BN;         // V rows past the end become zeros: their weights are
         const int slot = j % NS, use = j / NS;
         if (use > 0 && !__all_sync(kAll, mbar_wait(EMPTY(slot), (use - 1) & 1, abort_flag, kWaitNs))) {
@@ -345,9 +329,8 @@ prompt_tc2_kernel(const __grid_constant__ PromptParams p, const __grid_constant_
     const uint32_t lane_base = (uint32_t)(warp * 32) << 16;
     const uint32_t obuf = tmem + lane_base + 256;
     const float c2 = p.scale_log2;
-    const int64_t m = m0 + r;
-    const bool row_ok = r < p.rows_per_tile && m < nrows;
-    const int token = row_ok ? (int)(m / G) : 0;    // the row's place in its sequence
+    const int token = tok0 + r / G;                 // the row's place in its sequence
+    const bool row_ok = r < p.rows_per_tile && token < n;
     const bool warp_live = __any_sync(kAll, row_ok);
     float m_ref = -INFINITY, l = 0.f;
     bool ok = true;
@@ -435,8 +418,8 @@ prompt_tc2_kernel(const __grid_constant__ PromptParams p, const __grid_constant_
       const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
       const int my_s = (Pt + token / BN) / p.chunk_tiles;     // the row's last split
       const bool split = my_s > 0, write = row_ok && s <= my_s;
-      const int h = row_ok ? g * G + (int)(m % G) : 0;
-      const int64_t at = split ? prompt_slot(o0 + token, h, s, p.Hq, p.splits) : (o0 + token) * p.Hq + h;
+      const int h = g * G + r % G;
+      const int64_t at = split ? prompt_slot(o0 + token, h, s, p.Hq, p.splits) : (int64_t)(o0 + token) * p.Hq + h;
 #pragma unroll 1
       for (int c = 0; c < DV; c += 32) {
         uint32_t rr[32];
