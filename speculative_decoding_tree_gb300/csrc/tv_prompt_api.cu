@@ -47,7 +47,7 @@ int make_prompt_plan(const tv_desc* d, int64_t rows, int64_t max_rows, PromptPla
   // one, in chunks of four tiles or more; kernel 8, whose tiles take longer,
   // into about two waves of chunks of any length (2000 fp32 rows x 4 heads at
   // head_dim 256: 175, 108, 144 and 129 us with 1, 2, 3 and 4).
-  const int64_t ctas = p->units * d->num_kv_heads * (p->pub.kernel >= 7 ? d->head_dim / 128 : 1), sms = num_sms();
+  const int64_t ctas = p->units * d->num_kv_heads * (p->pub.kernel == 6 ? 1 : d->head_dim / 128), sms = num_sms();
   int64_t want = ctas > 0 ? (parts ? 2 * sms : sms) / ctas : 1;
   if (!parts && want > tiles / 4) want = tiles / 4;
   if (want > tiles) want = tiles;
@@ -154,7 +154,7 @@ int tv_prompt_attn(const tv_desc* desc, int64_t rows, int64_t max_rows, const vo
   p.scale_log2 = scale * 1.4426950408889634f;
   const cudaStream_t s = as_stream(stream);
   cudaError_t e = pl.pub.kernel == 8   ? launch_prompt_f32(p, desc->dtype, pl.units, s)
-                  : pl.pub.kernel == 7   ? launch_prompt_tc2(p, pl.units, s)
+                  : pl.pub.kernel == 7 ? launch_prompt_tc2(p, pl.units, s)
                                        : launch_prompt_tc(p, pl.units, s);
   if (e == cudaSuccess && split) e = launch_prompt_merge(p, s);
   return e == cudaSuccess ? TV_OK : TV_ERR_CUDA;

@@ -29,7 +29,7 @@
 //              scores and 64 columns of O; the pair exchanges its maxima
 //   warp 8     lane 0 copies: per key tile Q and K of each 64 channels (Q's
 //              parts do not all fit), then two blocks of V
-//   warp 9     owns tensor memory; lane 0 issues the products
+//   warp 9     owns tensor memory; one lane's instructions are the products
 // Every wait is bounded.
 #include <cuda.h>
 
@@ -287,69 +287,97 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_f32_kernel(const __grid_co
       for (int j = (u > NS ? u - NS : 0); j < u; ++j) mbar_wait(FULL(j % NS), (j / NS) & 1, &spare, kWaitNs);
     }
   } else if (warp == 9) {
-    // ============================================================ MMA issuer
-    if (lane == 0) {
-      constexpr uint32_t ID_QK = idesc_bf16_f32(BM, BN, 0, 0);
-      constexpr uint32_t ID_PV = idesc_bf16_f32(BM, CH, 0, 1);
-      const uint32_t ring_addr = smem_u32(ring);
-      int u = 0;
-      bool ok = true;
-      for (int t = 0; t < T && ok; ++t) {
-        for (int c = 0; c < KC && ok; ++c, u += 2) {
-          const int qs = u % NS, ks = (u + 1) % NS;
-          if (!mbar_wait(FULL(qs), (u / NS) & 1, abort_flag, kWaitNs) ||
-              !mbar_wait(FULL(ks), ((u + 1) / NS) & 1, abort_flag, kWaitNs)) {
-            ok = false;
-            break;
-          }
-          tc_fence_after();
-          auto product = [&](int a, int bp, uint32_t to, bool first) {
+    // ============================================================ MMA issuer (the whole warp, one lane's instructions)
+    constexpr uint32_t ID_QK = idesc_bf16_f32(BM, BN, 0, 0);
+    constexpr uint32_t ID_PV = idesc_bf16_f32(BM, CH, 0, 1);
+    constexpr uint32_t HI = desc_hi(1024, 2), P16 = PART / 16;
+    const uint32_t ring_lo = desc_lo(smem_u32(ring), 16), v_lo = desc_lo(smem_u32(ring), PART);
+    const uint32_t tm = __shfl_sync(kAll, tmem, 0);
+    const int nt = __shfl_sync(kAll, T, 0);
+    const bool one = elect_one();
+    auto wait = [&](uint32_t bar, uint32_t parity) {
+      return __all_sync(kAll, mbar_wait(bar, parity, abort_flag, kWaitNs)) != 0;
+    };
+    int slot = 0, phase = 0;
+    auto next = [&] {
+      if (++slot == NS) {
+        slot = 0;
+        phase ^= 1;
+      }
+    };
+    bool ok = true;
+    for (int t = 0; t < nt && ok; ++t) {
+      for (int c = 0; c < KC && ok; ++c) {
+        const int qs = slot;
+        ok = wait(FULL(qs), phase);
+        if (!ok) break;
+        next();
+        const int ks = slot;
+        ok = wait(FULL(ks), phase);
+        if (!ok) break;
+        next();
+        tc_fence_after();
+        const uint32_t q = ring_lo + qs * (SLOT / 16), k = ring_lo + ks * (SLOT / 16);
+        if (one) {
+          // parts a of Q and b of K, 16 channels a step
+          auto product = [&](uint32_t a, uint32_t b, uint32_t to) {
 #pragma unroll
-            for (int kk = 0; kk < CH / 16; ++kk)
-              mma_ss(tmem + to, smem_desc(ring_addr + qs * SLOT + a * PART + kk * 32, 16, 1024, 2),
-                     smem_desc(ring_addr + ks * SLOT + bp * PART + kk * 32, 16, 1024, 2), ID_QK,
-                     first && kk == 0 ? 0u : 1u);
+            for (int kk = 0; kk < CH / 16; ++kk) mma_ss_lo<true>(tm + to, a + kk * 2, b + kk * 2, HI, ID_QK);
           };
-          product(0, 2, T_SMALL, c == 0);
-          product(2, 0, T_SMALL, false);
-          product(1, 1, T_SMALL, false);
-          product(0, 1, T_SMALL, false);
-          product(1, 0, T_SMALL, false);
-          product(0, 0, T_BIG, c == 0);
+          if (c == 0) {
+            mma_ss_lo<false>(tm + T_SMALL, q, k + 2 * P16, HI, ID_QK);
+            mma_ss_lo<false>(tm + T_BIG, q, k, HI, ID_QK);
+          } else {
+            mma_ss_lo<true>(tm + T_SMALL, q, k + 2 * P16, HI, ID_QK);
+            mma_ss_lo<true>(tm + T_BIG, q, k, HI, ID_QK);
+          }
+#pragma unroll
+          for (int kk = 1; kk < CH / 16; ++kk) {
+            mma_ss_lo<true>(tm + T_SMALL, q + kk * 2, k + 2 * P16 + kk * 2, HI, ID_QK);
+            mma_ss_lo<true>(tm + T_BIG, q + kk * 2, k + kk * 2, HI, ID_QK);
+          }
+          product(q + 2 * P16, k, T_SMALL);
+          product(q + P16, k + P16, T_SMALL);
+          product(q, k + P16, T_SMALL);
+          product(q + P16, k, T_SMALL);
           mma_commit(EMPTY(qs));
           mma_commit(EMPTY(ks));
         }
+      }
+      if (!ok) break;
+      if (one) mma_commit(S_FULL);
+      ok = wait(P_FULL, t & 1) && (t == 0 || wait(O_EMPTY, (t - 1) & 1));
+      if (!ok) break;
+      for (int v = 0; v < DV / CH; ++v) {
+        ok = wait(FULL(slot), phase);
         if (!ok) break;
-        mma_commit(S_FULL);
-        if (!mbar_wait(P_FULL, t & 1, abort_flag, kWaitNs)) break;
-        if (t > 0 && !mbar_wait(O_EMPTY, (t - 1) & 1, abort_flag, kWaitNs)) break;
-        for (int v = 0; v < DV / CH; ++v, ++u) {
-          const int vs = u % NS;
-          if (!mbar_wait(FULL(vs), (u / NS) & 1, abort_flag, kWaitNs)) { ok = false; break; }
-          tc_fence_after();
-          auto product = [&](int a, int bp, bool first) {
-            const uint32_t pa = tmem + (a == 0 ? T_BIG : a == 1 ? T_BIG + 64 : T_SMALL);
+        tc_fence_after();
+        const uint32_t b = v_lo + slot * (SLOT / 16), to = tm + T_O + v * CH;
+        if (one) {
+          auto product = [&](uint32_t pa, uint32_t part, bool rest) {
 #pragma unroll
             for (int kk = 0; kk < BN / 16; ++kk)
-              mma_ts(tmem + T_O + v * CH, pa + kk * 8, smem_desc(ring_addr + vs * SLOT + bp * PART + kk * (16 * 128), PART, 1024, 2),
-                     ID_PV, first && kk == 0 ? 0u : 1u);
+              if (rest || kk > 0) mma_ts_lo<true>(to, tm + pa + kk * 8, part + kk * (16 * 128 / 16), HI, ID_PV);
           };
-          product(0, 2, true);
-          product(2, 0, false);
-          product(1, 1, false);
-          product(0, 1, false);
-          product(1, 0, false);
-          product(0, 0, false);
-          mma_commit(EMPTY(vs));
+          mma_ts_lo<false>(to, tm + T_BIG, b + 2 * P16, HI, ID_PV);
+          product(T_BIG, b + 2 * P16, false);
+          product(T_SMALL, b, true);
+          product(T_BIG + 64, b + P16, true);
+          product(T_BIG, b + P16, true);
+          product(T_BIG + 64, b, true);
+          product(T_BIG, b, true);
+          mma_commit(EMPTY(slot));
         }
-        if (!ok) break;
-        mma_commit(O_FULL);
+        next();
       }
-      // every product this thread issued has finished before tensor memory is freed
-      mma_commit(FIN);
-      int spare = 0;                                // (not abort_flag: this wait also follows a timeout)
-      mbar_wait(FIN, 0, &spare, kWaitNs);
+      if (!ok) break;
+      if (one) mma_commit(O_FULL);
     }
+    // every product issued has finished before tensor memory is freed
+    if (one) mma_commit(FIN);
+    int spare = 0;                                  // (not abort_flag: this wait also follows a timeout)
+    mbar_wait(FIN, 0, &spare, kWaitNs);
+    __syncwarp();
   } else {
     // ============================================================ softmax and epilogue
     const int half = warp >> 2;                     // keys 64 half .. of a tile, columns 64 half .. of O

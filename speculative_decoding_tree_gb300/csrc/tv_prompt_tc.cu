@@ -15,7 +15,10 @@
 //   warps 0-3, 4-7  softmax and epilogue of tile 0 and 1
 //   warp 8          TMA producer: Q, then K(0), V(0), K(1), V(1), ... in 32 KB
 //                   slots (a paged cache in boxes of 16 rows)
-//   warp 9          owns tensor memory; lane 0 issues the products
+//   warp 9          owns tensor memory; the warp runs the issue loop together and
+//                   one lane's instructions are the products: operands then
+//                   stay in uniform registers (a lane alone: 1.63 ms where this
+//                   takes 1.31 for 16384 rows x 32 heads)
 // Every wait is bounded (1 s); on a timeout the CTA raises TV_DEV_TIMEOUT and
 // every role leaves its loop.
 #include <cuda.h>
@@ -227,45 +230,59 @@ prompt_tc_kernel(const __grid_constant__ PromptParams p, const __grid_constant__
       for (int jj = (j > NS ? j - NS : 0); jj < j; ++jj) mbar_wait(FULL(jj % NS), (jj / NS) & 1, &spare, kWaitNs);
     }
   } else if (warp == 9) {
-    // ============================================================ MMA issuer
-    if (lane == 0) {
-      constexpr uint32_t ID_QK = idesc_bf16_f32(BM, BN, 0, 0);
-      constexpr uint32_t ID_PV = idesc_bf16_f32(BM, D, 0, 1);
-      constexpr uint32_t HI = desc_hi(1024, 2);
-      const uint32_t q_lo = desc_lo(smem_u32(sQ), 16), k_lo = desc_lo(smem_u32(ring), 16),
-                     v_lo = desc_lo(smem_u32(ring), BOX_BYTES);
-      auto qk = [&](int w, int slot) {
-        const uint32_t a = q_lo + w * (2 * BM * 128 / 16), bd = k_lo + slot * (SLOT_BYTES / 16);
-        const uint32_t to = tmem + (uint32_t)(w * 128);
+    // ============================================================ MMA issuer (the whole warp, one lane's instructions)
+    constexpr uint32_t ID_QK = idesc_bf16_f32(BM, BN, 0, 0);
+    constexpr uint32_t ID_PV = idesc_bf16_f32(BM, D, 0, 1);
+    constexpr uint32_t HI = desc_hi(1024, 2);
+    const uint32_t q_lo = desc_lo(smem_u32(sQ), 16), k_lo = desc_lo(smem_u32(ring), 16),
+                   v_lo = desc_lo(smem_u32(ring), BOX_BYTES);
+    const uint32_t tm = __shfl_sync(kAll, tmem, 0);
+    const int n0 = __shfl_sync(kAll, Tw[0], 0), n1 = __shfl_sync(kAll, Tw[1], 0), nt = max(n0, n1);
+    const bool one = elect_one();
+    auto wait = [&](uint32_t bar, uint32_t parity) {
+      return __all_sync(kAll, mbar_wait(bar, parity, abort_flag, kWaitNs)) != 0;
+    };
+    auto qk = [&](int w, int slot) {
+      const uint32_t a = q_lo + w * (2 * BM * 128 / 16), bd = k_lo + slot * (SLOT_BYTES / 16);
+      const uint32_t to = tm + (uint32_t)(w * 128);
+      if (one) {
         mma_ss_lo<false>(to, a, bd, HI, ID_QK);
 #pragma unroll
         for (int kk = 1; kk < D / 16; ++kk)
           mma_ss_lo<true>(to, a + (kk >> 2) * (BM * 128 / 16) + (kk & 3) * 2, bd + (kk >> 2) * (BOX_BYTES / 16) + (kk & 3) * 2,
                           HI, ID_QK);
         mma_commit(S_FULL(w));
-      };
-      bool ok = mbar_wait(Q_FULL, 0, abort_flag, kWaitNs) && mbar_wait(FULL(0), 0, abort_flag, kWaitNs);
-      tc_fence_after();
-      if (ok) {
-        for (int w = 0; w < 2; ++w)
-          if (Tw[w] > 0) qk(w, 0);
-        mma_commit(EMPTY(0));
       }
-      for (int t = 0; t < T && ok; ++t) {
-        const int jv = 2 * t + 1, jk = 2 * t + 2;   // V(t), K(t + 1)
-        const int vs = jv % NS, ks = jk % NS;
-        if (!mbar_wait(FULL(vs), (jv / NS) & 1, abort_flag, kWaitNs)) break;
-        if (t + 1 < T && !mbar_wait(FULL(ks), (jk / NS) & 1, abort_flag, kWaitNs)) break;
-        tc_fence_after();
-        const uint32_t bd = v_lo + vs * (SLOT_BYTES / 16);
+    };
+    bool ok = wait(Q_FULL, 0) && wait(FULL(0), 0);
+    tc_fence_after();
+    if (ok) {
+      if (n0 > 0) qk(0, 0);
+      if (n1 > 0) qk(1, 0);
+      if (one) mma_commit(EMPTY(0));
+    }
+    int vs = 1, vp = 0;                             // V(t)'s slot and phase; K(t + 1) follows it
+    for (int t = 0; t < nt && ok; ++t) {
+      int ks = vs + 1, kp = vp;
+      if (ks == NS) {
+        ks = 0;
+        kp ^= 1;
+      }
+      ok = wait(FULL(vs), vp) && (t + 1 >= nt || wait(FULL(ks), kp));
+      if (!ok) break;
+      tc_fence_after();
+      const uint32_t bd = v_lo + vs * (SLOT_BYTES / 16);
 #pragma unroll
-        for (int w = 0; w < 2; ++w) {
-          if (t < Tw[w]) {
-            const uint32_t to = tmem + 256 + (uint32_t)(w * D), pa = tmem + (uint32_t)(w * 128);
+      for (int w = 0; w < 2; ++w) {
+        const int nw = w == 0 ? n0 : n1;
+        if (t < nw) {
+          const uint32_t to = tm + 256 + (uint32_t)(w * D), pa = tm + (uint32_t)(w * 128);
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              if (!mbar_wait(P_FULL(w, h), t & 1, abort_flag, kWaitNs)) { ok = false; break; }
-              tc_fence_after();
+          for (int h = 0; h < 2; ++h) {
+            ok = ok && wait(P_FULL(w, h), t & 1);
+            if (!ok) break;
+            tc_fence_after();
+            if (one) {
 #pragma unroll
               for (int kq = 0; kq < BN / 32; ++kq) {
                 const int kk = h * (BN / 32) + kq;
@@ -273,20 +290,27 @@ prompt_tc_kernel(const __grid_constant__ PromptParams p, const __grid_constant__
                 else mma_ts_lo<true>(to, pa + kk * 8, bd + kk * (16 * 128 / 16), HI, ID_PV);
               }
             }
-            if (!ok) break;
-            if (t == Tw[w] - 1) mma_commit(O_DONE(w));
           }
-          if (w == 1) mma_commit(EMPTY(vs));
-          if (t + 1 < Tw[w]) qk(w, ks);
+          if (!ok) break;
+          if (one && t == nw - 1) mma_commit(O_DONE(w));
         }
-        if (!ok) break;
-        if (t + 1 < T) mma_commit(EMPTY(ks));
+        if (one && w == 1) mma_commit(EMPTY(vs));
+        if (t + 1 < nw) qk(w, ks);
       }
-      // every product this thread issued has finished before tensor memory is freed
-      mma_commit(FIN);
-      int spare = 0;                                // (not abort_flag: this wait also follows a timeout)
-      mbar_wait(FIN, 0, &spare, kWaitNs);
+      if (!ok) break;
+      if (one && t + 1 < nt) mma_commit(EMPTY(ks));
+      vs = ks + 1;
+      vp = kp;
+      if (vs == NS) {
+        vs = 0;
+        vp ^= 1;
+      }
     }
+    // every product issued has finished before tensor memory is freed
+    if (one) mma_commit(FIN);
+    int spare = 0;                                  // (not abort_flag: this wait also follows a timeout)
+    mbar_wait(FIN, 0, &spare, kWaitNs);
+    __syncwarp();
   } else if (warp < 8) {
     // ============================================================ softmax and epilogue
     const int w = warp >> 2;

@@ -7,16 +7,22 @@
 // scores).  M = 256 instructions (cta_group::2): each CTA holds its rows, half
 // the keys of a K tile and half the columns of a V tile, so a K/V byte crosses
 // from L2 once for 256 rows and a tile takes half the shared memory.
-//   S(t) = Q K(t)^T in one of two 128-column buffers; the weights P(t) go over
-//   them as bf16; O += P(t) V(t).  S(t + 1) is issued before O += P(t) V(t), so
-//   the softmax of a tile has the time of the products of another: 2048 clocks
-//   at head_dim 256, about twice what one warpgroup a CTA needs (a row a thread).
+//   S(t) = Q K(t)^T goes to one of two 128-column buffers, the weights P(t)
+//   over it as bf16, O += P(t) V(t).  S(t + 1) is issued before O += P(t) V(t).
+//   A tile's softmax takes about 1250 clocks (a thread a row) and 750 more
+//   from its last weights to the next scores where each waits for the other,
+//   its products 2048 at head_dim 256: two warpgroups therefore take the tiles
+//   in turn.  They share a row's reference (the exponent's offset): the group
+//   of tile t hands it on as soon as it knows the tile's maximum, and rescales
+//   O when that lies more than 2^8 above; each keeps its own sum.
+//   200 rows x 16 heads behind 32768 keys, head_dim 256: 90 us (102 with the
+//   products issued by a warp of one lane, 106 with one warpgroup).
 //
-//   warps 0-3  softmax and epilogue of the CTA's rows
-//   warp 4     TMA producer: Q, then K(0), K(1), V(0), K(2), V(1), ... in 32 KB
-//              slots; completion counts on the leader's barriers
-//   warp 5     owns tensor memory; the leader's lane 0 issues the products and
-//              multicasts every commit to both CTAs
+//   warps 0-3, 4-7  softmax of the even and the odd tiles, epilogue
+//   warp 8          TMA producer: Q, then K(0), K(1), V(0), K(2), V(1), ...;
+//                   completion counts on the leader's barriers
+//   warp 9          owns tensor memory; in the leader one lane's instructions
+//                   are the products, every commit is multicast to both CTAs
 // Every wait is bounded; the pair meets before tensor memory is freed.
 #include <cuda.h>
 
@@ -33,22 +39,30 @@ using namespace tc;
 constexpr int BM = 128;                         // query rows per CTA
 constexpr int BN = kPromptTile;                 // keys of a tile
 constexpr int KH = BN / 2;                      // keys of a K tile per CTA
-constexpr int DV = 256;                         // value columns per unit
-constexpr uint32_t SLOT = 32768;                // 64 keys x 256 channels of K, or 128 keys x 128 columns of V
-constexpr uint32_t kHeader = 3072, kUnitOfs = 1024;
-constexpr int kThreads = 192;
+constexpr uint32_t kHeader = 3072, kUnitOfs = 512;
+constexpr uint32_t kRefOfs = 1024;              // [128] floats: a row's reference
+constexpr uint32_t kSumOfs = 1536;              // [2][128] floats: the groups' sums
+static_assert(kSumOfs + 1024 <= kHeader, "header");
+constexpr int kThreads = 320;
 constexpr uint64_t kWaitNs = 1000000000ull;
 constexpr float kRescaleThreshold = 8.0f;       // rescale O when the maximum grows by more than 2^8
 
 template <int D>
 struct Cfg {
+  static constexpr int DV = 256;                // value columns of a unit
+  static constexpr int KC = 256;                // channels of a K slot
+  static constexpr int KS = D / KC;             // slots of a K tile
+  static constexpr uint32_t SLOT = KH * KC * 2; // 64 keys x KC channels of K, or 128 keys x DV / 2 columns of V
+  static constexpr int SB = 2;                  // buffers of S; O follows them in tensor memory
+  static constexpr uint32_t T_O = SB * 128;
+  static constexpr int AHEAD = SB - 1;          // tiles S runs ahead
   static constexpr uint32_t Q_BYTES = BM * D * 2;
   static constexpr int NS = (232448 - kHeader - Q_BYTES) / SLOT;
-  static constexpr int KS = D / 256;            // slots of a K tile
   static constexpr uint32_t SMEM = kHeader + Q_BYTES + NS * SLOT;
-  static constexpr int B_FULL = 0, B_EMPTY = NS, B_Q = 2 * NS, B_S = B_Q + 1, B_P = B_S + 2, B_O = B_P + 4,
-                       B_TAIL = B_O + 2, B_FIN = B_TAIL + 1, NBARS = B_FIN + 1;
+  static constexpr int B_FULL = 0, B_EMPTY = NS, B_Q = 2 * NS, B_S = B_Q + 1, B_P = B_S + SB, B_O = B_P + 2 * SB,
+                       B_REF = B_O + 2, B_SUM = B_REF + 8, B_TAIL = B_SUM + 4, B_FIN = B_TAIL + 1, NBARS = B_FIN + 1;
   static_assert(SMEM <= 232448, "shared memory over the 227 KB per-block limit");
+  static_assert(NBARS * 8 + 16 <= kUnitOfs && T_O + DV <= 512, "header, tensor memory");
 };
 
 template <int D>
@@ -57,13 +71,16 @@ prompt_tc2_kernel(const __grid_constant__ PromptParams p, const __grid_constant_
                   const __grid_constant__ CUtensorMap tm_kc, const __grid_constant__ CUtensorMap tm_vc,
                   const __grid_constant__ CUtensorMap tm_kr, const __grid_constant__ CUtensorMap tm_vr) {
   using C = Cfg<D>;
-  constexpr int NS = C::NS, KS = C::KS;
+  constexpr int NS = C::NS, KS = C::KS, KC = C::KC, DV = C::DV, SB = C::SB;
+  constexpr uint32_t SLOT = C::SLOT, T_O = C::T_O;
   constexpr unsigned kAll = 0xffffffffu;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem_raw);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem_raw + C::NBARS * 8);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   PromptUnit& s_unit = *reinterpret_cast<PromptUnit*>(smem_raw + kUnitOfs);
+  float* s_ref = reinterpret_cast<float*>(smem_raw + kRefOfs);
+  float* s_sum = reinterpret_cast<float*>(smem_raw + kSumOfs);
   uint8_t* sQ = smem_raw + kHeader;
   uint8_t* ring = sQ + C::Q_BYTES;
   auto bar = [&](int i) { return smem_u32(&bars[i]); };
@@ -72,6 +89,8 @@ prompt_tc2_kernel(const __grid_constant__ PromptParams p, const __grid_constant_
   auto S_FULL = [&](int i) { return bar(C::B_S + i); };
   auto P_FULL = [&](int i, int h) { return bar(C::B_P + 2 * i + h); };    // used in the leader
   auto O_DONE = [&](int i) { return bar(C::B_O + i); };
+  auto REF = [&](int q, int i) { return bar(C::B_REF + 2 * q + i); };    // row quarter q, tile parity i
+  auto SUM = [&](int q) { return bar(C::B_SUM + q); };
   const uint32_t Q_FULL = bar(C::B_Q), TAIL = bar(C::B_TAIL), FIN = bar(C::B_FIN);
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -86,12 +105,16 @@ prompt_tc2_kernel(const __grid_constant__ PromptParams p, const __grid_constant_
       mbar_init(EMPTY(i), 1);
     }
     mbar_init(Q_FULL, 2);
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < SB; ++i) {
       mbar_init(S_FULL(i), 1);
-      mbar_init(P_FULL(i, 0), 8);                   // the softmax warps of both CTAs
+      mbar_init(P_FULL(i, 0), 8);                   // a tile's softmax warps of both CTAs
       mbar_init(P_FULL(i, 1), 8);
-      mbar_init(O_DONE(i), 1);
     }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(O_DONE(i), 1);
+      for (int q = 0; q < 4; ++q) mbar_init(REF(q, i), 1);
+    }
+    for (int q = 0; q < 4; ++q) mbar_init(SUM(q), 2);   // the quarter's two warps
     mbar_init(TAIL, 1);
     mbar_init(FIN, 1);
     *abort_flag = 0;
@@ -106,11 +129,11 @@ prompt_tc2_kernel(const __grid_constant__ PromptParams p, const __grid_constant_
     }
     fence_proxy_async_smem();
   }
-  if (warp == 5) {
+  if (warp == 9) {
     tmem_alloc_pair(smem_u32(tmem_slot), 512);
     tmem_relinquish_pair();
   }
-  if (warp == 4 && lane == 0) {
+  if (warp == 8 && lane == 0) {
     tma_prefetch_desc(&tm_q);
     tma_prefetch_desc(&tm_kc);
     tma_prefetch_desc(&tm_vc);
@@ -145,7 +168,7 @@ prompt_tc2_kernel(const __grid_constant__ PromptParams p, const __grid_constant_
 
   if (T == 0) {
     // nothing for this pair
-  } else if (warp == 4) {
+  } else if (warp == 8) {
     // ============================================================ producer
     const bool leader = rank == 0, rows_here = tok0 < n;
     if (lane == 0) {
@@ -178,17 +201,21 @@ prompt_tc2_kernel(const __grid_constant__ PromptParams p, const __grid_constant_
       const int64_t e = min(a + len, P);
       return e > a ? (int)((e - a + kPageSize - 1) / kPageSize) : 0;
     };
-    int pid_a = page_id(0), pid_b = page_id(1), row_k = -1, row_v = -1;
+    int pid_a = page_id(0), pid_b = page_id(1);
+    int row_at[C::AHEAD + 1];                       // TMA rows of the tiles t, t - 1, ...
+#pragma unroll
+    for (int i = 0; i <= C::AHEAD; ++i) row_at[i] = -1;
     int j = 0, tail_uses = 0;
     bool ok = true;
-    for (int t = 0; t <= T && ok; ++t) {
-      row_v = row_k;
-      row_k = page_row(t, pid_a);
+    for (int t = 0; t < T + C::AHEAD && ok; ++t) {
+#pragma unroll
+      for (int i = C::AHEAD; i > 0; --i) row_at[i] = row_at[i - 1];
+      row_at[0] = page_row(t, pid_a);
       pid_a = pid_b;
       pid_b = page_id(t + 2);
-      for (int part = 0; part <= KS && ok; ++part) {   // the K slots of tile t, then V of tile t - 1
+      for (int part = 0; part <= KS && ok; ++part) {   // the K slots of tile t, then V of tile t - AHEAD
         const bool isv = part == KS;
-        const int tile = isv ? t - 1 : t;
+        const int tile = isv ? t - C::AHEAD : t;
         if (tile < 0 || tile >= T) continue;
         const int tt = t_begin + tile;
         const bool own = tt >= Pt;
@@ -205,8 +232,8 @@ prompt_tc2_kernel(const __grid_constant__ PromptParams p, const __grid_constant_
         const uint32_t fb = fix ? map_to_cta(TAIL, rank) : full_l;
         uint32_t total = 2 * SLOT;                  // bytes both CTAs bring (the leader expects them all)
         if (p.paged && !own)
-          total = (isv ? 2u * (uint32_t)pages_in(first, BN) * 2u
-                       : (uint32_t)(pages_in(first, KH) + pages_in(first + KH, KH)) * 4u) *
+          total = (isv ? 2u * (uint32_t)pages_in(first, BN) * (DV / 128)
+                       : (uint32_t)(pages_in(first, KH) + pages_in(first + KH, KH)) * (KC / 64)) *
                   (kPageSize * 128u);
         if (lane == 0) {
           if (fix) mbar_expect_tx(TAIL, total / 2);
@@ -217,28 +244,28 @@ prompt_tc2_kernel(const __grid_constant__ PromptParams p, const __grid_constant_
           if (lane == 0) {
             const int64_t row =
                 (own ? (int64_t)g * p.rows + o0 : ((int64_t)b * p.Hkv + g) * p.capacity) + first + (isv ? 0 : KH * rank);
-            if (!isv) {                             // 64 keys x 256 channels
-              for (int bx = 0; bx < 4; ++bx)
-                tma2_load_2d(smem_u32(dst + bx * (KH * 128)), own ? &tm_kr : &tm_kc, fb, part * 256 + bx * 64,
+            if (!isv) {                             // 64 keys x KC channels
+              for (int bx = 0; bx < KC / 64; ++bx)
+                tma2_load_2d(smem_u32(dst + bx * (KH * 128)), own ? &tm_kr : &tm_kc, fb, part * KC + bx * 64,
                              (int)row);
-            } else {                                // 128 keys x 128 columns
-              for (int bx = 0; bx < 2; ++bx)
+            } else {                                // 128 keys x DV / 2 columns
+              for (int bx = 0; bx < DV / 128; ++bx)
                 tma2_load_2d(smem_u32(dst + bx * (BN * 128)), own ? &tm_vr : &tm_vc, fb,
-                             vh * DV + 128 * (int)rank + bx * 64, (int)row);
+                             vh * DV + DV / 2 * (int)rank + bx * 64, (int)row);
             }
           }
         } else {
-          const int my_row = isv ? row_v : row_k;
+          const int my_row = isv ? row_at[C::AHEAD] : row_at[0];
           if (!isv) {
             const int pg = lane - 4 * (int)rank;    // lanes 4 rank .. 4 rank + 3 own the pages of this CTA's 64 keys
             if (pg >= 0 && pg < 4 && my_row >= 0)
-              for (int bx = 0; bx < 4; ++bx)
-                tma2_load_2d(smem_u32(dst + bx * (KH * 128) + pg * kPageSize * 128), &tm_kc, fb, part * 256 + bx * 64,
+              for (int bx = 0; bx < KC / 64; ++bx)
+                tma2_load_2d(smem_u32(dst + bx * (KH * 128) + pg * kPageSize * 128), &tm_kc, fb, part * KC + bx * 64,
                              my_row);
           } else if (my_row >= 0) {
-            for (int bx = 0; bx < 2; ++bx)
+            for (int bx = 0; bx < DV / 128; ++bx)
               tma2_load_2d(smem_u32(dst + bx * (BN * 128) + lane * kPageSize * 128), &tm_vc, fb,
-                           vh * DV + 128 * (int)rank + bx * 64, my_row);
+                           vh * DV + DV / 2 * (int)rank + bx * 64, my_row);
           }
         }
         __syncwarp();
@@ -249,7 +276,7 @@ prompt_tc2_kernel(const __grid_constant__ PromptParams p, const __grid_constant_
           }
           ++tail_uses;
           const int nz = BN - valid;
-          for (int e = lane; e < 2 * nz * 8; e += 32) {
+          for (int e = lane; e < DV / 128 * nz * 8; e += 32) {
             const int bx = e / (nz * 8), r = valid + (e / 8) % nz, q16 = e % 8;
             *reinterpret_cast<uint4*>(dst + bx * (BN * 128) + r * 128 + q16 * 16) = make_uint4(0, 0, 0, 0);
           }
@@ -269,75 +296,107 @@ prompt_tc2_kernel(const __grid_constant__ PromptParams p, const __grid_constant_
       mbar_wait(Q_FULL, 0, &spare, kWaitNs);
       for (int jj = (j > NS ? j - NS : 0); jj < j; ++jj) mbar_wait(FULL(jj % NS), (jj / NS) & 1, &spare, kWaitNs);
     }
-  } else if (warp == 5) {
-    // ============================================================ MMA issuer (leader)
-    if (lane == 0 && rank == 0) {
+  } else if (warp == 9) {
+    // ============================================================ MMA issuer (the leader's warp, one lane's instructions)
+    if (rank == 0) {
       constexpr uint32_t ID_QK = idesc_bf16_f32(2 * BM, BN, 0, 0);
       constexpr uint32_t ID_PV = idesc_bf16_f32(2 * BM, DV, 0, 1);
-      const uint32_t q_addr = smem_u32(sQ), ring_addr = smem_u32(ring);
-      bool ok = mbar_wait(Q_FULL, 0, abort_flag, kWaitNs);
+      constexpr uint32_t HI = desc_hi(1024, 2);
+      const uint32_t q_lo = desc_lo(smem_u32(sQ), 16), k_lo = desc_lo(smem_u32(ring), 16),
+                     v_lo = desc_lo(smem_u32(ring), BN * 128);
+      const uint32_t tm = __shfl_sync(kAll, tmem, 0);
+      const int nt = __shfl_sync(kAll, T, 0);
+      const bool one = elect_one();
+      auto wait = [&](uint32_t bar, uint32_t parity) {
+        return __all_sync(kAll, mbar_wait(bar, parity, abort_flag, kWaitNs)) != 0;
+      };
+      bool ok = wait(Q_FULL, 0);
       tc_fence_after();
-      int j = 0;
-      for (int t = 0; t <= T && ok; ++t) {
-        if (t < T) {
-          const uint32_t sbuf = tmem + (uint32_t)((t & 1) * 128);
-#pragma unroll
-          for (int ks = 0; ks < KS; ++ks, ++j) {
-            const int slot = j % NS;
-            if (!mbar_wait(FULL(slot), (j / NS) & 1, abort_flag, kWaitNs)) { ok = false; break; }
-            tc_fence_after();
-            const uint32_t kaddr = ring_addr + slot * SLOT;
-#pragma unroll
-            for (int kk = 0; kk < 16; ++kk) {
-              const uint64_t a = smem_desc(q_addr + (4 * ks + (kk >> 2)) * (BM * 128) + (kk & 3) * 32, 16, 1024, 2);
-              const uint64_t bd = smem_desc(kaddr + (kk >> 2) * (KH * 128) + (kk & 3) * 32, 16, 1024, 2);
-              mma_pair_ss(sbuf, a, bd, ID_QK, ks + kk > 0 ? 1u : 0u);
-            }
-            mma_commit_pair(EMPTY(slot));
-          }
-          if (!ok) break;
-          mma_commit_pair(S_FULL(t & 1));
+      int slot = 0, phase = 0, sk = 0, sv = 0, pv = 0;   // ring; buffer of the next S, of the next P, the latter's phase
+      auto next = [&] {
+        if (++slot == NS) {
+          slot = 0;
+          phase ^= 1;
         }
-        if (t >= 1) {
-          const int u = t - 1, slot = j % NS;
-          const uint32_t pbuf = tmem + (uint32_t)((u & 1) * 128), vaddr = ring_addr + slot * SLOT;
-          if (!mbar_wait(FULL(slot), (j / NS) & 1, abort_flag, kWaitNs)) { ok = false; break; }
-          tc_fence_after();
-          for (int h = 0; h < 2 && ok; ++h) {
-            if (!mbar_wait(P_FULL(u & 1, h), (u >> 1) & 1, abort_flag, kWaitNs)) { ok = false; break; }
-            tc_fence_after();
+      };
+      for (int t = 0; t < nt + C::AHEAD && ok; ++t) {
+        if (t < nt) {
+          const uint32_t to = tm + (uint32_t)(sk * 128);
 #pragma unroll
-            for (int kq = 0; kq < BN / 32; ++kq) {
-              const int kk = h * (BN / 32) + kq;
-              const uint64_t bd = smem_desc(vaddr + kk * (16 * 128), BN * 128, 1024, 2);
-              mma_pair_ts(tmem + 256, pbuf + kk * 8, bd, ID_PV, (u > 0 || kk > 0) ? 1u : 0u);
+          for (int ks = 0; ks < KS; ++ks) {
+            ok = ok && wait(FULL(slot), phase);
+            if (!ok) break;
+            tc_fence_after();
+            const uint32_t a = q_lo + ks * (KC / 64) * (BM * 128 / 16), bd = k_lo + slot * (SLOT / 16);
+            if (one) {
+              if (ks == 0) mma_pair_ss_lo<false>(to, a, bd, HI, ID_QK);
+              else mma_pair_ss_lo<true>(to, a, bd, HI, ID_QK);
+#pragma unroll
+              for (int kk = 1; kk < KC / 16; ++kk)
+                mma_pair_ss_lo<true>(to, a + (kk >> 2) * (BM * 128 / 16) + (kk & 3) * 2,
+                                     bd + (kk >> 2) * (KH * 128 / 16) + (kk & 3) * 2, HI, ID_QK);
+              mma_commit_pair(EMPTY(slot));
+            }
+            next();
+          }
+          if (!ok) break;
+          if (one) mma_commit_pair(S_FULL(sk));
+          sk = sk + 1 == SB ? 0 : sk + 1;
+        }
+        if (t >= C::AHEAD) {
+          const int u = t - C::AHEAD;
+          const uint32_t to = tm + T_O, pa = tm + (uint32_t)(sv * 128), bd = v_lo + slot * (SLOT / 16);
+          ok = wait(FULL(slot), phase);
+          if (!ok) break;
+          tc_fence_after();
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            ok = ok && wait(P_FULL(sv, h), pv & 1);
+            if (!ok) break;
+            tc_fence_after();
+            if (one) {
+#pragma unroll
+              for (int kq = 0; kq < BN / 32; ++kq) {
+                const int kk = h * (BN / 32) + kq;
+                if (kk == 0 && u == 0) mma_pair_ts_lo<false>(to, pa, bd, HI, ID_PV);
+                else mma_pair_ts_lo<true>(to, pa + kk * 8, bd + kk * (16 * 128 / 16), HI, ID_PV);
+              }
             }
           }
           if (!ok) break;
-          mma_commit_pair(EMPTY(slot));
-          mma_commit_pair(O_DONE(u & 1));
-          ++j;
+          if (one) {
+            mma_commit_pair(EMPTY(slot));
+            mma_commit_pair(O_DONE(u & 1));
+          }
+          next();
+          if (++sv == SB) {
+            sv = 0;
+            ++pv;
+          }
         }
       }
-      mma_commit_pair(FIN);
+      if (one) mma_commit_pair(FIN);
       int spare = 0;                                // (not abort_flag: this wait also follows a timeout)
       mbar_wait(FIN, 0, &spare, kWaitNs);
+      __syncwarp();
     }
   } else {
     // ============================================================ softmax and epilogue (own rows)
-    const int r = tid;                              // row of the tile == TMEM lane
-    const uint32_t lane_base = (uint32_t)(warp * 32) << 16;
-    const uint32_t obuf = tmem + lane_base + 256;
+    const int grp = warp >> 2, quarter = warp & 3;  // this group's tiles: grp, grp + 2, ...
+    const int r = quarter * 32 + lane;              // row of the tile == TMEM lane
+    const uint32_t lane_base = (uint32_t)(quarter * 32) << 16;
+    const uint32_t obuf = tmem + lane_base + T_O;
     const float c2 = p.scale_log2;
     const int token = tok0 + r / G;                 // the row's place in its sequence
     const bool row_ok = r < p.rows_per_tile && token < n;
     const bool warp_live = __any_sync(kAll, row_ok);
-    float m_ref = -INFINITY, l = 0.f;
+    float m_ref = -INFINITY, l = 0.f;               // the row's reference as this group last saw it; its tiles' sum
     bool ok = true;
-    for (int t = 0; t < T; ++t) {
-      if (!__all_sync(kAll, mbar_wait(S_FULL(t & 1), (t >> 1) & 1, abort_flag, kWaitNs))) { ok = false; break; }
+    for (int t = grp; t < T; t += 2) {
+      const int sb = t % SB;
+      if (!__all_sync(kAll, mbar_wait(S_FULL(sb), (t / SB) & 1, abort_flag, kWaitNs))) { ok = false; break; }
       tc_fence_after();
-      const uint32_t sbuf = tmem + lane_base + (uint32_t)((t & 1) * 128);
+      const uint32_t sbuf = tmem + lane_base + (uint32_t)(sb * 128);
       if (warp_live) {
         uint32_t sv[BN];
         tmem_ld_x128(sbuf, sv);
@@ -357,29 +416,41 @@ prompt_tc2_kernel(const __grid_constant__ PromptParams p, const __grid_constant_
         for (int e = 4; e < BN; e += 2)
           mq[(e >> 1) & 3] = fmax3(mq[(e >> 1) & 3], __uint_as_float(sv[e]), __uint_as_float(sv[e + 1]));
         const float mx = fmax3(mq[0], mq[1], fmaxf(mq[2], mq[3]));
-        const float m_new = fmaxf(m_ref, mx == -INFINITY ? -INFINITY : mx * c2);
-        const bool first = m_ref == -INFINITY;
-        const bool need = !first && m_new > m_ref + kRescaleThreshold;
+        const float m_tile = mx == -INFINITY ? -INFINITY : mx * c2;
+        float m_in = -INFINITY;                     // the reference after the tile before
+        if (t > 0) {
+          if (!__all_sync(kAll, mbar_wait(REF(quarter, (t - 1) & 1), ((t - 1) >> 1) & 1, abort_flag, kWaitNs))) {
+            ok = false;
+            break;
+          }
+          m_in = s_ref[r];
+        }
+        const bool first = m_in == -INFINITY;
+        const bool need = !first && m_tile > m_in + kRescaleThreshold;
+        const float m_out = first || need ? fmaxf(m_in, m_tile) : m_in;
         if (__any_sync(kAll, need)) {
           // O holds the tiles before this one once the last of their products is done
           const int u = t - 1;
           if (!__all_sync(kAll, mbar_wait(O_DONE(u & 1), (u >> 1) & 1, abort_flag, kWaitNs))) { ok = false; break; }
           tc_fence_after();
-          const float alpha = need ? ex2(m_ref - m_new) : 1.f;
+          const float alpha = need ? ex2(m_in - m_out) : 1.f;
 #pragma unroll 1
-          for (int c = 0; c < DV; c += 32) {
-            uint32_t rr[32];
-            tmem_ld_x32(obuf + c, rr);
+          for (int c = 0; c < DV; c += 16) {
+            uint32_t rr[16];
+            tmem_ld_x16(obuf + c, rr);
 #pragma unroll
-            for (int e = 0; e < 32; ++e) rr[e] = __float_as_uint(__uint_as_float(rr[e]) * alpha);
-            tmem_st_x32(obuf + c, rr);
-          }
-          if (need) {
-            l *= alpha;
-            m_ref = m_new;
+            for (int e = 0; e < 16; ++e) rr[e] = __float_as_uint(__uint_as_float(rr[e]) * alpha);
+            tmem_st_x16(obuf + c, rr);
           }
         }
-        if (first) m_ref = m_new;
+        s_ref[r] = m_out;
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(REF(quarter, t & 1));
+        if (m_out != m_ref) {                       // (from -inf: the sum is 0 and stays 0)
+          l *= m_ref == -INFINITY ? 0.f : ex2(m_ref - m_out);
+          m_ref = m_out;
+        }
         const float nm = m_ref == -INFINITY ? 0.f : -m_ref;   // nothing seen yet: 2^-inf = 0
         const uint64_t c2x2 = pk2(c2, c2), nmx2 = pk2(nm, nm);
         uint64_t l4[4] = {0ull, 0ull, 0ull, 0ull};
@@ -397,7 +468,7 @@ prompt_tc2_kernel(const __grid_constant__ PromptParams p, const __grid_constant_
           tmem_st_x32(sbuf + h * 32, pk);
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) mbar_arrive_cluster(map_to_cta(P_FULL(t & 1, h), 0));
+          if (lane == 0) mbar_arrive_cluster(map_to_cta(P_FULL(sb, h), 0));
         }
         const float2 la = up2(fadd2(fadd2(l4[0], l4[1]), fadd2(l4[2], l4[3])));
         l += la.x + la.y;
@@ -406,42 +477,86 @@ prompt_tc2_kernel(const __grid_constant__ PromptParams p, const __grid_constant_
         tc_fence_before();
         __syncwarp();
         if (lane == 0) {
-          mbar_arrive_cluster(map_to_cta(P_FULL(t & 1, 0), 0));
-          mbar_arrive_cluster(map_to_cta(P_FULL(t & 1, 1), 0));
+          mbar_arrive_cluster(map_to_cta(P_FULL(sb, 0), 0));
+          mbar_arrive_cluster(map_to_cta(P_FULL(sb, 1), 0));
         }
       }
     }
+    // Epilogue: the groups' sums, brought to the row's last reference, are added; each group writes half of the columns,
+    // through the query tile's shared memory, which no product reads any more: a thread stages 128 bytes of its row
+    // (16-byte piece c at c ^ (row & 7)), then 8 lanes store them together.
     const int u = T - 1;
-    if (ok) ok = __all_sync(kAll, mbar_wait(O_DONE(u & 1), (u >> 1) & 1, abort_flag, kWaitNs));
+    // (the last products by their own barrier: the group that is done first may be two phases of O_DONE ahead)
+    if (ok) ok = __all_sync(kAll, mbar_wait(FIN, 0, abort_flag, kWaitNs));
+    if (ok && warp_live)
+      ok = __all_sync(kAll, mbar_wait(REF(quarter, u & 1), (u >> 1) & 1, abort_flag, kWaitNs));
     if (ok && warp_live) {
       tc_fence_after();
-      const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
+      const float mf = s_ref[r];
+      s_sum[grp * 128 + r] = m_ref == -INFINITY ? 0.f : l * ex2(m_ref - mf);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(SUM(quarter));
+      ok = __all_sync(kAll, mbar_wait(SUM(quarter), 0, abort_flag, kWaitNs));
+      const float L = s_sum[r] + s_sum[128 + r];
+      const float inv = L > 0.f ? 1.f / L : (L == 0.f ? 0.f : L);
+      uint8_t* stage = sQ + warp * (32 * 128);
       const int my_s = (Pt + token / BN) / p.chunk_tiles;     // the row's last split
-      const bool split = my_s > 0, write = row_ok && s <= my_s;
-      const int h = g * G + r % G;
-      const int64_t at = split ? prompt_slot(o0 + token, h, s, p.Hq, p.splits) : (int64_t)(o0 + token) * p.Hq + h;
+      const bool part = my_s > 0, write = ok && row_ok && s <= my_s;
+      const int64_t slot = part ? prompt_slot(o0 + token, g * G + r % G, s, p.Hq, p.splits)
+                                : (int64_t)(o0 + token) * p.Hq + g * G + r % G;
+      // rows of each form in the warp: bf16 results, fp32 results, fp32 partials
+      const unsigned parts = __ballot_sync(kAll, write && part), rows = __ballot_sync(kAll, write && !part);
+      auto flush = [&](unsigned which, char* base, int64_t row_bytes, int64_t ofs) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int rr = 4 * i + (lane >> 3), c = lane & 7;
+          const int64_t at = __shfl_sync(kAll, slot, rr);
+          const uint4 v = *reinterpret_cast<const uint4*>(stage + rr * 128 + ((c ^ (rr & 7)) << 4));
+          if (which >> rr & 1u) *reinterpret_cast<uint4*>(base + at * row_bytes + ofs + c * 16) = v;
+        }
+      };
+      const int col0 = grp * (DV / 2);              // of the unit's columns
+      if (rows && p.out_bf16) {
 #pragma unroll 1
-      for (int c = 0; c < DV; c += 32) {
-        uint32_t rr[32];
-        tmem_ld_x32(obuf + c, rr);
-        if (!write) continue;
-        float v[32];
+        for (int c = 0; c < DV / 2; c += 64) {
+          __syncwarp();
 #pragma unroll
-        for (int e = 0; e < 32; ++e) v[e] = __uint_as_float(rr[e]) * inv;
-        const int64_t to = at * D + vh * DV + c;
-        if (!split && p.out_bf16) {
-          uint4* dst = reinterpret_cast<uint4*>(reinterpret_cast<__nv_bfloat16*>(p.out) + to);
+          for (int hf = 0; hf < 2; ++hf) {
+            uint32_t rr[32];
+            tmem_ld_x32(obuf + col0 + c + 32 * hf, rr);
 #pragma unroll
-          for (int e = 0; e < 4; ++e)
-            dst[e] = make_uint4(pack_bf16(v[8 * e], v[8 * e + 1]), pack_bf16(v[8 * e + 2], v[8 * e + 3]),
-                                pack_bf16(v[8 * e + 4], v[8 * e + 5]), pack_bf16(v[8 * e + 6], v[8 * e + 7]));
-        } else {
-          float4* dst = reinterpret_cast<float4*>((split ? p.o_part : reinterpret_cast<float*>(p.out)) + to);
+            for (int e = 0; e < 4; ++e) {
+              uint32_t w[4];
 #pragma unroll
-          for (int e = 0; e < 8; ++e) dst[e] = make_float4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
+              for (int q = 0; q < 4; ++q)
+                w[q] = pack_bf16(__uint_as_float(rr[8 * e + 2 * q]) * inv, __uint_as_float(rr[8 * e + 2 * q + 1]) * inv);
+              *reinterpret_cast<uint4*>(stage + lane * 128 + (((4 * hf + e) ^ (lane & 7)) << 4)) =
+                  make_uint4(w[0], w[1], w[2], w[3]);
+            }
+          }
+          __syncwarp();
+          flush(rows, reinterpret_cast<char*>(p.out), D * 2, (vh * DV + col0 + c) * 2);
         }
       }
-      if (write && split && vh == 0) p.ml_part[at] = make_float2(m_ref, l);
+      const unsigned wide = parts | (p.out_bf16 ? 0u : rows);
+      if (wide) {
+#pragma unroll 1
+        for (int c = 0; c < DV / 2; c += 32) {
+          uint32_t rr[32];
+          tmem_ld_x32(obuf + col0 + c, rr);
+          __syncwarp();
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            *reinterpret_cast<float4*>(stage + lane * 128 + ((e ^ (lane & 7)) << 4)) =
+                make_float4(__uint_as_float(rr[4 * e]) * inv, __uint_as_float(rr[4 * e + 1]) * inv,
+                            __uint_as_float(rr[4 * e + 2]) * inv, __uint_as_float(rr[4 * e + 3]) * inv);
+          __syncwarp();
+          const int64_t ofs = (vh * DV + col0 + c) * 4;
+          if (parts) flush(parts, reinterpret_cast<char*>(p.o_part), D * 4, ofs);
+          if (wide & ~parts) flush(wide & ~parts, reinterpret_cast<char*>(p.out), D * 4, ofs);
+        }
+      }
+      if (write && part && vh == 0 && grp == 0) p.ml_part[slot] = make_float2(mf, L);
     }
   }
 
@@ -450,7 +565,7 @@ prompt_tc2_kernel(const __grid_constant__ PromptParams p, const __grid_constant_
   // once the peer has seen it, no arrive of the pair's products is under way
   // to its shared memory, and the cluster barrier keeps either CTA from
   // leaving before the other is done.
-  if (T > 0 && warp == 5 && lane == 0 && rank != 0) {
+  if (T > 0 && warp == 9 && lane == 0 && rank != 0) {
     int spare = 0;
     mbar_wait(FIN, 0, &spare, kWaitNs);
   }
@@ -458,7 +573,7 @@ prompt_tc2_kernel(const __grid_constant__ PromptParams p, const __grid_constant_
   __syncthreads();
   if (tid == 0 && *abort_flag) set_status(p.status, TV_DEV_TIMEOUT);
   cluster_sync_relaxed();
-  if (warp == 5) {
+  if (warp == 9) {
     tc_fence_after();
     tmem_dealloc_pair(tmem, 512);
   }
@@ -476,6 +591,7 @@ bool encode(CUtensorMap* m, const void* ptr, int rank, const cuuint64_t* dims, c
 
 template <int D>
 cudaError_t launch_d(const PromptParams& p, int64_t units, cudaStream_t st) {
+  constexpr int DV = Cfg<D>::DV;
   CUtensorMap mq, mkc, mvc, mkr, mvr;
   const cuuint64_t row_bytes = (cuuint64_t)D * 2;
   {
