@@ -18,7 +18,8 @@ from . import (BF16, F32, make_desc, make_expand_desc, tree_accept_commit, tree_
                tv_lm_head_argmax, tv_lm_head_workspace_size, tree_accept_commit_argmax,
                make_window, tree_verify_attn_window, tv_window_workspace_size, tree_verify_attn_kv4,
                tree_accept_commit_argmax_kv4, tv_kv4_append, tv_kv4_cache_bytes, tv_kv4_read, tv_kv4_workspace_size,
-               tv_attn_plan, tv_kv4_attn_plan, tv_window_attn_plan)
+               tv_attn_plan, tv_kv4_attn_plan, tv_window_attn_plan, tv_prompt_attn, tv_prompt_rope_store,
+               tv_prompt_workspace_size, make_logits_desc, tv_token_counts_add, tv_tree_logits_process)
 
 _DT = {torch.float32: F32, torch.bfloat16: BF16}
 
@@ -298,6 +299,84 @@ class DeviceExpand:
             self.step(s, stream)
 
 
+class DevicePrompt:
+    """Prompts (or chunks of them) on their way into a step's cache: `lens[b]`
+    new rows of sequence b behind what is committed.  run() rotates the rows,
+    writes their keys and values into the cache, attends to prefix and rows, and
+    moves the step's prefix lengths on."""
+
+    def __init__(self, step, lens, theta=1e4, max_prefix=0):
+        d, dev = step.desc, step.device
+        self.step, self.theta, self.rows, self.max_rows = step, theta, sum(lens), max(lens)
+        self.desc = make_desc(batch=d.batch, num_q_heads=d.num_q_heads, num_kv_heads=d.num_kv_heads,
+                              head_dim=d.head_dim, dtype=d.dtype, max_nodes=1, total_rows=d.batch,
+                              capacity=d.capacity, max_prefix=max_prefix, page_size=d.page_size,
+                              num_pages=d.num_pages, out_f32=d.out_f32, scale=d.scale)
+        offs = [0]
+        for n in lens:
+            offs.append(offs[-1] + n)
+        self.offsets = torch.tensor(offs, dtype=torch.int32, device=dev)
+        dt = step.q.dtype
+        self.q = torch.empty(self.rows, d.num_q_heads, d.head_dim, dtype=dt, device=dev)
+        self.k_rows = torch.empty(d.num_kv_heads, self.rows, d.head_dim, dtype=dt, device=dev)
+        self.v_rows = torch.empty_like(self.k_rows)
+        self.out = torch.empty(self.rows, d.num_q_heads, d.head_dim, dtype=step.out.dtype, device=dev)
+        self.new_prefix = torch.empty(d.batch, dtype=torch.int32, device=dev)
+        self.ws_bytes = tv_prompt_workspace_size(self.desc, self.rows, self.max_rows)
+        self.workspace = torch.empty(max(self.ws_bytes, 256), dtype=torch.uint8, device=dev)
+
+    def rope_store(self, q, k, v, stream=None):
+        st = self.step
+        tv_prompt_rope_store(self.desc, self.rows, self.max_rows, self.theta, q, k, v, st.prefix_len, self.offsets,
+                             self.q, self.k_rows, self.v_rows, st.k_cache, st.v_cache, st.page_table, self.new_prefix,
+                             st.status, stream)
+
+    def attn(self, stream=None):
+        st = self.step
+        tv_prompt_attn(self.desc, self.rows, self.max_rows, self.q, st.k_cache, st.v_cache, st.page_table,
+                       st.prefix_len, self.offsets, self.k_rows, self.v_rows, self.out, self.workspace, self.ws_bytes,
+                       st.status, stream)
+
+    def run(self, q, k, v, stream=None):
+        """q [rows, Hq, d], k and v [rows, Hkv, d] as the projections leave them."""
+        self.rope_store(q, k, v, stream)
+        self.attn(stream)
+        with _on(stream):
+            self.step.prefix_len.copy_(self.new_prefix)
+
+
+class LogitControl:
+    """Penalties, biases and grammar masks on a step's logits, with the token
+    counts they go by.  penalties [B, 3] float (repetition, frequency,
+    presence); biases: (offsets, tokens, values) or None; mask [rows, words]
+    int32 or None."""
+
+    def __init__(self, step, penalties, biases=None, mask=None):
+        B = step.desc.batch
+        self.step, self.mask = step, mask
+        self.penalties = penalties
+        self.biases = (None, None, None) if biases is None else biases
+        self.counts = torch.zeros(B, (step.vocab + 7) // 8 * 8, dtype=torch.int16, device=step.device)
+        self.desc = make_logits_desc(batch=B, vocab=step.vocab, max_nodes=step.desc.max_nodes,
+                                     total_rows=step.desc.total_rows, logits_dtype=step.logits_dtype,
+                                     biases=0 if biases is None else biases[1].numel())
+
+    def read(self, tokens, offsets, stream=None):
+        """The prompts' tokens (packed, int32)."""
+        tv_token_counts_add(self.desc, tokens, offsets, tokens.numel(), True, self.counts, self.step.status, stream)
+
+    def emitted(self, stream=None):
+        """What the step's accept + commit emitted."""
+        st = self.step
+        tv_token_counts_add(self.desc, st.tokens, None, st.desc.max_nodes, False, self.counts, st.status, stream)
+
+    def process(self, stream=None):
+        """The step's logits, in place (after its mask call)."""
+        st = self.step
+        tv_tree_logits_process(self.desc, st.logits, self.counts, self.penalties, *self.biases, self.mask, st.draft,
+                               st.node_offsets, st.anc, st.logits, st.status, stream)
+
+
 class DeviceLmHead:
     """Device buffers of one lm_head workload (workloads.LmHeadSpec): hidden
     rows and weights resident, the argmax and max-logit outputs, the
@@ -341,12 +420,17 @@ def main(argv=None):
     ap.add_argument("--window", default="", help="W,S: rows see the last W and the first S positions")
     ap.add_argument("--kv4", action="store_true",
                     help="the prefix in a 4-bit cache (with --window too); acceptance on the logits' argmax")
+    ap.add_argument("--prompt", type=int, default=0,
+                    help="N: first put N prompt rows a sequence through RoPE, the cache's writes and causal attention")
+    ap.add_argument("--steer", action="store_true", help="penalties on the logits before acceptance")
     ap.add_argument("--expand", default="", help="run a dynamic-expansion workload instead (eagle2, batched)")
     ap.add_argument("--lm-head", default="", help="run a fused lm_head + argmax workload instead (qwen, batched)")
     ap.add_argument("--vocab", type=int, default=0, help="with --lm-head: a smaller vocabulary (e.g. for a profiler)")
     a = ap.parse_args(argv)
     if a.kv4 and a.sampled > 0:
         ap.error("--sampled: the 4-bit cache is committed on a given argmax only")
+    if a.kv4 and a.prompt:
+        ap.error("--prompt: prompts into the 4-bit cache go through its append")
     _build.build()
     if a.lm_head:
         spec = wl.LMHEAD_CONFIGS[a.lm_head]
@@ -372,8 +456,22 @@ def main(argv=None):
     st = DeviceKv4Step(w, win) if a.kv4 else (DeviceWindowStep(w, *win) if win else DeviceStep(w))
     target = st.logits.float().argmax(1).to(torch.int32) if a.kv4 else None
     p0 = st.prefix_len.clone()
+    prompt = control = None
+    if a.prompt:                                 # rows of noise, into positions the workload's prefix holds after it
+        fill = min(a.prompt, int(p0.min()))
+        prompt = DevicePrompt(st, [fill] * st.desc.batch)
+        rows = [torch.randn(prompt.rows, h, st.desc.head_dim, device=st.device).to(st.q.dtype)
+                for h in (st.desc.num_q_heads, st.desc.num_kv_heads, st.desc.num_kv_heads)]
+    if a.steer:
+        control = LogitControl(st, torch.tensor([[1.1, 0.1, 0.1]] * st.desc.batch, device=st.device))
     for _ in range(a.steps):
+        if prompt:
+            st.prefix_len.zero_()
+            prompt.run(*rows)
         st.prefix_len.copy_(p0)
+        if control:
+            st.mask()
+            control.process()
         if a.attn_only:
             st.mask()
             st.attn()
@@ -385,6 +483,8 @@ def main(argv=None):
             st.step(target)
         else:
             st.step()
+        if control and not a.attn_only:
+            control.emitted()
     torch.cuda.synchronize()
     status = int(st.status[0].item())
     print(f"{w.spec.name}: {a.steps} steps, device status {status}")
