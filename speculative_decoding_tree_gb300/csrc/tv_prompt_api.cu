@@ -47,7 +47,10 @@ int make_prompt_plan(const tv_desc* d, int64_t rows, int64_t max_rows, PromptPla
   // one, in chunks of four tiles or more; kernel 8, whose tiles take longer,
   // into about two waves of chunks of any length (2000 fp32 rows x 4 heads at
   // head_dim 256: 175, 108, 144 and 129 us with 1, 2, 3 and 4).
-  const int64_t ctas = p->units * d->num_kv_heads * (p->pub.kernel == 6 ? 1 : d->head_dim / 128), sms = num_sms();
+  const int64_t sms = num_sms();
+  int64_t ctas;
+  if (!mul_ok(p->units, d->num_kv_heads, &ctas) || !mul_ok(ctas, p->pub.kernel == 6 ? 1 : d->head_dim / 128, &ctas))
+    return TV_ERR_OVERFLOW;
   int64_t want = ctas > 0 ? (parts ? 2 * sms : sms) / ctas : 1;
   if (!parts && want > tiles / 4) want = tiles / 4;
   if (want > tiles) want = tiles;

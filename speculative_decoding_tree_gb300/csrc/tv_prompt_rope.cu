@@ -203,6 +203,7 @@ int tv_prompt_rope_store(const tv_desc* desc, int64_t rows, int64_t max_rows, do
                        d_v_rows, d_k_cache, d_v_cache, d_page_table, d_new_prefix_len, d_status};
   for (const void* x : all)
     if (!aligned16(x)) return TV_ERR_ALIGN;
+  if (d_new_prefix_len == d_prefix_len) return TV_ERR_SHAPE;   // other rows still read the old lengths
   PRopeParams p = {};
   p.q_in = d_q_in; p.k_in = d_k_in; p.v_in = d_v_in;
   p.prefix_len = d_prefix_len; p.row_offsets = d_row_offsets;

@@ -98,6 +98,14 @@ def test_rope_arguments(L):
             assert _rope(L, d, ptrs=but(13, i, None)) == -1, i
         assert _rope(L, d, ptrs=but(13, i, FAKE + 4)) == -11, i
     assert _rope(L, _desc(page_size=16, num_pages=300), ptrs=but(13, 10, None)) == -1
+    assert _rope(L, d) == -6                             # the new lengths over the old ones
+
+
+def test_grids_that_do_not_fit(L):
+    n = ctypes.c_size_t(0)
+    wide = _desc(num_q_heads=2 ** 30, num_kv_heads=2 ** 30, batch=2 ** 31 - 1, page_size=16, num_pages=1, capacity=16,
+                 max_prefix=0)
+    assert L.tv_prompt_workspace_size(ctypes.byref(wide), 2 ** 20, 2 ** 20, ctypes.byref(n)) == -9
 
 
 def _logits(**kw):
