@@ -17,7 +17,7 @@
 // lie in memory as the matrix unit reads them (rows of 128 bytes, 16-byte
 // piece c at c ^ (row & 7)); rows that do not exist are zeros.  (Splitting in
 // the attention kernel itself, for every unit again, took 158 - 208 us where
-// this takes 108.)  The second copies those blocks to shared memory,
+// this took 108.)  The second copies those blocks to shared memory,
 // 48 KB each, and multiplies.
 //
 // A unit is 128 query rows (token, group head) of one sequence and KV head and
@@ -47,7 +47,8 @@ constexpr int DV = 128;                         // columns of V of a unit
 constexpr int CH = 64;                          // channels of a slot
 constexpr uint32_t PART = 128 * CH * 2;         // bytes of one bf16 part of a slot
 constexpr uint32_t SLOT = 3 * PART;
-constexpr int NS = 4;
+constexpr int NS = 4;                           // (even: DV / CH = 2 slots of V lie side by side)
+static_assert(DV / CH == 2 && NS % 2 == 0, "V's slots");
 constexpr uint32_t kHeader = 3072;
 constexpr uint32_t SMEM = kHeader + NS * SLOT;
 static_assert(SMEM <= 232448, "shared memory over the 227 KB per-block limit");
@@ -289,9 +290,9 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_f32_kernel(const __grid_co
   } else if (warp == 9) {
     // ============================================================ MMA issuer (the whole warp, one lane's instructions)
     constexpr uint32_t ID_QK = idesc_bf16_f32(BM, BN, 0, 0);
-    constexpr uint32_t ID_PV = idesc_bf16_f32(BM, CH, 0, 1);
+    constexpr uint32_t ID_PV = idesc_bf16_f32(BM, DV, 0, 1);
     constexpr uint32_t HI = desc_hi(1024, 2), P16 = PART / 16;
-    const uint32_t ring_lo = desc_lo(smem_u32(ring), 16), v_lo = desc_lo(smem_u32(ring), PART);
+    const uint32_t ring_lo = desc_lo(smem_u32(ring), 16), v_lo = desc_lo(smem_u32(ring), SLOT);
     const uint32_t tm = __shfl_sync(kAll, tmem, 0);
     const int nt = __shfl_sync(kAll, T, 0);
     const bool one = elect_one();
@@ -348,27 +349,30 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_f32_kernel(const __grid_co
       if (one) mma_commit(S_FULL);
       ok = wait(P_FULL, t & 1) && (t == 0 || wait(O_EMPTY, (t - 1) & 1));
       if (!ok) break;
-      for (int v = 0; v < DV / CH; ++v) {
-        ok = wait(FULL(slot), phase);
-        if (!ok) break;
-        tc_fence_after();
-        const uint32_t b = v_lo + slot * (SLOT / 16), to = tm + T_O + v * CH;
-        if (one) {
-          auto product = [&](uint32_t pa, uint32_t part, bool rest) {
+      // both blocks of V at once: 128 columns (64 run at 0.64 of the rate).  A tile's slots are even in number and so is
+      // the ring, so the two are neighbours, a slot apart.
+      const int vs = slot;
+      ok = wait(FULL(vs), phase) && wait(FULL(vs + 1), phase);
+      if (!ok) break;
+      next();
+      next();
+      tc_fence_after();
+      if (one) {
+        const uint32_t b = v_lo + vs * (SLOT / 16), to = tm + T_O;
+        auto product = [&](uint32_t pa, uint32_t part, bool rest) {
 #pragma unroll
-            for (int kk = 0; kk < BN / 16; ++kk)
-              if (rest || kk > 0) mma_ts_lo<true>(to, tm + pa + kk * 8, part + kk * (16 * 128 / 16), HI, ID_PV);
-          };
-          mma_ts_lo<false>(to, tm + T_BIG, b + 2 * P16, HI, ID_PV);
-          product(T_BIG, b + 2 * P16, false);
-          product(T_SMALL, b, true);
-          product(T_BIG + 64, b + P16, true);
-          product(T_BIG, b + P16, true);
-          product(T_BIG + 64, b, true);
-          product(T_BIG, b, true);
-          mma_commit(EMPTY(slot));
-        }
-        next();
+          for (int kk = 0; kk < BN / 16; ++kk)
+            if (rest || kk > 0) mma_ts_lo<true>(to, tm + pa + kk * 8, part + kk * (16 * 128 / 16), HI, ID_PV);
+        };
+        mma_ts_lo<false>(to, tm + T_BIG, b + 2 * P16, HI, ID_PV);
+        product(T_BIG, b + 2 * P16, false);
+        product(T_SMALL, b, true);
+        product(T_BIG + 64, b + P16, true);
+        product(T_BIG, b + P16, true);
+        product(T_BIG + 64, b, true);
+        product(T_BIG, b, true);
+        mma_commit(EMPTY(vs));
+        mma_commit(EMPTY(vs + 1));
       }
       if (!ok) break;
       if (one) mma_commit(O_FULL);
