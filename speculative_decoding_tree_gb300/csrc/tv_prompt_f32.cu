@@ -49,7 +49,7 @@ constexpr uint32_t PART = 128 * CH * 2;         // bytes of one bf16 part of a s
 constexpr uint32_t SLOT = 3 * PART;
 constexpr int NS = 4;                           // (even: DV / CH = 2 slots of V lie side by side)
 static_assert(DV / CH == 2 && NS % 2 == 0, "V's slots");
-constexpr uint32_t kHeader = 3072;
+constexpr uint32_t kHeader = 3 * 1024;
 constexpr uint32_t SMEM = kHeader + NS * SLOT;
 static_assert(SMEM <= 232448, "shared memory over the 227 KB per-block limit");
 constexpr int kThreads = 320;
@@ -488,9 +488,12 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_f32_kernel(const __grid_co
         if (!split && p.out_bf16) {
           uint4* dst = reinterpret_cast<uint4*>(reinterpret_cast<__nv_bfloat16*>(p.out) + to);
 #pragma unroll
-          for (int e = 0; e < 8; ++e)
-            dst[e] = make_uint4(pack_bf16(o[8 * e] * inv, o[8 * e + 1] * inv), pack_bf16(o[8 * e + 2] * inv, o[8 * e + 3] * inv),
-                                pack_bf16(o[8 * e + 4] * inv, o[8 * e + 5] * inv), pack_bf16(o[8 * e + 6] * inv, o[8 * e + 7] * inv));
+          for (int e = 0; e < 8; ++e) {
+            uint32_t w[4];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) w[q] = pack_bf16(o[8 * e + 2 * q] * inv, o[8 * e + 2 * q + 1] * inv);
+            dst[e] = make_uint4(w[0], w[1], w[2], w[3]);
+          }
         } else {
           float4* dst = reinterpret_cast<float4*>((split ? p.o_part : reinterpret_cast<float*>(p.out)) + to);
 #pragma unroll
@@ -515,8 +518,8 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_f32_kernel(const __grid_co
 template <bool BF16, int D>
 cudaError_t launch_d(const PromptParams& p, int64_t units, cudaStream_t st) {
   const Blocks blocks(p.max_prefix, p.rows, p.B, p.G);
-  cudaError_t e = launch_dep(prompt_split_kernel<BF16, D>, dim3((unsigned)(blocks.ktiles + blocks.qtiles), p.Hkv * (D / CH)),
-                             dim3(256), 0, st, p);
+  const dim3 grid((unsigned)(blocks.ktiles + blocks.qtiles), p.Hkv * (D / CH));
+  cudaError_t e = launch_dep(prompt_split_kernel<BF16, D>, grid, dim3(256), 0, st, p);
   if (e != cudaSuccess) return e;
   e = ensure_max_dynamic_smem<prompt_f32_kernel<D>>((int)SMEM);
   if (e != cudaSuccess) return e;

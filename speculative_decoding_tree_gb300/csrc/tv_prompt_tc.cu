@@ -39,7 +39,7 @@ constexpr int BN = kPromptTile;                 // keys of a tile
 constexpr uint32_t BOX_BYTES = BN * 128;        // 128 rows x 64 bf16
 constexpr uint32_t SLOT_BYTES = 2 * BOX_BYTES;
 constexpr int NS = 5;                           // ring slots
-constexpr uint32_t kHeader = 3072, kUnitOfs = 1024;
+constexpr uint32_t kHeader = 3 * 1024, kUnitOfs = 1024;
 constexpr uint32_t Q_BYTES = 2 * BM * D * 2;
 constexpr uint32_t SMEM = kHeader + Q_BYTES + NS * SLOT_BYTES;
 static_assert(SMEM <= 232448, "shared memory over the 227 KB per-block limit");

@@ -39,7 +39,7 @@ using namespace tc;
 constexpr int BM = 128;                         // query rows per CTA
 constexpr int BN = kPromptTile;                 // keys of a tile
 constexpr int KH = BN / 2;                      // keys of a K tile per CTA
-constexpr uint32_t kHeader = 3072, kUnitOfs = 512;
+constexpr uint32_t kHeader = 3 * 1024, kUnitOfs = 512;
 constexpr uint32_t kRefOfs = 1024;              // [128] floats: a row's reference
 constexpr uint32_t kSumOfs = 1536;              // [2][128] floats: the groups' sums
 static_assert(kSumOfs + 1024 <= kHeader, "header");

@@ -303,10 +303,12 @@ class DevicePrompt:
     """Prompts (or chunks of them) on their way into a step's cache: `lens[b]`
     new rows of sequence b behind what is committed.  run() rotates the rows,
     writes their keys and values into the cache, attends to prefix and rows, and
-    moves the step's prefix lengths on."""
+    moves the step's prefix lengths on.  max_prefix: a bound on what is committed
+    before (the step's own if None)."""
 
-    def __init__(self, step, lens, theta=1e4, max_prefix=0):
+    def __init__(self, step, lens, theta=1e4, max_prefix=None):
         d, dev = step.desc, step.device
+        max_prefix = d.max_prefix if max_prefix is None else int(max_prefix)
         self.step, self.theta, self.rows, self.max_rows = step, theta, sum(lens), max(lens)
         self.desc = make_desc(batch=d.batch, num_q_heads=d.num_q_heads, num_kv_heads=d.num_kv_heads,
                               head_dim=d.head_dim, dtype=d.dtype, max_nodes=1, total_rows=d.batch,

@@ -213,3 +213,35 @@ def test_captured_loop():
 
 def test_command():
     assert runner.main(["--config", "1", "--steps", "2", "--prompt", "20", "--steer"]) == 0
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_pages_beyond_32_bit_offsets(dtype):
+    """The sequence's pages lie behind 2^31 values of a pool."""
+    pages, hkv, d, P, n = 140000, 8, 128, 100, 60
+    k_cache, v_cache = (torch.empty(pages, hkv, 16, d, dtype=dtype, device="cuda") for _ in range(2))
+    assert k_cache.numel() > 2 ** 31
+    table = torch.arange(pages - 1, pages - 12, -1, dtype=torch.int32, device="cuda")[None].contiguous()
+    past = [torch.randn(hkv, 112, d, generator=torch.Generator().manual_seed(i)).to(dtype).cuda() for i in range(2)]
+    for x, y in ((k_cache, past[0]), (v_cache, past[1])):
+        x[table[0, :7].long()] = y.reshape(hkv, 7, 16, d).transpose(0, 1)
+    g = torch.Generator().manual_seed(5)
+    q, k, v = (torch.randn(n, h, d, generator=g).to(dtype).cuda() for h in (hkv, hkv, hkv))
+    i32 = dict(dtype=torch.int32, device="cuda")
+    prefix, offs, new, status = torch.tensor([P], **i32), torch.tensor([0, n], **i32), torch.zeros(1, **i32), torch.zeros(4, **i32)
+    desc = tv.make_desc(batch=1, num_q_heads=hkv, num_kv_heads=hkv, head_dim=d, max_nodes=1, total_rows=1, capacity=176,
+                        dtype=tv.BF16 if dtype == torch.bfloat16 else tv.F32, max_prefix=P, page_size=16, num_pages=pages)
+    kr, vr = (torch.empty(hkv, n, d, dtype=dtype, device="cuda") for _ in range(2))
+    tv.tv_prompt_rope_store(desc, n, n, 1e4, q, k, v, prefix, offs, q, kr, vr, k_cache, v_cache, table, new, status)
+    out = torch.empty_like(q)
+    size = tv.tv_prompt_workspace_size(desc, n, n)
+    ws = torch.empty(max(size, 256), dtype=torch.uint8, device="cuda")
+    tv.tv_prompt_attn(desc, n, n, q, k_cache, v_cache, table, prefix, offs, kr, vr, out, ws, size, status)
+    torch.cuda.synchronize()
+    assert int(status[0]) == 0 and int(new[0]) == P + n
+    for x, rows in ((k_cache, kr), (v_cache, vr)):
+        assert torch.equal(x[table[0].long()].transpose(0, 1).flatten(1, 2)[:, P:P + n], rows)
+    f = lambda x: x.double().cpu().numpy()
+    bf16 = dtype == torch.bfloat16
+    ref, lim = reference(f(q), f(past[0][:, :P]), f(past[1][:, :P]), f(kr), f(vr), d ** -0.5, bf16, not bf16)
+    assert (np.abs(f(out) - ref) <= lim).all()
