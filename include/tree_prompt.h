@@ -35,8 +35,9 @@
  * Conventions are those of tree_verify.h: the caller's buffers, 16-byte
  * aligned device pointers, host errors before anything is enqueued, device
  * faults OR-ed into *d_status, nothing allocated or synchronised,
- * deterministic results.  rows = 0 or max_rows = 0 enqueues nothing (the
- * pointers are then not looked at).
+ * deterministic results.  rows = 0 or max_rows = 0 enqueues nothing: the
+ * pointers are then not looked at, and no output is written, the new lengths
+ * neither.
  *
  * Device faults of both calls: where a sequence's offsets are invalid
  * (TV_DEV_BAD_OFFSETS) it is skipped, and what the call leaves in the outputs of

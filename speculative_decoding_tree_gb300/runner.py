@@ -329,6 +329,10 @@ class DevicePrompt:
 
     def rope_store(self, q, k, v, stream=None):
         st = self.step
+        if self.rows == 0:                               # the call would enqueue nothing, the lengths neither
+            with _on(stream):
+                self.new_prefix.copy_(st.prefix_len)
+            return
         tv_prompt_rope_store(self.desc, self.rows, self.max_rows, self.theta, q, k, v, st.prefix_len, self.offsets,
                              self.q, self.k_rows, self.v_rows, st.k_cache, st.v_cache, st.page_table, self.new_prefix,
                              st.status, stream)

@@ -1,0 +1,40 @@
+"""What DevicePrompt, LogitControl and the command do around the library's calls
+(CPU: the calls enqueue nothing, or stand-ins record them)."""
+from types import SimpleNamespace
+
+import pytest
+import torch
+
+import speculative_decoding_tree_gb300 as tv
+from speculative_decoding_tree_gb300 import _build, runner
+
+P0 = [3, 0, 17]
+
+
+@pytest.fixture(autouse=True)
+def no_gpu(monkeypatch):
+    _build.build()
+    monkeypatch.setattr(tv, "_current_stream", lambda: 0)
+
+
+def step(**kw):
+    """What DevicePrompt and LogitControl look at of a step, on the CPU."""
+    B = len(P0)
+    desc = tv.make_desc(batch=B, num_q_heads=4, num_kv_heads=2, head_dim=128, dtype=tv.BF16, max_nodes=4, total_rows=6,
+                        capacity=64, max_prefix=20)
+    bf = dict(dtype=torch.bfloat16)
+    base = dict(desc=desc, device=torch.device("cpu"), vocab=50, logits_dtype=tv.F32, page_table=None,
+                q=torch.zeros(6, 4, 128, **bf), out=torch.zeros(6, 4, 128, **bf), k_cache=torch.zeros(B, 2, 64, 128, **bf),
+                v_cache=torch.zeros(B, 2, 64, 128, **bf), prefix_len=torch.tensor(P0, dtype=torch.int32),
+                status=torch.zeros(4, dtype=torch.int32), tokens=torch.zeros(B, 4, dtype=torch.int32),
+                logits=torch.zeros(6, 50))
+    return SimpleNamespace(**{**base, **kw})
+
+
+def test_empty_prompts_leave_the_lengths():
+    st = step()
+    pr = runner.DevicePrompt(st, [0, 0, 0])
+    pr.new_prefix.fill_(-77)                             # as uninitialised memory may be
+    none = torch.zeros(0, 4, 128, dtype=torch.bfloat16)
+    pr.run(none, none[:, :2], none[:, :2])
+    assert st.prefix_len.tolist() == P0 and pr.new_prefix.tolist() == P0
