@@ -460,7 +460,8 @@ def main(argv=None):
                          argmax_fn=lambda x: torch.argmax(x.float(), dim=1))   # plants the draft tokens
     win = tuple(int(x) for x in a.window.split(",")) if a.window else None
     st = DeviceKv4Step(w, win) if a.kv4 else (DeviceWindowStep(w, *win) if win else DeviceStep(w))
-    target = st.logits.float().argmax(1).to(torch.int32) if a.kv4 else None
+    argmax = lambda: st.logits.float().argmax(1).to(torch.int32)
+    target = argmax() if a.kv4 else None
     p0 = st.prefix_len.clone()
     prompt = control = None
     if a.prompt:                                 # rows of noise, into positions the workload's prefix holds after it
@@ -486,7 +487,7 @@ def main(argv=None):
             st.attn()
             st.accept_commit_sampled(a.sampled, 1234, _)
         elif a.kv4:
-            st.step(target)
+            st.step(argmax() if control else target)
         else:
             st.step()
         if control and not a.attn_only:

@@ -38,3 +38,53 @@ def test_empty_prompts_leave_the_lengths():
     none = torch.zeros(0, 4, 128, dtype=torch.bfloat16)
     pr.run(none, none[:, :2], none[:, :2])
     assert st.prefix_len.tolist() == P0 and pr.new_prefix.tolist() == P0
+
+
+class Recorder(SimpleNamespace):
+    """A step of the command on the CPU: `seen` has the logits that acceptance went by, step by step."""
+
+    def __init__(self, w, *_):
+        super().__init__(**vars(step()), seen=[])
+        self.logits = torch.arange(300.0).reshape(6, 50) % 7
+        self.mask = self.attn = lambda *_: None
+        made.append(self)
+
+    def step(self, argmax=None):
+        self.seen.append(self.logits.clone() if argmax is None else argmax)
+
+
+class AddOne:
+    """A control that adds 10 to token 3 of every row."""
+
+    def __init__(self, st, *_, **__):
+        self.st = st
+        self.process = lambda: st.logits[:, 3].add_(10)
+
+    def __getattr__(self, name):
+        return lambda *_: None
+
+
+made = []
+
+
+@pytest.fixture
+def command(monkeypatch):
+    for name in ("DeviceStep", "DeviceKv4Step"):
+        monkeypatch.setattr(runner, name, Recorder)
+    monkeypatch.setattr(runner, "LogitControl", AddOne)
+    monkeypatch.setattr(torch.cuda, "synchronize", lambda: None)
+
+    def run(*args):
+        made.clear()
+        assert runner.main(["--config", "1", *args]) == 0
+        return made[0]
+    return run
+
+
+def test_the_4_bit_step_accepts_on_steered_logits(command):
+    raw = torch.arange(300.0).reshape(6, 50) % 7
+    steered = raw.clone()
+    steered[:, 3] += 10
+    st = command("--kv4", "--steps", "1", "--steer")
+    assert st.seen[0].dtype == torch.int32 and st.seen[0].tolist() == [3] * 6
+    assert command("--kv4", "--steps", "1").seen[0].tolist() == raw.argmax(1).tolist()
