@@ -471,12 +471,14 @@ def main(argv=None):
                 for h in (st.desc.num_q_heads, st.desc.num_kv_heads, st.desc.num_kv_heads)]
     if a.steer:
         control = LogitControl(st, torch.tensor([[1.1, 0.1, 0.1]] * st.desc.batch, device=st.device))
+        raw = st.logits.clone()                  # the target's logits are the same every step
     for _ in range(a.steps):
         if prompt:
             st.prefix_len.zero_()
             prompt.run(*rows)
         st.prefix_len.copy_(p0)
         if control:
+            st.logits.copy_(raw)
             st.mask()
             control.process()
         if a.attn_only:

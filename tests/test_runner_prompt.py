@@ -88,3 +88,12 @@ def test_the_4_bit_step_accepts_on_steered_logits(command):
     st = command("--kv4", "--steps", "1", "--steer")
     assert st.seen[0].dtype == torch.int32 and st.seen[0].tolist() == [3] * 6
     assert command("--kv4", "--steps", "1").seen[0].tolist() == raw.argmax(1).tolist()
+
+
+@pytest.mark.parametrize("kind", [(), ("--kv4",)])
+def test_every_step_steers_the_targets_logits(command, kind):
+    raw = torch.arange(300.0).reshape(6, 50) % 7
+    raw[:, 3] += 10
+    st = command(*kind, "--steps", "3", "--steer")
+    want = torch.full((6,), 3, dtype=torch.int32) if kind else raw
+    assert len(st.seen) == 3 and all(torch.equal(x, want) for x in st.seen) and torch.equal(st.logits, raw)
