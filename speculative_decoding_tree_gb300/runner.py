@@ -371,6 +371,14 @@ class LogitControl:
         """The prompts' tokens (packed, int32)."""
         tv_token_counts_add(self.desc, tokens, offsets, tokens.numel(), True, self.counts, self.step.status, stream)
 
+    def started(self, stream=None):
+        """The roots of the step's trees, as emitted.  Once, before a sequence's
+        first step: a later root is the last token that emitted() counted."""
+        st = self.step
+        with _on(stream):                                # the tokens live and die on the call's stream
+            roots = st.draft[st.node_offsets[:-1].long()]
+            tv_token_counts_add(self.desc, roots, None, 1, False, self.counts, st.status, stream)
+
     def emitted(self, stream=None):
         """What the step's accept + commit emitted."""
         st = self.step
@@ -471,6 +479,7 @@ def main(argv=None):
                 for h in (st.desc.num_q_heads, st.desc.num_kv_heads, st.desc.num_kv_heads)]
     if a.steer:
         control = LogitControl(st, torch.tensor([[1.1, 0.1, 0.1]] * st.desc.batch, device=st.device))
+        control.started()
         raw = st.logits.clone()                  # the target's logits are the same every step
     for _ in range(a.steps):
         if prompt:

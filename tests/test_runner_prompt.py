@@ -97,3 +97,11 @@ def test_every_step_steers_the_targets_logits(command, kind):
     st = command(*kind, "--steps", "3", "--steer")
     want = torch.full((6,), 3, dtype=torch.int32) if kind else raw
     assert len(st.seen) == 3 and all(torch.equal(x, want) for x in st.seen) and torch.equal(st.logits, raw)
+
+
+def test_first_roots_are_counted_as_emitted(monkeypatch):
+    calls = []
+    monkeypatch.setattr(runner, "tv_token_counts_add", lambda d, t, o, n, prompt, *_: calls.append((t.tolist(), o, n, prompt)))
+    st = step(draft=torch.tensor([9, 1, 4, 30, 31, 8], dtype=torch.int32), node_offsets=torch.tensor([0, 2, 3, 6], dtype=torch.int32))
+    runner.LogitControl(st, torch.ones(3, 3)).started()
+    assert calls == [([9, 4, 30], None, 1, False)]
