@@ -304,12 +304,19 @@ class DevicePrompt:
     new rows of sequence b behind what is committed.  run() rotates the rows,
     writes their keys and values into the cache, attends to prefix and rows, and
     moves the step's prefix lengths on.  max_prefix: a bound on what is committed
-    before (the step's own if None)."""
+    before (the step's own if None).  A windowed step's prompts have to fit the
+    window, where rows see all that is before them; a 4-bit step's go through
+    its append."""
 
     def __init__(self, step, lens, theta=1e4, max_prefix=None):
+        if isinstance(step, DeviceKv4Step):
+            raise NotImplementedError("prompts into the 4-bit cache have no DevicePrompt: use DeviceKv4Step.append")
         d, dev = step.desc, step.device
         max_prefix = d.max_prefix if max_prefix is None else int(max_prefix)
         self.step, self.theta, self.rows, self.max_rows = step, theta, sum(lens), max(lens)
+        if isinstance(step, DeviceWindowStep) and step.win.window < max_prefix + self.max_rows:
+            raise NotImplementedError(f"rows at positions up to {max_prefix + self.max_rows - 1} do not see the window of "
+                                      f"{step.win.window} alone: the prompt attention has no window")
         self.desc = make_desc(batch=d.batch, num_q_heads=d.num_q_heads, num_kv_heads=d.num_kv_heads,
                               head_dim=d.head_dim, dtype=d.dtype, max_nodes=1, total_rows=d.batch,
                               capacity=d.capacity, max_prefix=max_prefix, page_size=d.page_size,
@@ -445,6 +452,8 @@ def main(argv=None):
         ap.error("--sampled: the 4-bit cache is committed on a given argmax only")
     if a.kv4 and a.prompt:
         ap.error("--prompt: prompts into the 4-bit cache go through its append")
+    if a.window and a.prompt:
+        ap.error("--prompt: the prompt attention has no window")
     _build.build()
     if a.lm_head:
         spec = wl.LMHEAD_CONFIGS[a.lm_head]

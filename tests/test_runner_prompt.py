@@ -105,3 +105,23 @@ def test_first_roots_are_counted_as_emitted(monkeypatch):
     st = step(draft=torch.tensor([9, 1, 4, 30, 31, 8], dtype=torch.int32), node_offsets=torch.tensor([0, 2, 3, 6], dtype=torch.int32))
     runner.LogitControl(st, torch.ones(3, 3)).started()
     assert calls == [([9, 4, 30], None, 1, False)]
+
+
+def test_windowed_prompts_are_refused():
+    st = runner.DeviceWindowStep.__new__(runner.DeviceWindowStep)
+    vars(st).update(vars(step()), win=tv.make_window(30, 4))
+    with pytest.raises(NotImplementedError, match="window"):
+        runner.DevicePrompt(st, [5, 11, 0])                  # positions up to 20 + 10
+    assert runner.DevicePrompt(st, [5, 10, 0]).rows == 15   # 29 is the last that sees everything
+    assert runner.DevicePrompt(st, [30, 1, 0], max_prefix=0).rows == 31
+
+
+def test_prompts_of_4_bit_steps_are_refused():
+    with pytest.raises(NotImplementedError, match="append"):
+        runner.DevicePrompt(runner.DeviceKv4Step.__new__(runner.DeviceKv4Step), [5])
+
+
+def test_command_refuses_windowed_prompts(capsys):
+    with pytest.raises(SystemExit) as e:
+        runner.main(["--window", "64,4", "--prompt", "5"])
+    assert e.value.code == 2 and "--prompt" in capsys.readouterr().err
