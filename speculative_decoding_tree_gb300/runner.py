@@ -34,10 +34,12 @@ def _on(stream):
 
 
 def _keep(stream, *tensors):
-    """The tensors' memory is not given on before `stream` has passed this point."""
+    """The tensors' memory is not given on before `stream` has passed this point
+    (None and addresses: nothing of torch's to keep)."""
     if stream is not None:
         for t in tensors:
-            t.record_stream(_torch_stream(stream))
+            if isinstance(t, torch.Tensor):
+                t.record_stream(_torch_stream(stream))
 
 
 class DeviceStep:
@@ -306,7 +308,9 @@ class DevicePrompt:
     moves the step's prefix lengths on.  max_prefix: a bound on what is committed
     before (the step's own if None).  A windowed step's prompts have to fit the
     window, where rows see all that is before them; a 4-bit step's go through
-    its append."""
+    its append.  With a stream, a call keeps the inputs and this object's buffers
+    from reuse until the stream has passed it; that it runs after what made them
+    is the caller's."""
 
     def __init__(self, step, lens, theta=1e4, max_prefix=None):
         if isinstance(step, DeviceKv4Step):
@@ -315,8 +319,8 @@ class DevicePrompt:
         max_prefix = d.max_prefix if max_prefix is None else int(max_prefix)
         self.step, self.theta, self.rows, self.max_rows = step, theta, sum(lens), max(lens)
         if isinstance(step, DeviceWindowStep) and step.win.window < max_prefix + self.max_rows:
-            raise NotImplementedError(f"rows at positions up to {max_prefix + self.max_rows - 1} do not see the window of "
-                                      f"{step.win.window} alone: the prompt attention has no window")
+            raise NotImplementedError(f"rows at positions up to {max_prefix + self.max_rows - 1} in a window of "
+                                      f"{step.win.window}: the prompt attention has no window")
         self.desc = make_desc(batch=d.batch, num_q_heads=d.num_q_heads, num_kv_heads=d.num_kv_heads,
                               head_dim=d.head_dim, dtype=d.dtype, max_nodes=1, total_rows=d.batch,
                               capacity=d.capacity, max_prefix=max_prefix, page_size=d.page_size,
@@ -336,6 +340,7 @@ class DevicePrompt:
 
     def rope_store(self, q, k, v, stream=None):
         st = self.step
+        _keep(stream, q, k, v, self.q, self.k_rows, self.v_rows, self.offsets, self.new_prefix)
         if self.rows == 0:                               # the call would enqueue nothing, the lengths neither
             with _on(stream):
                 self.new_prefix.copy_(st.prefix_len)
@@ -346,6 +351,7 @@ class DevicePrompt:
 
     def attn(self, stream=None):
         st = self.step
+        _keep(stream, self.q, self.k_rows, self.v_rows, self.offsets, self.out, self.workspace)
         tv_prompt_attn(self.desc, self.rows, self.max_rows, self.q, st.k_cache, st.v_cache, st.page_table,
                        st.prefix_len, self.offsets, self.k_rows, self.v_rows, self.out, self.workspace, self.ws_bytes,
                        st.status, stream)
@@ -362,7 +368,7 @@ class LogitControl:
     """Penalties, biases and grammar masks on a step's logits, with the token
     counts they go by.  penalties [B, 3] float (repetition, frequency,
     presence); biases: (offsets, tokens, values) or None; mask [rows, words]
-    int32 or None."""
+    int32 or None.  Streams are as DevicePrompt takes them."""
 
     def __init__(self, step, penalties, biases=None, mask=None):
         B = step.desc.batch
@@ -377,6 +383,7 @@ class LogitControl:
     def read(self, tokens, offsets, stream=None):
         """The prompts' tokens (packed, int32)."""
         tv_token_counts_add(self.desc, tokens, offsets, tokens.numel(), True, self.counts, self.step.status, stream)
+        _keep(stream, tokens, offsets, self.counts)
 
     def started(self, stream=None):
         """The roots of the step's trees, as emitted.  Once, before a sequence's
@@ -385,17 +392,20 @@ class LogitControl:
         with _on(stream):                                # the tokens live and die on the call's stream
             roots = st.draft[st.node_offsets[:-1].long()]
             tv_token_counts_add(self.desc, roots, None, 1, False, self.counts, st.status, stream)
+        _keep(stream, self.counts)
 
     def emitted(self, stream=None):
         """What the step's accept + commit emitted."""
         st = self.step
         tv_token_counts_add(self.desc, st.tokens, None, st.desc.max_nodes, False, self.counts, st.status, stream)
+        _keep(stream, self.counts)
 
     def process(self, stream=None):
         """The step's logits, in place (after its mask call)."""
         st = self.step
         tv_tree_logits_process(self.desc, st.logits, self.counts, self.penalties, *self.biases, self.mask, st.draft,
                                st.node_offsets, st.anc, st.logits, st.status, stream)
+        _keep(stream, self.counts, self.penalties, self.mask, *self.biases)
 
 
 class DeviceLmHead:

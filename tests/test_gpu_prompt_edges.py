@@ -58,3 +58,48 @@ def test_a_trees_first_row_is_steered_like_plain_decoding(side):
             got = st.logits[o0 + i].double().cpu().numpy()
             # five fp32 roundings of values below 2^5, then the type's half step
             assert (np.abs(got - want) <= half * np.abs(want) + 5 * 2.0 ** -19).all()
+
+
+def busy():
+    """Allocations of every small size on the current stream, filled: memory that was given back is written again."""
+    keep = [torch.full((n,), 2 ** 30 + 7, dtype=torch.int32, device="cuda") for n in [5] * 64 + [128] * 64]
+    return keep + [torch.full((60, h, 128), 9.0, dtype=torch.bfloat16, device="cuda") for h in [4] * 16 + [2] * 16]
+
+
+@pytest.mark.parametrize("kind", ["stream", "address"])
+def test_chunks_on_a_side_stream(kind):
+    """Prompts, their rows and their tokens are let go of while the stream has yet to read them."""
+    lens = [20, 31, 9]
+
+    def chunk(st, ctl, arg):
+        g = torch.Generator("cuda").manual_seed(4)
+        rows = [torch.randn(60, h, 128, generator=g, device="cuda").to(torch.bfloat16) for h in (4, 2, 2)]
+        said = torch.randint(0, st.vocab, (60,), generator=g, device="cuda").int()
+        offs = torch.tensor([0, 20, 51, 60], dtype=torch.int32, device="cuda")
+        pr = runner.DevicePrompt(st, lens, max_prefix=0)
+        if arg is not None:
+            side.wait_stream(torch.cuda.current_stream())
+        pr.run(*rows, arg)
+        ctl.read(said, offs, arg)
+        return pr.out
+
+    results = []
+    side = torch.cuda.Stream()
+    for arg in (None, side if kind == "stream" else side.cuda_stream):
+        w, st = tree_step(paged=True)
+        ctl = runner.LogitControl(st, torch.ones(3, 3, device="cuda"))
+        st.prefix_len.zero_()
+        torch.cuda.synchronize()
+        if arg is not None:
+            with torch.cuda.stream(side):
+                torch.cuda._sleep(20_000_000)            # the calls run well after they were made
+        out = chunk(st, ctl, arg)
+        keep = busy()
+        torch.cuda.synchronize()
+        assert int(st.status[0]) == 0 and st.prefix_len.tolist() == lens
+        caches = [torch.cat([x[st.page_table[b].long()].transpose(0, 1).flatten(1, 2)[:, :n] for b, n in enumerate(lens)], 1)
+                  for x in (st.k_cache, st.v_cache)]
+        results.append([out.clone(), ctl.counts.clone(), *caches])
+        del keep
+    for x, y in zip(*results):
+        assert torch.equal(x, y)

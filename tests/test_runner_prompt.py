@@ -125,3 +125,28 @@ def test_command_refuses_windowed_prompts(capsys):
     with pytest.raises(SystemExit) as e:
         runner.main(["--window", "64,4", "--prompt", "5"])
     assert e.value.code == 2 and "--prompt" in capsys.readouterr().err
+
+
+def test_calls_on_a_stream_keep_what_they_use(monkeypatch):
+    """Every tensor a call hands to the library that is not the step's own is kept until the stream has passed."""
+    step_own, handed, kept = set(), set(), set()
+    ids = lambda xs: {x.data_ptr() for x in xs if isinstance(x, torch.Tensor) and x.numel()}
+    for name in ("tv_prompt_rope_store", "tv_prompt_attn", "tv_token_counts_add", "tv_tree_logits_process"):
+        monkeypatch.setattr(runner, name, lambda *a: handed.update(ids(a)))
+    monkeypatch.setattr(runner, "_keep", lambda stream, *t: kept.update(ids(t)) if stream is not None else None)
+    monkeypatch.setattr(runner, "_on", lambda stream: runner.contextlib.nullcontext())
+    i32 = dict(dtype=torch.int32)
+    st = step(draft=torch.zeros(6, **i32), node_offsets=torch.tensor([0, 2, 3, 6], **i32), anc=torch.zeros(6, dtype=torch.int64))
+    step_own = ids(vars(st).values())
+    pr = runner.DevicePrompt(st, [5, 3, 0])
+    bias = (torch.zeros(4, **i32), torch.zeros(2, **i32), torch.zeros(2))
+    ctl = runner.LogitControl(st, torch.ones(3, 3), bias, torch.zeros(6, 2, **i32))
+    tokens, offsets = torch.zeros(8, **i32), torch.tensor([0, 5, 8, 8], **i32)
+    rows = [torch.zeros(8, h, 128, dtype=torch.bfloat16) for h in (4, 2, 2)]
+    calls = [lambda: pr.rope_store(*rows, 7), lambda: pr.attn(7), lambda: pr.run(*rows, 7), lambda: ctl.process(7),
+             lambda: ctl.read(tokens, offsets, 7), lambda: ctl.emitted(7)]
+    for call in calls:
+        handed.clear()
+        kept.clear()
+        call()
+        assert handed - step_own and not handed - step_own - kept
