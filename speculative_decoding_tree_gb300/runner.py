@@ -316,6 +316,8 @@ class DevicePrompt:
         if isinstance(step, DeviceKv4Step):
             raise NotImplementedError("prompts into the 4-bit cache have no DevicePrompt: use DeviceKv4Step.append")
         d, dev = step.desc, step.device
+        if len(lens) != d.batch or min(lens) < 0:
+            raise ValueError(f"lens: {d.batch} sequences want a number of rows each, 0 or more, not {list(lens)}")
         max_prefix = d.max_prefix if max_prefix is None else int(max_prefix)
         self.step, self.theta, self.rows, self.max_rows = step, theta, sum(lens), max(lens)
         if isinstance(step, DeviceWindowStep) and step.win.window < max_prefix + self.max_rows:

@@ -150,3 +150,10 @@ def test_calls_on_a_stream_keep_what_they_use(monkeypatch):
         kept.clear()
         call()
         assert handed - step_own and not handed - step_own - kept
+
+
+@pytest.mark.parametrize("lens", [[], [4, 5], [1, 2, 3, 4], [3, -1, 2]])
+def test_one_length_a_sequence(lens):
+    """Fewer lengths would make offsets that end before the last sequence's."""
+    with pytest.raises(ValueError, match="lens"):
+        runner.DevicePrompt(step(), lens)
