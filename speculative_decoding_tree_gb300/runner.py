@@ -376,6 +376,8 @@ class LogitControl:
         B = step.desc.batch
         self.step, self.mask = step, mask
         self.penalties = penalties
+        if biases is not None and biases[1].numel() == 0:
+            biases = None                                # an empty tensor has no address for the call
         self.biases = (None, None, None) if biases is None else biases
         self.counts = torch.zeros(B, (step.vocab + 7) // 8 * 8, dtype=torch.int16, device=step.device)
         self.desc = make_logits_desc(batch=B, vocab=step.vocab, max_nodes=step.desc.max_nodes,

@@ -157,3 +157,13 @@ def test_one_length_a_sequence(lens):
     """Fewer lengths would make offsets that end before the last sequence's."""
     with pytest.raises(ValueError, match="lens"):
         runner.DevicePrompt(step(), lens)
+
+
+def test_an_empty_bias_list_is_no_bias(monkeypatch):
+    calls = []
+    monkeypatch.setattr(runner, "tv_tree_logits_process", lambda *a: calls.append(a))
+    i32 = dict(dtype=torch.int32)
+    st = step(draft=torch.zeros(6, **i32), node_offsets=torch.tensor([0, 2, 3, 6], **i32), anc=torch.zeros(6, dtype=torch.int64))
+    ctl = runner.LogitControl(st, torch.ones(3, 3), (torch.zeros(4, **i32), torch.zeros(0, **i32), torch.zeros(0)))
+    ctl.process()
+    assert ctl.desc.biases == 0 and calls[0][4:7] == (None, None, None)
