@@ -66,6 +66,24 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatil
   }
 }
 
+// mbar_wait for a copy that the caller's exit would leave under way: where the
+// wait is given up, the copy is waited for all the same, with a limit of its
+// own, so that it does not land in a CTA that has left.
+__device__ __forceinline__ bool mbar_wait_landed(uint32_t bar, uint32_t parity, volatile int* abort_flag,
+                                                 uint64_t limit_ns) {
+  if (mbar_wait(bar, parity, abort_flag, limit_ns)) return true;
+  int spare = 0;
+  mbar_wait(bar, parity, &spare, limit_ns);
+  return false;
+}
+
+// The time of a wait, for copies that no barrier of this CTA counts.
+__device__ __forceinline__ void wait_ns(uint64_t limit_ns) {
+  const uint64_t t0 = globaltimer_ns();
+  while (globaltimer_ns() - t0 < limit_ns) {
+  }
+}
+
 // mbar_wait with a suspend-time hint of 1 ms: the thread sleeps in the
 // instruction instead of polling, which matters where many warps wait beside
 // warps that compute

@@ -358,7 +358,7 @@ tv_attn_tc2_kernel(const __grid_constant__ AttnParams p, const __grid_constant__
         __syncwarp();
         if (tail_fix) {
           // this CTA's rows past the end become zeros before any MMA reads them
-          if (!__all_sync(kAll, mbar_wait(TAIL, tail_uses & 1, abort_flag, kWaitNs))) {
+          if (!__all_sync(kAll, mbar_wait_landed(TAIL, tail_uses & 1, abort_flag, kWaitNs))) {
             ok = false;
             break;
           }
@@ -378,7 +378,9 @@ tv_attn_tc2_kernel(const __grid_constant__ AttnParams p, const __grid_constant__
     }
     // drain: the copies of both CTAs (the leader's barriers count them) have
     // landed before the pair's last barrier, after a timeout too (abort_flag is
-    // up then, and these waits have their own)
+    // up then, and these waits have their own; a step that the leader no longer
+    // counts gets the time of a wait in the peer)
+    if (lane == 0 && !leader && !ok) wait_ns(kWaitNs);
     if (lane == 0 && leader) {
       int spare = 0;
       mbar_wait(Q_FULL, 0, &spare, kWaitNs);

@@ -350,7 +350,7 @@ tv_attn_tcp_kernel(const __grid_constant__ AttnParams p, const __grid_constant__
           __syncwarp();
           if (tail_fix) {
             // the chunk's rows past the end become zeros before the MMA reads them
-            if (!__all_sync(kAll, mbar_wait(TAIL, tail_uses & 1, abort_flag, kWaitNs))) {
+            if (!__all_sync(kAll, mbar_wait_landed(TAIL, tail_uses & 1, abort_flag, kWaitNs))) {
               ok = false;
               break;
             }

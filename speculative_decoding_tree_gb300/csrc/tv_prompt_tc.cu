@@ -207,7 +207,7 @@ prompt_tc_kernel(const __grid_constant__ PromptParams p, const __grid_constant__
         }
         __syncwarp();
         if (fix) {
-          if (!__all_sync(kAll, mbar_wait(TAIL, tail_uses & 1, abort_flag, kWaitNs))) {
+          if (!__all_sync(kAll, mbar_wait_landed(TAIL, tail_uses & 1, abort_flag, kWaitNs))) {
             ok = false;
             break;
           }

@@ -270,7 +270,7 @@ prompt_tc2_kernel(const __grid_constant__ PromptParams p, const __grid_constant_
         }
         __syncwarp();
         if (fix) {
-          if (!__all_sync(kAll, mbar_wait(TAIL, tail_uses & 1, abort_flag, kWaitNs))) {
+          if (!__all_sync(kAll, mbar_wait_landed(TAIL, tail_uses & 1, abort_flag, kWaitNs))) {
             ok = false;
             break;
           }
@@ -290,7 +290,8 @@ prompt_tc2_kernel(const __grid_constant__ PromptParams p, const __grid_constant_
       }
     }
     // drain: the copies of both CTAs (the leader's barriers count them) have landed before the pair's last barrier,
-    // after a timeout too
+    // after a timeout too: a step that the leader no longer counts gets the time of a wait in the peer
+    if (lane == 0 && !leader && !ok) wait_ns(kWaitNs);
     if (lane == 0 && leader) {
       int spare = 0;
       mbar_wait(Q_FULL, 0, &spare, kWaitNs);
