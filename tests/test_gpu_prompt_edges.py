@@ -6,7 +6,7 @@ import torch
 
 import speculative_decoding_tree_gb300 as tv
 from gpu_helpers import workload
-from oracle import logits as ol
+from oracle import logits as ol, prompt as op
 from prompt_helpers import Prompts, reference
 from speculative_decoding_tree_gb300 import runner, workloads as wl
 
@@ -103,3 +103,104 @@ def test_chunks_on_a_side_stream(kind):
         del keep
     for x, y in zip(*results):
         assert torch.equal(x, y)
+
+
+@pytest.mark.parametrize("d,hq,hkv", [(128, 4, 1), (256, 2, 1), (512, 2, 1)])
+def test_a_score_of_minus_infinity_has_no_weight(d, hq, hkv):
+    """bf16: a key of -inf against queries above 0 is seen and weighs nothing, in the prefix and among the rows."""
+    c = Prompts([150], [200], hq, hkv, d, "bf16", seed=12)
+    c.q.abs_()
+    c.q[c.q == 0] = 1
+    inf = float("-inf")
+    c.k_rows[:, 60] = c.k_rows[:, 130] = inf
+    c.past[0][0][:, 7] = inf
+    c.k_cache[0, :, 7] = inf
+    for x, y in zip(c.gpu, (c.q, c.k_rows, c.v_rows)):
+        x.copy_(y)
+    c.attn()
+    torch.cuda.synchronize()
+    assert int(c.status[0]) == 0
+    q, kp, vp, kr, vr = c.seq(0)
+    got = c.out.double().cpu().numpy()
+    gone = [60, 130]
+    for a, b in ((0, 60), (60, 130), (130, 200)):            # rows a .. b - 1 see the same rows of -inf
+        keep = np.array([i for i in range(b) if i not in gone])
+        live = np.array([i for i in range(a, b) if i not in gone])
+        rows = np.concatenate([np.searchsorted(keep, live)])
+        ref, lim = reference(q[keep], np.delete(kp, 7, 1), np.delete(vp, 7, 1), kr[:, keep], vr[:, keep], c.scale, True, False)
+        assert (np.abs(got[live] - ref[rows]) <= lim[rows]).all()
+    # the rows of -inf themselves see the others
+    for i in gone:
+        keep = np.array([j for j in range(i) if j not in gone])
+        one = op.attention(q[i:i + 1], np.concatenate([np.delete(kp, 7, 1), kr[:, keep[:-1]]], 1),
+                           np.concatenate([np.delete(vp, 7, 1), vr[:, keep[:-1]]], 1), kr[:, keep[-1:]], vr[:, keep[-1:]], c.scale)
+        assert np.abs(got[i] - one[0]).max() <= 3 * 2.0 ** -8 * np.abs(vr).max()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("d,hq,hkv", [(128, 4, 1), (256, 2, 1), (512, 2, 1)])
+@pytest.mark.parametrize("bad", [float("inf"), float("-inf")])
+def test_infinite_keys_of_later_rows(d, hq, hkv, dtype, bad):
+    c = Prompts([30], [200], hq, hkv, d, dtype, seed=13)
+    c.k_rows[:, 150:] = bad
+    c.gpu[1].copy_(c.k_rows)
+    c.attn()
+    torch.cuda.synchronize()
+    q, kp, vp, kr, vr = c.seq(0)
+    ref, lim = reference(q[:150], kp, vp, kr[:, :150], vr[:, :150], c.scale, c.bf16, c.out_f32)
+    assert (np.abs(c.out[:150].double().cpu().numpy() - ref) <= lim).all()
+
+
+def steer(x, counts=None, pen=None, bias=None, mask=None, nodes=None):
+    """One sequence of rows without drafts on their paths, through the library."""
+    R, V = x.shape
+    i32 = dict(dtype=torch.int32, device="cuda")
+    T = 0 if bias is None else len(bias[0])
+    desc = tv.make_logits_desc(batch=1, vocab=V, max_nodes=R, total_rows=R, biases=T,
+                               logits_dtype=tv.BF16 if x.dtype == torch.bfloat16 else tv.F32)
+    to = lambda t: None if t is None else t.cuda()
+    bo = bt = bv = None
+    if T:
+        bo, bt, bv = torch.tensor([0, T], **i32), torch.tensor(bias[0], **i32), torch.tensor(bias[1], device="cuda")
+    out, status = torch.full_like(x, 5.0).cuda(), torch.zeros(4, **i32)
+    keep = [to(x), to(counts), to(pen), to(mask)]
+    tv.tv_tree_logits_process(desc, keep[0], keep[1], keep[2], bo, bt, bv, keep[3], None, torch.tensor([0, R], **i32), None,
+                              out, status)
+    torch.cuda.synchronize()
+    assert int(status[0]) == 0
+    return out.cpu()
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("V", [64, 4099, 8200])
+def test_logits_that_nothing_touches_keep_their_bits(V, dtype):
+    """Only counted, biased and masked tokens change; every other one is the input, bit for bit."""
+    g = torch.Generator().manual_seed(V)
+    x = (torch.randn(9, V, generator=g) * 3).to(dtype)
+    x[0, 1], x[1, 2], x[2, 0], x[3, 4] = float("nan"), float("inf"), float("-inf"), -0.0
+    bits = lambda t: t.view(torch.int16 if dtype == torch.bfloat16 else torch.int32)
+    assert torch.equal(bits(steer(x)), bits(x))
+    counts = torch.zeros(1, (V + 7) // 8 * 8, dtype=torch.int16)
+    counts[0, 7], counts[0, V - 1] = 3, -32768
+    pen = torch.tensor([[1.5, 0.25, 0.5]])
+    mask = torch.full((9, (V + 31) // 32), -1, dtype=torch.int32)
+    mask[:, 1] = ~(1 << 5)                                   # token 37
+    got = steer(x, counts, pen, ([11, 12], [2.0, -1.0]), mask)
+    touched = torch.zeros(V, dtype=torch.bool)
+    touched[torch.tensor([7, 11, 12, 37, V - 1])] = True
+    assert torch.equal(bits(got)[:, ~touched], bits(x)[:, ~touched])
+    assert (got[:, 37] == float("-inf")).all() and not torch.equal(got[:, 7], x[:, 7])
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_infinities_and_nan_of_touched_logits(dtype):
+    """NaN and +inf stay through penalties and biases, -inf too; forbidden ones become -inf whatever they are."""
+    x = torch.zeros(4, 96, dtype=dtype)
+    x[0, :], x[1, :], x[2, :], x[3, :] = float("nan"), float("inf"), float("-inf"), 2.0
+    counts = torch.zeros(1, 96, dtype=torch.int16)
+    counts[0, :32] = 2
+    mask = torch.tensor([[-1, -1, 0]] * 4, dtype=torch.int32)
+    got = steer(x, counts, torch.tensor([[2.0, 0.25, 0.5]]), (list(range(16, 48)), [1.0] * 32), mask).float()
+    assert torch.isnan(got[0, :64]).all() and (got[1, :64] == float("inf")).all()
+    assert (got[2] == float("-inf")).all() and (got[:, 64:] == float("-inf")).all()
+    assert got[3, :64].tolist() == [0.0] * 16 + [1.0] * 16 + [3.0] * 16 + [2.0] * 16
