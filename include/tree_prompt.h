@@ -80,7 +80,9 @@ int tv_prompt_rope_store(const tv_desc* desc, int64_t rows, int64_t max_rows, do
                          int32_t* d_status, void* stream);
 
 /* Bytes of scratch tv_prompt_attn needs (256-byte aligned; any contents; one
- * call at a time), and the plan it runs: kernel 6 tcgen05 with two query tiles a
+ * call at a time).  Few rows over many keys are split over the keys and many
+ * rows are not, so a smaller call may need more than a larger one: the size is
+ * that of these rows, max_rows and max_prefix alone.  And the plan it runs: kernel 6 tcgen05 with two query tiles a
  * CTA (bf16, head_dim 128), 7 tcgen05 on CTA pairs (bf16, 256 and 512), 8
  * tcgen05 on numbers in three bf16 parts (fp32; bf16 with more than 128 query
  * heads a KV head or a cache of 2^31 rows); chunk and num_splits count keys in
