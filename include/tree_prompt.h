@@ -61,7 +61,8 @@ extern "C" {
  *   d_k_cache, d_v_cache, position P_b + i, both or neither (NULL), with
  *   d_page_table when the cache is paged;
  *   d_new_prefix_len [B] or NULL: P_b + n_b, or d_prefix_len[b] as it was
- *   where the sequence is skipped.  It must not be d_prefix_len (TV_ERR_SHAPE).
+ *   where the sequence is skipped, or where the sum passes 2^31 - 1
+ *   (TV_DEV_CAPACITY).  It must not be d_prefix_len (TV_ERR_SHAPE).
  * d_q_in [rows, Hq, d], d_k_in and d_v_in [rows, Hkv, d].  No other buffers may
  * overlap.  With a cache, a sequence whose rows do not fit (P_b + n_b >
  * capacity: TV_DEV_CAPACITY) is skipped whole, and so is one whose prefix

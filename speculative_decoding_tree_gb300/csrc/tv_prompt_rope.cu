@@ -92,7 +92,11 @@ __global__ void __launch_bounds__(kThreads) prompt_rope_kernel(const __grid_cons
       int64_t o0, n, P;
       const bool ok = prompt_rows(p.row_offsets, b, p.rows, p.max_rows, p.status, &o0, &n) && n > 0 &&
                       rope_prefix(p, b, n, &P);
-      if (p.new_prefix_len) p.new_prefix_len[b] = ok ? (int)(P + n) : p.prefix_len[b];
+      const bool fits = ok && P + n <= INT32_MAX;   // (without a cache the rows may go further than a length can)
+      if (p.new_prefix_len) {
+        if (ok && !fits) set_status(p.status, TV_DEV_CAPACITY);
+        p.new_prefix_len[b] = fits ? (int)(P + n) : p.prefix_len[b];
+      }
     }
     return;
   }

@@ -204,3 +204,14 @@ def test_infinities_and_nan_of_touched_logits(dtype):
     assert torch.isnan(got[0, :64]).all() and (got[1, :64] == float("inf")).all()
     assert (got[2] == float("-inf")).all() and (got[:, 64:] == float("-inf")).all()
     assert got[3, :64].tolist() == [0.0] * 16 + [1.0] * 16 + [3.0] * 16 + [2.0] * 16
+
+
+def test_a_length_beyond_its_type_is_reported():
+    """Rows up to position 2^31 + 19 are rotated (no cache); the new length does not fit and stays."""
+    from test_gpu_prompt_rope import Rows
+    c = Rows([2 ** 31 - 100, 5], [120, 3], 2, 1, 128, "f32", cache=False, cap=2 ** 31 - 16, seed=2)
+    c.run(1e4)
+    assert int(c.status[0]) == 16 and c.new.tolist() == [2 ** 31 - 100, 8]
+    want = op.rotate(c.q.double().cpu().numpy(), op.positions(c.p, c.offs), 1e4)
+    # the fraction of a turn a position times is off by at most 2^-52 relative: 2^31 * 0.16 * 2^-52 turns
+    assert np.abs(c.q_out.double().cpu().numpy() - want).max() < 5e-6
