@@ -103,8 +103,9 @@ int tv_prompt_attn_plan(const tv_desc* desc, int64_t rows, int64_t max_rows, tv_
  * d_k_cache and d_v_cache may be NULL when max_prefix = 0.  The cache, q and
  * the rows are only read.  A row's answer does not depend on other sequences'
  * rows or on cache positions past its prefix; V of a later row of its own
- * sequence must be finite (a weight of 0 multiplies it).  A page id out of
- * range reads as zeros (TV_DEV_BAD_PAGE). */
+ * sequence must be finite (a weight of 0 multiplies it).  bf16: a score of -inf
+ * weighs nothing, and a row all of whose scores are -inf gives zeros.  A page id
+ * out of range reads as zeros (TV_DEV_BAD_PAGE). */
 int tv_prompt_attn(const tv_desc* desc, int64_t rows, int64_t max_rows, const void* d_q, const void* d_k_cache,
                    const void* d_v_cache, const int32_t* d_page_table, const int32_t* d_prefix_len,
                    const int32_t* d_row_offsets, const void* d_k_rows, const void* d_v_rows, void* d_out,

@@ -215,3 +215,19 @@ def test_a_length_beyond_its_type_is_reported():
     want = op.rotate(c.q.double().cpu().numpy(), op.positions(c.p, c.offs), 1e4)
     # the fraction of a turn a position times is off by at most 2^-52 relative: 2^31 * 0.16 * 2^-52 turns
     assert np.abs(c.q_out.double().cpu().numpy() - want).max() < 5e-6
+
+
+@pytest.mark.parametrize("p,n", [(0, 140), (2000, 3)])
+@pytest.mark.parametrize("d,hq,hkv", [(128, 4, 1), (256, 2, 1), (512, 2, 1)])
+def test_rows_of_minus_infinity_alone_are_zeros(d, hq, hkv, p, n):
+    """bf16, one key chunk and several: the rows before row 2 see scores of -inf alone."""
+    c = Prompts([p], [n], hq, hkv, d, "bf16", seed=14)
+    assert (c.plan()["num_splits"] > 1) == (p > 0)
+    c.gpu[0].fill_(1.0)
+    c.gpu[1][:, :2] = float("-inf")
+    c.k_cache[:, :, :p] = float("-inf")
+    c.attn()
+    torch.cuda.synchronize()
+    assert int(c.status[0]) == 0 and (c.out[:2] == 0).all()
+    # row 2 sees one key besides: its value, weight 1, rounded to bf16 from the product with 1 / 1
+    assert torch.equal(c.out[2], c.gpu[2][:, 2].repeat_interleave(hq // hkv, 0))
