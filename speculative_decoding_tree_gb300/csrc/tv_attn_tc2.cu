@@ -674,16 +674,6 @@ tv_attn_tc2_kernel(const __grid_constant__ AttnParams p, const __grid_constant__
 
 // ------------------------------------------------------------------ host
 
-bool encode2(CUtensorMap* m, const void* ptr, int rank, const cuuint64_t* dims, const cuuint64_t* strides,
-             const cuuint32_t* box, CUtensorMapDataType type = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16) {
-  EncodeTiledFn fn = encode_tiled_fn();
-  if (!fn) return false;
-  cuuint32_t es[3] = {1, 1, 1};
-  return fn(m, type, rank, const_cast<void*>(ptr), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
-            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) ==
-         CUDA_SUCCESS;
-}
-
 template <int D>
 cudaError_t launch_tc2_t(const AttnParams& p, cudaStream_t st) {
   CUtensorMap mq, mkc, mvc, mkt, mvt, mop;
@@ -692,7 +682,7 @@ cudaError_t launch_tc2_t(const AttnParams& p, cudaStream_t st) {
     cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)p.Hq, (cuuint64_t)p.R};
     cuuint64_t strides[2] = {row_bytes, row_bytes * p.Hq};
     cuuint32_t box[3] = {64, (cuuint32_t)p.G, (cuuint32_t)(BM / p.G)};
-    if (!encode2(&mq, p.q, 3, dims, strides, box)) return cudaErrorInvalidValue;
+    if (!encode_rows(&mq, p.q, 3, dims, strides, box)) return cudaErrorInvalidValue;
   }
   {
     const cuuint64_t rows = p.paged ? (cuuint64_t)p.num_pages * p.Hkv * kPageSize
@@ -701,7 +691,7 @@ cudaError_t launch_tc2_t(const AttnParams& p, cudaStream_t st) {
     cuuint64_t strides[1] = {row_bytes};
     cuuint32_t kbox[2] = {64, (cuuint32_t)(p.paged ? kPageSize : KH)};
     cuuint32_t vbox[2] = {64, (cuuint32_t)(p.paged ? kPageSize : BN)};
-    if (!encode2(&mkc, p.k_cache, 2, dims, strides, kbox) || !encode2(&mvc, p.v_cache, 2, dims, strides, vbox))
+    if (!encode_rows(&mkc, p.k_cache, 2, dims, strides, kbox) || !encode_rows(&mvc, p.v_cache, 2, dims, strides, vbox))
       return cudaErrorInvalidValue;
   }
   {
@@ -709,7 +699,7 @@ cudaError_t launch_tc2_t(const AttnParams& p, cudaStream_t st) {
     cuuint64_t strides[1] = {row_bytes};
     cuuint32_t kbox[2] = {64, KH};
     cuuint32_t vbox[2] = {64, BN};
-    if (!encode2(&mkt, p.k_tree, 2, dims, strides, kbox) || !encode2(&mvt, p.v_tree, 2, dims, strides, vbox))
+    if (!encode_rows(&mkt, p.k_tree, 2, dims, strides, kbox) || !encode_rows(&mvt, p.v_tree, 2, dims, strides, vbox))
       return cudaErrorInvalidValue;
   }
   {
@@ -720,8 +710,8 @@ cudaError_t launch_tc2_t(const AttnParams& p, cudaStream_t st) {
     cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)p.splits, rows};
     cuuint64_t strides[2] = {(cuuint64_t)D * es, (cuuint64_t)D * es * p.splits};
     cuuint32_t box[3] = {p.part_bf16 ? 64u : 32u, 1u, BM};
-    if (!encode2(&mop, p.o_part, 3, dims, strides, box,
-                 p.part_bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32))
+    if (!encode_rows(&mop, p.o_part, 3, dims, strides, box,
+                     p.part_bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32))
       return cudaErrorInvalidValue;
   }
   cudaError_t e = ensure_max_dynamic_smem<tv_attn_tc2_kernel<D>>((int)Cfg2<D>::SMEM);

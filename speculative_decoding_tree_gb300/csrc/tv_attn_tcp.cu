@@ -668,16 +668,6 @@ tv_attn_tcp_kernel(const __grid_constant__ AttnParams p, const __grid_constant__
 
 // ---------------------------------------------------------------- host
 
-bool encode_p(CUtensorMap* m, const void* ptr, int rank, const cuuint64_t* dims, const cuuint64_t* strides,
-              const cuuint32_t* box) {
-  EncodeTiledFn fn = encode_tiled_fn();
-  if (!fn) return false;
-  cuuint32_t es[3] = {1, 1, 1};
-  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank, const_cast<void*>(ptr), dims, strides, box, es,
-            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
 }  // namespace
 
 cudaError_t launch_attn_tcp(const AttnParams& p, cudaStream_t st) {
@@ -688,7 +678,7 @@ cudaError_t launch_attn_tcp(const AttnParams& p, cudaStream_t st) {
     cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)p.Hq, (cuuint64_t)p.R};
     cuuint64_t strides[2] = {row_bytes, row_bytes * p.Hq};
     cuuint32_t box[3] = {64, (cuuint32_t)p.G, (cuuint32_t)(BM / p.G)};
-    if (!encode_p(&mq, p.q, 3, dims, strides, box)) return cudaErrorInvalidValue;
+    if (!encode_rows(&mq, p.q, 3, dims, strides, box)) return cudaErrorInvalidValue;
   }
   {
     const cuuint64_t rows = p.paged ? (cuuint64_t)p.num_pages * p.Hkv * kPageSize
@@ -696,14 +686,14 @@ cudaError_t launch_attn_tcp(const AttnParams& p, cudaStream_t st) {
     cuuint64_t dims[2] = {(cuuint64_t)D, rows};
     cuuint64_t strides[1] = {row_bytes};
     cuuint32_t box[2] = {64, (cuuint32_t)(p.paged ? kPageSize : BN)};
-    if (!encode_p(&mkc, p.k_cache, 2, dims, strides, box) || !encode_p(&mvc, p.v_cache, 2, dims, strides, box))
+    if (!encode_rows(&mkc, p.k_cache, 2, dims, strides, box) || !encode_rows(&mvc, p.v_cache, 2, dims, strides, box))
       return cudaErrorInvalidValue;
   }
   {
     cuuint64_t dims[2] = {(cuuint64_t)D, (cuuint64_t)p.Hkv * p.R};
     cuuint64_t strides[1] = {row_bytes};
     cuuint32_t box[2] = {64, BN};
-    if (!encode_p(&mkt, p.k_tree, 2, dims, strides, box) || !encode_p(&mvt, p.v_tree, 2, dims, strides, box))
+    if (!encode_rows(&mkt, p.k_tree, 2, dims, strides, box) || !encode_rows(&mvt, p.v_tree, 2, dims, strides, box))
       return cudaErrorInvalidValue;
   }
   cudaError_t e = ensure_max_dynamic_smem<tv_attn_tcp_kernel>((int)SMEM);

@@ -473,16 +473,6 @@ prompt_tc_kernel(const __grid_constant__ PromptParams p, const __grid_constant__
   }
 }
 
-bool encode(CUtensorMap* m, const void* ptr, int rank, const cuuint64_t* dims, const cuuint64_t* strides,
-            const cuuint32_t* box) {
-  EncodeTiledFn fn = encode_tiled_fn();
-  if (!fn) return false;
-  cuuint32_t es[3] = {1, 1, 1};
-  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank, const_cast<void*>(ptr), dims, strides, box, es,
-            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
 }  // namespace
 
 bool prompt_tc_supported(const tv_desc* d, int64_t rows) {
@@ -501,13 +491,13 @@ cudaError_t launch_prompt_tc(const PromptParams& p, int64_t units, cudaStream_t 
     cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)p.Hq, (cuuint64_t)p.rows};
     cuuint64_t strides[2] = {row_bytes, row_bytes * p.Hq};
     cuuint32_t box[3] = {64, (cuuint32_t)p.G, (cuuint32_t)(BM / p.G)};
-    if (!encode(&mq, p.q, 3, dims, strides, box)) return cudaErrorInvalidValue;
+    if (!encode_rows(&mq, p.q, 3, dims, strides, box)) return cudaErrorInvalidValue;
   }
   {
     cuuint64_t dims[2] = {(cuuint64_t)D, (cuuint64_t)p.Hkv * p.rows};
     cuuint64_t strides[1] = {row_bytes};
     cuuint32_t box[2] = {64, BN};
-    if (!encode(&mkr, p.k_rows, 2, dims, strides, box) || !encode(&mvr, p.v_rows, 2, dims, strides, box))
+    if (!encode_rows(&mkr, p.k_rows, 2, dims, strides, box) || !encode_rows(&mvr, p.v_rows, 2, dims, strides, box))
       return cudaErrorInvalidValue;
   }
   mkc = mkr;                                        // no prefix: never read
@@ -518,7 +508,7 @@ cudaError_t launch_prompt_tc(const PromptParams& p, int64_t units, cudaStream_t 
     cuuint64_t dims[2] = {(cuuint64_t)D, rows};
     cuuint64_t strides[1] = {row_bytes};
     cuuint32_t box[2] = {64, (cuuint32_t)(p.paged ? kPageSize : BN)};
-    if (!encode(&mkc, p.k_cache, 2, dims, strides, box) || !encode(&mvc, p.v_cache, 2, dims, strides, box))
+    if (!encode_rows(&mkc, p.k_cache, 2, dims, strides, box) || !encode_rows(&mvc, p.v_cache, 2, dims, strides, box))
       return cudaErrorInvalidValue;
   }
   const cudaError_t e = ensure_max_dynamic_smem<prompt_tc_kernel>((int)SMEM);

@@ -580,16 +580,6 @@ prompt_tc2_kernel(const __grid_constant__ PromptParams p, const __grid_constant_
   }
 }
 
-bool encode(CUtensorMap* m, const void* ptr, int rank, const cuuint64_t* dims, const cuuint64_t* strides,
-            const cuuint32_t* box) {
-  EncodeTiledFn fn = encode_tiled_fn();
-  if (!fn) return false;
-  cuuint32_t es[3] = {1, 1, 1};
-  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank, const_cast<void*>(ptr), dims, strides, box, es,
-            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
 template <int D>
 cudaError_t launch_d(const PromptParams& p, int64_t units, cudaStream_t st) {
   constexpr int DV = Cfg<D>::DV;
@@ -599,13 +589,13 @@ cudaError_t launch_d(const PromptParams& p, int64_t units, cudaStream_t st) {
     cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)p.Hq, (cuuint64_t)p.rows};
     cuuint64_t strides[2] = {row_bytes, row_bytes * p.Hq};
     cuuint32_t box[3] = {64, (cuuint32_t)p.G, (cuuint32_t)(BM / p.G)};
-    if (!encode(&mq, p.q, 3, dims, strides, box)) return cudaErrorInvalidValue;
+    if (!encode_rows(&mq, p.q, 3, dims, strides, box)) return cudaErrorInvalidValue;
   }
   const cuuint64_t strides[1] = {row_bytes};
   {
     cuuint64_t dims[2] = {(cuuint64_t)D, (cuuint64_t)p.Hkv * p.rows};
     cuuint32_t kbox[2] = {64, KH}, vbox[2] = {64, BN};
-    if (!encode(&mkr, p.k_rows, 2, dims, strides, kbox) || !encode(&mvr, p.v_rows, 2, dims, strides, vbox))
+    if (!encode_rows(&mkr, p.k_rows, 2, dims, strides, kbox) || !encode_rows(&mvr, p.v_rows, 2, dims, strides, vbox))
       return cudaErrorInvalidValue;
   }
   mkc = mkr;                                        // no prefix: never read
@@ -615,7 +605,7 @@ cudaError_t launch_d(const PromptParams& p, int64_t units, cudaStream_t st) {
                                                  : (cuuint64_t)p.B * p.Hkv * p.capacity};
     cuuint32_t kbox[2] = {64, (cuuint32_t)(p.paged ? kPageSize : KH)};
     cuuint32_t vbox[2] = {64, (cuuint32_t)(p.paged ? kPageSize : BN)};
-    if (!encode(&mkc, p.k_cache, 2, dims, strides, kbox) || !encode(&mvc, p.v_cache, 2, dims, strides, vbox))
+    if (!encode_rows(&mkc, p.k_cache, 2, dims, strides, kbox) || !encode_rows(&mvc, p.v_cache, 2, dims, strides, vbox))
       return cudaErrorInvalidValue;
   }
   const cudaError_t e = ensure_max_dynamic_smem<prompt_tc2_kernel<D>>((int)Cfg<D>::SMEM);
