@@ -21,7 +21,8 @@
  * (vocab + 7) / 8 * 8 words: bit 15 is set when the token stands in the
  * prompt, bits 0 - 14 hold how often it was emitted (no more than 32767 are
  * counted).  All zeros is a new sequence.  tv_token_counts_add counts a
- * prompt's tokens or a step's emitted ones.
+ * prompt's tokens, the token that the prompt's last row gave (the first tree's
+ * root) and each step's emitted ones.
  *
  * Conventions are those of tree_verify.h.
  */

@@ -46,7 +46,7 @@ int make_prompt_plan(const tv_desc* d, int64_t rows, int64_t max_rows, PromptPla
   // Few units of many keys are split over the keys: so that about every SM has
   // one, in chunks of four tiles or more; kernel 8, whose tiles take longer,
   // into about two waves of chunks of any length (2000 fp32 rows x 4 heads at
-  // head_dim 256: 175, 108, 144 and 129 us with 1, 2, 3 and 4).
+  // head_dim 256: 134, 84, 113 and 101 us with 1, 2, 3 and 4).
   const int64_t sms = num_sms();
   int64_t ctas;
   if (!mul_ok(p->units, d->num_kv_heads, &ctas) || !mul_ok(ctas, p->pub.kernel == 6 ? 1 : d->head_dim / 128, &ctas))

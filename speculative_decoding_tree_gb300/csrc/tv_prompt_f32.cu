@@ -16,8 +16,9 @@
 // the grouping of heads, into blocks of 128 rows x 64 channels x 3 parts that
 // lie in memory as the matrix unit reads them (rows of 128 bytes, 16-byte
 // piece c at c ^ (row & 7)); rows that do not exist are zeros.  (Splitting in
-// the attention kernel itself, for every unit again, took 158 - 208 us where
-// this took 108.)  The second copies those blocks to shared memory,
+// the attention kernel itself, for every unit again, took 158 - 208 us for
+// 2000 rows x 4 heads at head_dim 256 where this took 108, and takes 84 - 89
+// now.)  The second copies those blocks to shared memory,
 // 48 KB each, and multiplies.
 //
 // A unit is 128 query rows (token, group head) of one sequence and KV head and
