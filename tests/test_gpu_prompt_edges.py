@@ -231,3 +231,45 @@ def test_rows_of_minus_infinity_alone_are_zeros(d, hq, hkv, p, n):
     assert int(c.status[0]) == 0 and (c.out[:2] == 0).all()
     # row 2 sees one key besides: its value, weight 1, rounded to bf16 from the product with 1 / 1
     assert torch.equal(c.out[2], c.gpu[2][:, 2].repeat_interleave(hq // hkv, 0))
+
+
+@pytest.mark.parametrize("d", [128, 256, 512])
+def test_wide_groups_of_bf16_heads(d):
+    """More than 128 query heads a KV head: bf16 on the kernel of three parts, paged, behind a prefix, split and not."""
+    for p, n in (([300, 0, 17], [9, 20, 1]), ([0] * 4, [160] * 4)):
+        c = Prompts(p, n, 130, 1, d, "bf16", paged=True, pad=2, seed=15)
+        assert c.plan()["kernel"] == 8
+        c.attn()
+        c.check()
+
+
+@pytest.mark.parametrize("args", [("--kv4", "--steer"), ("--window", "512,4", "--steer"), ("--sampled", "0.7", "--steer"),
+                                  ("--attn-only", "--steer"), ("--prompt", "70")])
+def test_command_forms(args):
+    assert runner.main(["--config", "3", "--steps", "2", *args]) == 0
+
+
+def test_command_steers_before_the_4_bit_step_accepts(monkeypatch):
+    """The argmax that the 4-bit step walks on is that of the logits as steered once."""
+    seen = []
+
+    class Step(runner.DeviceKv4Step):
+        def step(self, argmax, stream=None):
+            seen.append((argmax.clone(), self.logits.clone()))
+            super().step(argmax, stream)
+
+    monkeypatch.setattr(runner, "DeviceKv4Step", Step)
+    assert runner.main(["--config", "3", "--steps", "2", "--kv4", "--steer"]) == 0
+    w = wl.make_workload(wl.CONFIGS[3], canary=0.0, argmax_fn=lambda x: torch.argmax(x.float(), dim=1))
+    st = Step(w)
+    ctl = runner.LogitControl(st, torch.tensor([[1.1, 0.1, 0.1]] * st.desc.batch, device="cuda"))
+    ctl.started()
+    raw = st.logits.clone()
+    for argmax, logits in seen:
+        st.logits.copy_(raw)
+        st.mask()
+        ctl.process()
+        assert torch.equal(logits, st.logits) and not torch.equal(logits, raw)
+        assert torch.equal(argmax, st.logits.float().argmax(1).to(torch.int32))
+        st.accept_commit_argmax(argmax)
+        ctl.emitted()
